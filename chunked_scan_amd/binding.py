@@ -30,7 +30,9 @@ STATUS = {0: "LA_OK", -1: "LA_ERR_NULL", -2: "LA_ERR_SHAPE", -3: "LA_ERR_DTYPE",
 NOALLOC_SCRATCH_BYTES = 32 << 20  # LA_NOALLOC_SCRATCH_BYTES of la_chunk.h
 EXPORTS = ("la_chunk_fwd", "la_chunk_fwd_noalloc", "la_chunk_fwd_decayed", "la_chunk_bwd", "la_chunk_bwd_states", "la_state_scan", "la_state_correct", "la_state_correct_live",
            "la_cumdecay", "la_trim_workspace", "la_chain_status", "la_set_chain_spin_limit", "la_status_str", "la_supported",
-           "la_version")
+           "la_version", "la_short_conv", "la_short_conv_bwd_workspace", "la_short_conv_bwd", "la_short_conv_step",
+           "la_ssm_workspace", "la_ssm_scan", "la_ssm_scan_bwd", "la_ssm_step", "la_add_norm", "la_add_norm_q8",
+           "la_add_norm_bwd_workspace", "la_add_norm_bwd")
 
 
 TRACE_MAX = 16
@@ -51,6 +53,40 @@ class Shape(ctypes.Structure):
         ("total_stride", ctypes.c_int64), ("subseg_chunks", ctypes.c_int32), ("fwd_schedule", ctypes.c_int32),
         ("stream", ctypes.c_void_p),
         ("trace", ctypes.POINTER(Trace)),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """la_rows: element strides of a [B, L, D] view."""
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class ConvShape(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("D", ctypes.c_int64), ("width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("nslots", ctypes.c_int32),
+        ("x", Rows), ("y", Rows), ("dy", Rows), ("dx", Rows),
+        ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
+    ]
+
+
+class SsmShape(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("D", ctypes.c_int64), ("N", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("softplus", ctypes.c_int32), ("nslots", ctypes.c_int32),
+        ("u", Rows), ("dt", Rows), ("b", Rows), ("c", Rows), ("z", Rows), ("y", Rows),
+        ("dy", Rows), ("du", Rows), ("ddt", Rows), ("db", Rows), ("dc", Rows), ("dz", Rows),
+        ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
+    ]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("group", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64), ("dh_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
     ]
 
 
@@ -114,6 +150,24 @@ def lib() -> ctypes.CDLL:
                   L.la_state_correct_live, L.la_cumdecay, L.la_supported, L.la_version, L.la_chain_status,
                   L.la_set_chain_spin_limit):
             f.restype = ctypes.c_int
+        CS, SS, NS, U64 = ctypes.POINTER(ConvShape), ctypes.POINTER(SsmShape), ctypes.POINTER(NormShape), ctypes.c_uint64
+        L.la_short_conv.argtypes = [P] * 7 + [CS]
+        L.la_short_conv_bwd_workspace.argtypes = [CS]
+        L.la_short_conv_bwd.argtypes = [P] * 12 + [U64, CS]
+        L.la_short_conv_step.argtypes = [P] * 6 + [CS]
+        L.la_ssm_workspace.argtypes = [SS, ctypes.c_int32]
+        L.la_ssm_scan.argtypes = [P] * 13 + [U64, SS]
+        L.la_ssm_scan_bwd.argtypes = [P] * 22 + [U64, SS]
+        L.la_ssm_step.argtypes = [P] * 11 + [SS]
+        L.la_add_norm.argtypes = [P] * 6 + [NS]
+        L.la_add_norm_q8.argtypes = [P] * 7 + [NS]
+        L.la_add_norm_bwd_workspace.argtypes = [NS]
+        L.la_add_norm_bwd.argtypes = [P] * 8 + [U64, NS]
+        for f in (L.la_short_conv, L.la_short_conv_bwd, L.la_short_conv_step, L.la_ssm_scan, L.la_ssm_scan_bwd,
+                  L.la_ssm_step, L.la_add_norm, L.la_add_norm_q8, L.la_add_norm_bwd):
+            f.restype = ctypes.c_int
+        for f in (L.la_short_conv_bwd_workspace, L.la_ssm_workspace, L.la_add_norm_bwd_workspace):
+            f.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -451,3 +505,357 @@ def la_set_chain_spin_limit(limit: int) -> int:
     """Polls per flag before a chained wave gives up, for later launches; returns the previous value
     (a negative limit only reads it)."""
     return lib().la_set_chain_spin_limit(limit)
+
+
+# ------------------------------------------------------------------------------------------------
+# Selective state space layer: short convolution, selective scan, residual norm.  Activations may be
+# strided views whose last dim is contiguous; every tensor of a call lives on one device.  Work is
+# enqueued on ``stream`` (default: the device's current stream), and what a call allocates (outputs not
+# given, workspace) is allocated for that stream.
+
+
+class _On:
+    """The device and stream of a call: makes both current while the call allocates and enqueues."""
+
+    def __init__(self, t: torch.Tensor, name: str, stream):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        self.device = t.device
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
+        self.stream = stream
+
+    def __enter__(self):
+        self._dev = torch.cuda.device(self.device)
+        self._dev.__enter__()
+        self._st = torch.cuda.stream(self.stream)  # no-op for None
+        self._st.__enter__()
+        self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        self._st.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+    def check(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
+        """``t`` (or None) with that type and shape on the call's device; dense, or any strides with a
+        contiguous last dim."""
+        if t is None:
+            return None
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, not {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if dense and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if not dense and t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the last dim must be contiguous")
+        return t
+
+    def out(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
+        if t is None:
+            return torch.empty(tuple(shape), dtype=dtype, device=self.device)
+        return self.check(t, name, dtype, shape, dense)
+
+    def workspace(self, fn: str, nbytes: int) -> torch.Tensor:
+        if nbytes < 0:
+            _check(fn, nbytes)
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+
+def _rows(t: Optional[torch.Tensor]) -> Rows:
+    """The batch and token strides of a [B, L, D] tensor (or [B, D]: the batch stride)."""
+    if t is None or t.numel() == 0 or t.is_contiguous():
+        return Rows(0, 0)
+    if t.dim() == 2:
+        # {0, 0} would mean dense: one repeated row is told apart by its unused token stride
+        return Rows(t.stride(0), t.shape[1])
+    b, s = t.stride(0), t.stride(1)
+    if b == 0 and s == 0:
+        raise ValueError("a view that repeats one row over batch and tokens is not supported: make it contiguous")
+    return Rows(b, s)
+
+
+def _dims(t: torch.Tensor, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dims, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _finish(shape, on: _On, timer):
+    shape.stream = on.handle
+    if timer is not None:
+        shape.trace = ctypes.pointer(timer.trace)
+    return shape
+
+
+def _conv_common(on, x, weight, bias, D, W, dtype):
+    on.check(weight, "weight", torch.float32, (D, W))
+    on.check(bias, "bias", torch.float32, (D,))
+    on.check(x, "x", dtype, x.shape, dense=False)
+
+
+def la_short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                  state_in: Optional[torch.Tensor] = None, *, lengths: Optional[torch.Tensor] = None,
+                  silu: bool = True, y: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                  want_state: bool = False, stream=None, timer=None):
+    """Depthwise causal convolution over tokens with an optional SiLU.  x [B,L,D] (f32 or bf16, strided
+    rows allowed), weight f32 [D,W] (W = 2, 3 or 4; the last tap meets the current token), bias f32 [D]
+    or None, state_in [B,W-1,D] (x's dtype, the inputs before the first token, oldest first) or None,
+    lengths int32 [B] or None.  Returns (y [B,L,D], state_out [B,W-1,D] or None); rows of y behind a
+    sequence's length are left as they were."""
+    B, L, D = _dims(x, "x", 3)
+    W = _dims(weight, "weight", 2)[1]
+    dt = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        _conv_common(on, x, weight, bias, D, W, x.dtype)
+        on.check(state_in, "state_in", x.dtype, (B, W - 1, D))
+        on.check(lengths, "lengths", torch.int32, (B,))
+        y = on.out(y, "y", x.dtype, (B, L, D), dense=False)
+        if state_out is not None or want_state:
+            state_out = on.out(state_out, "state_out", x.dtype, (B, W - 1, D))
+        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0, x=_rows(x), y=_rows(y)), on, timer)
+        _check("la_short_conv", lib().la_short_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(lengths),
+                                                    _ptr(y), _ptr(state_out), ctypes.byref(shp)))
+    return y, state_out
+
+
+def la_short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      state_in: Optional[torch.Tensor] = None, d_state_out: Optional[torch.Tensor] = None, *,
+                      lengths: Optional[torch.Tensor] = None, silu: bool = True, dx: Optional[torch.Tensor] = None,
+                      stream=None, timer=None):
+    """Backward of la_short_conv.  Returns (dx [B,L,D], d_weight f32 [D,W], d_bias f32 [D] or None without
+    a bias, d_state_in [B,W-1,D] or None without a state_in); dx is zero behind a sequence's length."""
+    B, L, D = _dims(x, "x", 3)
+    W = _dims(weight, "weight", 2)[1]
+    dt = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        _conv_common(on, x, weight, bias, D, W, x.dtype)
+        on.check(dy, "dy", x.dtype, (B, L, D), dense=False)
+        on.check(state_in, "state_in", x.dtype, (B, W - 1, D))
+        on.check(d_state_out, "d_state_out", x.dtype, (B, W - 1, D))
+        on.check(lengths, "lengths", torch.int32, (B,))
+        dx = on.out(dx, "dx", x.dtype, (B, L, D), dense=False)
+        dw = on.out(None, "d_weight", torch.float32, (D, W))
+        db = on.out(None, "d_bias", torch.float32, (D,)) if bias is not None else None
+        ds = on.out(None, "d_state_in", x.dtype, (B, W - 1, D)) if state_in is not None else None
+        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0, x=_rows(x), dy=_rows(dy), dx=_rows(dx)), on, timer)
+        n = lib().la_short_conv_bwd_workspace(ctypes.byref(shp))
+        ws = on.workspace("la_short_conv_bwd_workspace", n)
+        _check("la_short_conv_bwd", lib().la_short_conv_bwd(
+            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(lengths), _ptr(dy), _ptr(d_state_out), _ptr(dx),
+            _ptr(dw), _ptr(db), _ptr(ds), _ptr(ws), n, ctypes.byref(shp)))
+    return dx, dw, db, ds
+
+
+def la_short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, *, slots: Optional[torch.Tensor] = None,
+                       silu: bool = True, y: Optional[torch.Tensor] = None, stream=None, timer=None) -> torch.Tensor:
+    """One token of each of B sequences.  x [B,D]; state [S,W-1,D] (x's dtype), updated in place; slots
+    int32 [B] names each row's state (None: row b uses state b).  Rows whose slot is not in 0..S-1, and
+    rows after the first that names a slot, are padding: their y is left as it was.  Returns y [B,D]."""
+    B, D = _dims(x, "x", 2)
+    W = _dims(weight, "weight", 2)[1]
+    S = _dims(state, "state", 3)[0]
+    dt = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        _conv_common(on, x, weight, bias, D, W, x.dtype)
+        on.check(state, "state", x.dtype, (S, W - 1, D))
+        on.check(slots, "slots", torch.int32, (B,))
+        y = on.out(y, "y", x.dtype, (B, D), dense=False)
+        shp = _finish(ConvShape(B, 1, D, W, dt, int(silu), S, x=_rows(x), y=_rows(y)), on, timer)
+        _check("la_short_conv_step", lib().la_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots),
+                                                              _ptr(y), ctypes.byref(shp)))
+    return y
+
+
+def _ssm_common(on, u, dt, A, B_, C, D, z, dt_bias, rows, Dn, N):
+    e = u.dtype
+    on.check(u, "u", e, rows + (Dn,), dense=False)
+    on.check(dt, "dt", e, rows + (Dn,), dense=False)
+    on.check(A, "A", torch.float32, (Dn, N))
+    on.check(B_, "B", e, rows + (N,), dense=False)
+    on.check(C, "C", e, rows + (N,), dense=False)
+    on.check(D, "D", torch.float32, (Dn,))
+    on.check(z, "z", e, rows + (Dn,), dense=False)
+    on.check(dt_bias, "dt_bias", torch.float32, (Dn,))
+
+
+def la_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *,
+                D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                dt_bias: Optional[torch.Tensor] = None, s_in: Optional[torch.Tensor] = None,
+                lengths: Optional[torch.Tensor] = None, softplus: bool = True, y: Optional[torch.Tensor] = None,
+                s_out: Optional[torch.Tensor] = None, want_state: bool = True, stream=None, timer=None):
+    """Selective scan: S_t = exp(delta_t A) S_{t-1} + B_t (delta_t u_t), y_t = (C_t S_t + D u_t) silu(z_t), with
+    delta = softplus(dt + dt_bias) (or dt + dt_bias).  u, dt, z [B,L,D] and B, C [B,L,N] (f32 or bf16,
+    strided rows allowed), A f32 [D,N], D and dt_bias f32 [D], s_in f32 [B,N,D], lengths int32 [B].
+    Returns (y [B,L,D], s_out f32 [B,N,D] or None); s_out may be s_in.  Rows of y behind a sequence's
+    length are left as they were."""
+    Bn, L, Dn = _dims(u, "u", 3)
+    N = _dims(A, "A", 2)[1]
+    code = _dtype_code(u)
+    with _On(u, "u", stream) as on:
+        _ssm_common(on, u, dt, A, B, C, D, z, dt_bias, (Bn, L), Dn, N)
+        on.check(s_in, "s_in", torch.float32, (Bn, N, Dn))
+        on.check(lengths, "lengths", torch.int32, (Bn,))
+        y = on.out(y, "y", u.dtype, (Bn, L, Dn), dense=False)
+        if s_out is not None or want_state:
+            s_out = on.out(s_out, "s_out", torch.float32, (Bn, N, Dn))
+        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
+                               z=_rows(z), y=_rows(y)), on, timer)
+        n = lib().la_ssm_workspace(ctypes.byref(shp), 0)
+        ws = on.workspace("la_ssm_workspace", n)
+        _check("la_ssm_scan", lib().la_ssm_scan(_ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                                _ptr(dt_bias), _ptr(s_in), _ptr(lengths), _ptr(y), _ptr(s_out),
+                                                _ptr(ws), n, ctypes.byref(shp)))
+    return y, s_out
+
+
+def la_ssm_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                    dy: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                    dt_bias: Optional[torch.Tensor] = None, s_in: Optional[torch.Tensor] = None,
+                    ds_out: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                    softplus: bool = True, du: Optional[torch.Tensor] = None, ddt: Optional[torch.Tensor] = None,
+                    dz: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
+                    dC: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """Backward of la_ssm_scan from dy [B,L,D] and ds_out f32 [B,N,D] (None: zero).  Returns (du, ddt, dA, dB,
+    dC, dD, dz, d_dt_bias, ds_in); those of arguments that are None are None.  du, ddt, dz, dB and dC may
+    be given as strided views (slices of a projection's gradient); they are zero behind a sequence's length."""
+    Bn, L, Dn = _dims(u, "u", 3)
+    N = _dims(A, "A", 2)[1]
+    code = _dtype_code(u)
+    f32 = torch.float32
+    with _On(u, "u", stream) as on:
+        _ssm_common(on, u, dt, A, B, C, D, z, dt_bias, (Bn, L), Dn, N)
+        on.check(dy, "dy", u.dtype, (Bn, L, Dn), dense=False)
+        on.check(s_in, "s_in", f32, (Bn, N, Dn))
+        on.check(ds_out, "ds_out", f32, (Bn, N, Dn))
+        on.check(lengths, "lengths", torch.int32, (Bn,))
+        if z is None and dz is not None:
+            raise ValueError("dz without z")
+        du = on.out(du, "du", u.dtype, (Bn, L, Dn), dense=False)
+        ddt = on.out(ddt, "ddt", u.dtype, (Bn, L, Dn), dense=False)
+        dz = on.out(dz, "dz", u.dtype, (Bn, L, Dn), dense=False) if z is not None else None
+        dB = on.out(dB, "dB", u.dtype, (Bn, L, N), dense=False)
+        dC = on.out(dC, "dC", u.dtype, (Bn, L, N), dense=False)
+        dA = on.out(None, "dA", f32, (Dn, N))
+        dD = on.out(None, "dD", f32, (Dn,)) if D is not None else None
+        dbias = on.out(None, "d_dt_bias", f32, (Dn,)) if dt_bias is not None else None
+        ds_in = on.out(None, "ds_in", f32, (Bn, N, Dn)) if s_in is not None else None
+        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
+                               z=_rows(z), dy=_rows(dy), du=_rows(du), ddt=_rows(ddt), db=_rows(dB), dc=_rows(dC),
+                               dz=_rows(dz)), on, timer)
+        n = lib().la_ssm_workspace(ctypes.byref(shp), 1)
+        ws = on.workspace("la_ssm_workspace", n)
+        _check("la_ssm_scan_bwd", lib().la_ssm_scan_bwd(
+            _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(s_in), _ptr(lengths),
+            _ptr(dy), _ptr(ds_out), _ptr(du), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz), _ptr(dbias),
+            _ptr(ds_in), _ptr(ws), n, ctypes.byref(shp)))
+    return du, ddt, dA, dB, dC, dD, dz, dbias, ds_in
+
+
+def la_ssm_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                state: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                dt_bias: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, softplus: bool = True,
+                y: Optional[torch.Tensor] = None, stream=None, timer=None) -> torch.Tensor:
+    """One token of each of B sequences of la_ssm_scan.  u, dt, z [B,D], B, C [B,N]; state f32 [S,N,D],
+    updated in place; slots as in la_short_conv_step.  Returns y [B,D]."""
+    Bn, Dn = _dims(u, "u", 2)
+    N = _dims(A, "A", 2)[1]
+    S = _dims(state, "state", 3)[0]
+    code = _dtype_code(u)
+    with _On(u, "u", stream) as on:
+        _ssm_common(on, u, dt, A, B, C, D, z, dt_bias, (Bn,), Dn, N)
+        on.check(state, "state", torch.float32, (S, N, Dn))
+        on.check(slots, "slots", torch.int32, (Bn,))
+        y = on.out(y, "y", u.dtype, (Bn, Dn), dense=False)
+        shp = _finish(SsmShape(Bn, 1, Dn, N, code, int(softplus), S, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
+                               z=_rows(z), y=_rows(y)), on, timer)
+        _check("la_ssm_step", lib().la_ssm_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                                _ptr(dt_bias), _ptr(state), _ptr(slots), _ptr(y), ctypes.byref(shp)))
+    return y
+
+
+def _row_stride(t: Optional[torch.Tensor], name: str) -> int:
+    if t is None or t.numel() == 0 or t.is_contiguous() or t.shape[0] == 1:
+        return 0
+    if t.stride(0) == 0:
+        raise ValueError(f"{name}: a view that repeats one row is not supported")
+    return t.stride(0)
+
+
+def _norm_args(on, x, residual, weight, h, M, D):
+    on.check(x, "x", x.dtype, (M, D), dense=False)
+    on.check(residual, "residual", x.dtype, (M, D), dense=False)
+    on.check(weight, "weight", torch.float32, (D,))
+
+
+def la_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, row by row.  x, residual [M,D] (f32 or bf16,
+    strided rows allowed), weight f32 [D].  Returns (y [M,D], h [M,D], rstd f32 [M]); without a residual
+    and without an h given, h is x itself.  h may be given as residual or x (updated in place)."""
+    M, D = _dims(x, "x", 2)
+    code = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        _norm_args(on, x, residual, weight, h, M, D)
+        want = residual is not None or h is not None
+        h = on.out(h, "h", x.dtype, (M, D), dense=False) if want else None
+        y = on.out(y, "y", x.dtype, (M, D), dense=False)
+        rstd = on.out(None, "rstd", torch.float32, (M,))
+        shp = _finish(NormShape(M, D, code, 0, eps, x_stride=_row_stride(x, "x"),
+                                residual_stride=_row_stride(residual, "residual"), y_stride=_row_stride(y, "y"),
+                                h_stride=_row_stride(h, "h")), on, timer)
+        _check("la_add_norm", lib().la_add_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(h), _ptr(rstd),
+                                                ctypes.byref(shp)))
+    return y, (h if want else x), rstd
+
+
+def la_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                   eps: float = 1e-5, group: int = 0, q: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """la_add_norm with y in 8 bits: returns (q float8_e4m3fn [M,D], scale f32 [M, D / group] (group 0: [M,1]),
+    h, rstd) with y ~ q * scale of its row (group 0) or of its 32, 64 or 128 adjacent elements."""
+    M, D = _dims(x, "x", 2)
+    code = _dtype_code(x)
+    if group not in (0, 32, 64, 128) or (group and D % group):
+        raise ValueError(f"group must be 0, 32, 64 or 128 and divide D = {D}, not {group}")
+    with _On(x, "x", stream) as on:
+        _norm_args(on, x, residual, weight, h, M, D)
+        want = residual is not None or h is not None
+        h = on.out(h, "h", x.dtype, (M, D), dense=False) if want else None
+        q = on.out(q, "q", torch.float8_e4m3fn, (M, D))
+        scale = on.out(scale, "scale", torch.float32, (M, D // group if group else 1))
+        rstd = on.out(None, "rstd", torch.float32, (M,))
+        shp = _finish(NormShape(M, D, code, group, eps, x_stride=_row_stride(x, "x"),
+                                residual_stride=_row_stride(residual, "residual"), h_stride=_row_stride(h, "h")), on,
+                      timer)
+        _check("la_add_norm_q8", lib().la_add_norm_q8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(q), _ptr(scale), _ptr(h),
+                                                      _ptr(rstd), ctypes.byref(shp)))
+    return q, scale, (h if want else x), rstd
+
+
+def la_add_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                    dh: Optional[torch.Tensor] = None, *, dx: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """Backward of la_add_norm from dy [M,D], the forward's h and rstd, and dh [M,D] (the derivative that
+    reaches h along the residual stream; None: zero).  Returns (dx [M,D], d_weight f32 [D]); dx is the
+    derivative of x and of the residual alike and may be given as dh or dy."""
+    M, D = _dims(dy, "dy", 2)
+    code = _dtype_code(dy)
+    with _On(dy, "dy", stream) as on:
+        on.check(dy, "dy", dy.dtype, (M, D), dense=False)
+        on.check(h, "h", dy.dtype, (M, D), dense=False)
+        on.check(dh, "dh", dy.dtype, (M, D), dense=False)
+        on.check(weight, "weight", torch.float32, (D,))
+        on.check(rstd, "rstd", torch.float32, (M,))
+        dx = on.out(dx, "dx", dy.dtype, (M, D), dense=False)
+        dw = on.out(None, "d_weight", torch.float32, (D,))
+        shp = _finish(NormShape(M, D, code, 0, 1.0, h_stride=_row_stride(h, "h"), dy_stride=_row_stride(dy, "dy"),
+                                dh_stride=_row_stride(dh, "dh"), dx_stride=_row_stride(dx, "dx")), on, timer)
+        n = lib().la_add_norm_bwd_workspace(ctypes.byref(shp))
+        ws = on.workspace("la_add_norm_bwd_workspace", n)
+        _check("la_add_norm_bwd", lib().la_add_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx),
+                                                        _ptr(dw), _ptr(ws), n, ctypes.byref(shp)))
+    return dx, dw

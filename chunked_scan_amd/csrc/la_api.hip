@@ -170,7 +170,7 @@ la::Tracer make_tracer(const la_shape* s) {
 
 extern "C" {
 
-int32_t la_version(void) { return (1 << 16) | 2; }
+int32_t la_version(void) { return (1 << 16) | 3; }
 
 la_status la_trim_workspace(void) { return from_hip(la::workspace_trim()); }
 

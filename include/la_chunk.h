@@ -59,7 +59,8 @@ typedef enum la_status {
     LA_ERR_UNSUPPORTED = -5, /* valid request that the library has no kernel for (e.g. dk > 128) */
     LA_ERR_LAUNCH = -6,      /* the HIP runtime refused a launch or a workspace allocation */
     LA_ERR_DECAY = -7,       /* unknown decay mode, or gate_norm <= 0 in gate mode */
-    LA_ERR_WORKSPACE = -8,   /* la_chunk_fwd_noalloc: the call needs more than LA_NOALLOC_SCRATCH_BYTES */
+    LA_ERR_WORKSPACE = -8,   /* la_chunk_fwd_noalloc: the call needs more than LA_NOALLOC_SCRATCH_BYTES; calls
+                                that take a workspace: it is NULL, unaligned or too small */
     LA_ERR_TIMEOUT = -9      /* la_chain_status: a chained forward's bounded wait gave up */
 } la_status;
 
@@ -355,6 +356,209 @@ la_status la_state_correct_live(const void* q, const float* cumdecay, const floa
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DECAY, LA_ERR_ALIAS or LA_ERR_LAUNCH.
  */
 la_status la_cumdecay(const float* decay, float* cumdecay, float* total, const la_shape* shape);
+
+/* ------------------------------------------------------------------------------------------------
+ * Selective state space layer: the short causal convolution, the selective scan and the residual
+ * root-mean-square norm of a layer whose state recurrence has the form above but whose decay is
+ * made from an input-dependent step size and differs per key AND value dim:
+ *        S_t[n,d] = exp(delta_t[d] A[n,d]) S_{t-1}[n,d] + B_t[n] (delta_t[d] u_t[d]),
+ *        y_t[d]   = sum_n C_t[n] S_t[n,d],
+ * i.e. keys B, queries C, values delta u, and a state S in R^{N x D} per sequence.
+ *
+ * Layouts.  Activations are [B, L, D] with the channels contiguous and any batch and token strides
+ * (la_rows, in elements); the scan's B and C are [B, L, N] likewise; parameters are dense float32;
+ * states are dense.  Strides may be any non-negative values of an input (rows may repeat); rows of
+ * an output must not overlap.  No alignment beyond the element's is needed (16-byte aligned rows
+ * run fastest).  Two views that interleave in one buffer (the two halves of a projection's output)
+ * count as separate when their row strides agree and their columns do not meet.
+ *
+ * Padded batches.  `lengths` (int32[B] on the device, or NULL: all L) cuts sequence b to its first
+ * lengths[b] tokens (values outside 0..L are taken as the nearer bound): outputs behind them are
+ * left as they were, the returned state is the one after the last token (with no tokens: the
+ * incoming one), and a backward pass writes zeros to the gradients behind them.
+ *
+ * Memory.  These calls allocate nothing.  Those that need scratch memory take a workspace (device,
+ * 16-byte aligned, contents undefined before and after, at least the bytes that the matching
+ * _workspace call returns for the same shape), so calls that may overlap in time need separate
+ * ones.  Calls may be captured into graphs; a graph keeps using the workspace it was captured with.
+ *
+ * Limits.  B <= 2^20, B * L <= 2^24 tokens, B * D <= 2^25, B * L * D <= 2^36 elements; the norm M <= 2^25
+ * rows and M * D <= 2^34; beyond them LA_ERR_UNSUPPORTED.  A view's strides may span 2^42 elements
+ * in all; beyond it LA_ERR_SHAPE.
+ *
+ * Numerics.  Sums, states and statistics are held in fp32 whatever the activations' type; outputs
+ * are rounded once, to nearest even.  No atomics: results do not depend on scheduling.
+ * ---------------------------------------------------------------------------------------------- */
+
+/* Element strides of a [B, L, D] view; {0, 0} means dense. */
+typedef struct la_rows {
+    int64_t batch;
+    int64_t token;
+} la_rows;
+
+typedef struct la_conv_shape {
+    int64_t B;      /* sequences, >= 0 */
+    int64_t L;      /* tokens per sequence, >= 0 (la_short_conv_step: not used) */
+    int64_t D;      /* channels, >= 0 */
+    int32_t width;  /* taps W: 2, 3 or 4 */
+    int32_t dtype;  /* la_dtype of x, y, the states and their gradients */
+    int32_t silu;   /* 1: y = v / (1 + exp(-v)) of the convolution's value v; 0: y = v */
+    int32_t nslots; /* la_short_conv_step: states in the pool, >= 0 */
+    la_rows x, y, dy, dx; /* la_short_conv_step: the batch strides of x and y alone */
+    void* stream;
+    la_trace* trace;
+} la_conv_shape;
+
+/*
+ * Depthwise causal convolution of W taps with a bias and an optional SiLU:
+ *        y_t[d] = act(bias[d] + sum_j weight[d, j] x_{t-W+1+j}[d]),     j = 0..W-1,
+ * where x_{-1} .. x_{-(W-1)} come from state_in.
+ *   x         : [B,L,D] dtype                      weight : float[D,W], the last tap meets x_t
+ *   bias      : float[D] or NULL (zero)            lengths: int32[B] or NULL
+ *   state_in  : [B,W-1,D] dtype, the inputs before the first token, oldest first; NULL: zeros
+ *   y         : [B,L,D] dtype, written             state_out: [B,W-1,D] dtype or NULL, the last
+ *               W-1 inputs (of state_in and x together): the state_in of the tokens that follow.
+ * No output may overlap another argument.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
+ */
+la_status la_short_conv(const void* x, const float* weight, const float* bias, const void* state_in,
+                        const int32_t* lengths, void* y, void* state_out, const la_conv_shape* shape);
+
+/* Bytes of workspace of la_short_conv_bwd (0 is possible), or a negative la_status. */
+int64_t la_short_conv_bwd_workspace(const la_conv_shape* shape);
+
+/*
+ * Backward of la_short_conv from dy [B,L,D] and d_state_out [B,W-1,D] (NULL: zero).  Writes
+ * dx [B,L,D] dtype, d_weight float[D,W], d_bias float[D] or NULL, d_state_in [B,W-1,D] dtype or
+ * NULL.  Outputs of the forward are not needed.  No output may overlap another argument.
+ * Returns the codes of la_short_conv, or LA_ERR_WORKSPACE.
+ */
+la_status la_short_conv_bwd(const void* x, const float* weight, const float* bias, const void* state_in,
+                            const int32_t* lengths, const void* dy, const void* d_state_out, void* dx,
+                            float* d_weight, float* d_bias, void* d_state_in, void* workspace,
+                            uint64_t workspace_bytes, const la_conv_shape* shape);
+
+/*
+ * One token of each of B sequences: x and y [B,D]; state [nslots,W-1,D] dtype is a pool that
+ * is updated in place.  slots (int32[B], or NULL: row b uses slot b and nslots must be >= B) names
+ * each row's state.  A row whose slot is outside 0..nslots-1 is padding: its y is left as it was.
+ * Of rows that name the same slot the first one counts and the others are padding.
+ * Returns the codes of la_short_conv.
+ */
+la_status la_short_conv_step(const void* x, const float* weight, const float* bias, void* state,
+                             const int32_t* slots, void* y, const la_conv_shape* shape);
+
+typedef struct la_ssm_shape {
+    int64_t B;         /* sequences, >= 0 */
+    int64_t L;         /* tokens per sequence, >= 0 (la_ssm_step: not used) */
+    int64_t D;         /* channels (value dims), >= 0 */
+    int32_t N;         /* state size (key dims), 1..64 */
+    int32_t dtype;     /* la_dtype of u, dt, B, C, z, y and their gradients */
+    int32_t softplus;  /* 1: delta = log(1 + exp(dt + dt_bias)); 0: delta = dt + dt_bias */
+    int32_t nslots;    /* la_ssm_step: states in the pool, >= 0 */
+    la_rows u, dt, b, c, z, y;       /* la_ssm_step: the batch strides alone */
+    la_rows dy, du, ddt, db, dc, dz; /* la_ssm_scan_bwd */
+    void* stream;
+    la_trace* trace;
+} la_ssm_shape;
+
+/* Bytes of workspace of la_ssm_scan (backward = 0) or la_ssm_scan_bwd (backward = 1), or a
+ * negative la_status. */
+int64_t la_ssm_workspace(const la_ssm_shape* shape, int32_t backward);
+
+/*
+ * Selective scan over every sequence:
+ *        delta_t = dt_t + dt_bias, through softplus if shape->softplus
+ *        S_t[n,d] = exp(delta_t[d] A[d,n]) S_{t-1}[n,d] + delta_t[d] u_t[d] B_t[n]
+ *        y_t[d]   = (sum_n C_t[n] S_t[n,d] + Dskip[d] u_t[d]) z_t[d] / (1 + exp(-z_t[d]))
+ *   u, dt : [B,L,D] dtype         A : float[D,N] (negative for a decay; not checked)
+ *   Bm, Cm: [B,L,N] dtype         Dskip, dt_bias : float[D] or NULL (zero)
+ *   z     : [B,L,D] dtype or NULL (no gate)        s_in : float[B,N,D] initial state or NULL (zero)
+ *   y     : [B,L,D] dtype, written                  s_out: float[B,N,D] final state or NULL; may be
+ *           the same pointer as s_in.
+ * No output may otherwise overlap another argument.  A channel with a non-finite input gives
+ * non-finite values from that token on.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED,
+ * LA_ERR_WORKSPACE or LA_ERR_LAUNCH.
+ */
+la_status la_ssm_scan(const void* u, const void* dt, const float* A, const void* Bm, const void* Cm,
+                      const float* Dskip, const void* z, const float* dt_bias, const float* s_in,
+                      const int32_t* lengths, void* y, float* s_out, void* workspace,
+                      uint64_t workspace_bytes, const la_ssm_shape* shape);
+
+/*
+ * Backward of la_ssm_scan from dy [B,L,D] and ds_out float[B,N,D] (NULL: zero).  Writes du, ddt
+ * [B,L,D] dtype, dA float[D,N], dB, dC [B,L,N] dtype, dD float[D] or NULL, dz [B,L,D] dtype
+ * (exactly when z is given), d_dt_bias float[D] or NULL, ds_in float[B,N,D] or NULL.  States are
+ * recomputed from the forward's inputs.  No output may overlap another argument.
+ * Returns the codes of la_ssm_scan.
+ */
+la_status la_ssm_scan_bwd(const void* u, const void* dt, const float* A, const void* Bm, const void* Cm,
+                          const float* Dskip, const void* z, const float* dt_bias, const float* s_in,
+                          const int32_t* lengths, const void* dy, const float* ds_out, void* du, void* ddt,
+                          float* dA, void* dB, void* dC, float* dD, void* dz, float* d_dt_bias,
+                          float* ds_in, void* workspace, uint64_t workspace_bytes,
+                          const la_ssm_shape* shape);
+
+/*
+ * One token of each of B sequences: u, dt, z, y [B,D], Bm, Cm [B,N]; state float[nslots,N,D] is
+ * a pool that is updated in place; slots as in la_short_conv_step.
+ * Returns the codes of la_ssm_scan but LA_ERR_WORKSPACE.
+ */
+la_status la_ssm_step(const void* u, const void* dt, const float* A, const void* Bm, const void* Cm,
+                      const float* Dskip, const void* z, const float* dt_bias, float* state,
+                      const int32_t* slots, void* y, const la_ssm_shape* shape);
+
+typedef struct la_norm_shape {
+    int64_t M;      /* rows, >= 0 */
+    int64_t D;      /* row length, 1..16384 */
+    int32_t dtype;  /* la_dtype of x, residual, y, h, dy, dh, dx */
+    int32_t group;  /* la_add_norm_q8: elements per scale: 0 (the whole row), 32, 64 or 128 (D a multiple) */
+    float eps;      /* > 0, finite */
+    int32_t reserved;  /* 0 */
+    int64_t x_stride, residual_stride, y_stride, h_stride; /* elements between rows; 0 = D.  The  */
+    int64_t dy_stride, dh_stride, dx_stride;               /* 8-bit output is dense               */
+    void* stream;
+    la_trace* trace;
+} la_norm_shape;
+
+/*
+ * Residual addition and root-mean-square norm:
+ *        h = x + residual,   r = 1 / sqrt(mean_d h[d]^2 + eps),   y[d] = h[d] r weight[d].
+ *   x, residual : [M,D] dtype; residual NULL: h = x       weight : float[D]
+ *   y           : [M,D] dtype, written
+ *   h           : [M,D] dtype or NULL, the sum, rounded (the norm takes the unrounded sum); may be
+ *                 the same pointer, with the same stride, as residual or x
+ *   rstd        : float[M] or NULL, r of every row.
+ * No output may otherwise overlap another argument.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
+ */
+la_status la_add_norm(const void* x, const void* residual, const float* weight, void* y, void* h,
+                      float* rstd, const la_norm_shape* shape);
+
+/*
+ * la_add_norm whose y is held in 8 bits: q uint8[M,D] dense, OCP e4m3 codes, and scale
+ * float[M, D / group] (group 0: float[M]), with y ~ value(q) * scale, scale = (largest |y| of the
+ * group) / 448, or 1 where that is zero; y / scale is rounded to the nearest e4m3 value, ties to even.
+ * A group that holds a NaN or an infinity has a non-finite scale.  Other arguments and the return
+ * codes as for la_add_norm.
+ */
+la_status la_add_norm_q8(const void* x, const void* residual, const float* weight, void* q, float* scale,
+                         void* h, float* rstd, const la_norm_shape* shape);
+
+/* Bytes of workspace of la_add_norm_bwd, or a negative la_status. */
+int64_t la_add_norm_bwd_workspace(const la_norm_shape* shape);
+
+/*
+ * Backward of la_add_norm from dy [M,D], the forward's h and rstd, and dh [M,D] (the derivative
+ * with respect to h itself from the residual stream; NULL: zero).  With xh = h r:
+ *        dx = dresidual = r (dy weight - xh mean_d(dy weight xh)) + dh,     d_weight = sum_rows dy xh.
+ * Writes dx [M,D] dtype (may be the same pointer, with the same stride, as dh or dy) and d_weight
+ * float[D].  Returns the codes of la_add_norm, or LA_ERR_WORKSPACE.
+ */
+la_status la_add_norm_bwd(const void* dy, const void* h, const float* weight, const float* rstd,
+                          const void* dh, void* dx, float* d_weight, void* workspace,
+                          uint64_t workspace_bytes, const la_norm_shape* shape);
 
 /* Releases the current device's workspace: when the device holds buffers kept between calls, it
  * waits for the device to be idle and frees them; then it returns the pool's memory that no
