@@ -132,6 +132,9 @@ struct WsCut {
 typedef const __attribute__((address_space(4))) float* scalar_f32;
 __device__ __forceinline__ scalar_f32 as_scalar(const float* p) { return (scalar_f32)(uintptr_t)p; }
 
+// A value that is the same in all lanes, moved to a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // 1 / (1 + e^-x): the hardware's base-2 exponential and reciprocal, about 1 ulp each.  For x far

@@ -19,20 +19,19 @@
 // pass costs (G - 1) / G of one more recurrence without the output sum.
 #include "la_mixer.h"
 #include "ssm_common.h"
+#include "ssm_tile.h"
 
 namespace la {
 namespace {
-
-constexpr int TB = 8;  // tokens per block of loads
 
 struct FwdDev {
     const void* u;
     const void* dt;
     const void* z;
-    const float* A;
     const float* Dskip;
     const float* dt_bias;
     const float* bc;     // [B, L, 2 NP]
+    const float* a2;     // [NP, D] rates times log2(e)
     const float* hin;    // [B, G, N, D] states entering the segments; null: zero (G = 1)
     const int32_t* lengths;
     void* y;
@@ -46,10 +45,19 @@ struct FwdDev {
     la_rows su, sdt, sz, sy;
 };
 
+// The first launch: B and C as fp32 [B, L, 2 NP] and A log2(e) as [NP, D] (channels contiguous, so that a
+// wave's loads of its rates coalesce), zeros behind N.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_bc_kernel(const T* __restrict__ Bm, const T* __restrict__ Cm, la_rows sb,
-                                                      la_rows sc, float* __restrict__ bc, int64_t rows, int64_t L, int N,
-                                                      int NP) {
+__global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ Bm, const T* __restrict__ Cm,
+                                                   const float* __restrict__ A, la_rows sb, la_rows sc,
+                                                   float* __restrict__ bc, float* __restrict__ a2, int64_t rows, int64_t L,
+                                                   int64_t D, int N, int NP, unsigned nbc) {
+    if (blockIdx.x >= nbc) {
+        const int64_t i = (int64_t)(blockIdx.x - nbc) * 256 + threadIdx.x;
+        const int64_t n = i / D, d = i % D;
+        if (n < NP) a2[i] = n < N ? A[d * N + n] * LOG2E : 0.f;
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t r = i / (2 * NP);
     if (r >= rows) return;
@@ -64,79 +72,105 @@ __global__ __launch_bounds__(256) void pack_bc_kernel(const T* __restrict__ Bm, 
     bc[i] = v;
 }
 
-template <typename T, int NP, bool STATE>
+// STATE: the first pass (a segment's end state from zero and its sum of delta), else the second.  VEC: rows are
+// 16-byte aligned and whole 8-channel chunks.  Tokens of a tile behind the segment's end repeat its last row
+// with delta = 0 (decay 1, input 0): they leave the state alone and are not stored.
+template <typename E, int NP, bool STATE, bool VEC>
 __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
+    constexpr int NS = STATE ? 2 : 3;
+    __shared__ __align__(16) E tile[STATE ? 2 : 4][TT * 64];  // u, dt, z, y
     // blocks: channel block fastest, then segment, then sequence
     const unsigned r = blockIdx.x / p.cb;
     const int g = (int)(r % p.ng);
     const int64_t b = r / p.ng;
     const int64_t d0 = (int64_t)(blockIdx.x % p.cb) * 64;
-    const bool live = d0 + threadIdx.x < p.D;
-    const int lane = live ? threadIdx.x : 0;  // idle lanes repeat the block's first channel and write nothing
-    const int64_t d = d0 + lane;
+    const int lane = threadIdx.x;
+    const bool live = d0 + lane < p.D;
+    const int64_t d = live ? d0 + lane : p.D - 1;  // lanes behind the last channel repeat it
+    const TilePlace pl(d0, p.D);
 
     float h[NP], A2[NP];
 #pragma unroll
     for (int n = 0; n < NP; n++) {
-        A2[n] = n < p.N ? p.A[d * p.N + n] * LOG2E : 0.f;
-        h[n] = !STATE && p.hin && n < p.N ? p.hin[((b * p.G + g) * p.N + n) * p.D + d] : 0.f;
+        A2[n] = p.a2[n * p.D + d];
+        h[n] = 0.f;
+    }
+    if (!STATE && p.hin) {
+#pragma unroll
+        for (int n = 0; n < NP; n++) {
+            const float v = p.hin[((b * p.G + g) * p.N + min(n, p.N - 1)) * p.D + d];
+            h[n] = n < p.N ? v : 0.f;
+        }
     }
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     const float skip = !STATE && p.Dskip ? p.Dskip[d] : 0.f;
-    const int64_t len = seq_len(p.lengths, b, p.L);
-    const int64_t t0 = g * p.seglen, t1 = min(t0 + p.seglen, len);
+    const int t0 = (int)(g * p.seglen), t1 = min(t0 + (int)p.seglen, uniform((int)seq_len(p.lengths, b, p.L)));
     const bool gate = !STATE && p.z;
+    const E* ub = (const E*)p.u + b * p.su.batch + d0;
+    const E* xb = (const E*)p.dt + b * p.sdt.batch + d0;
+    const E* zb = gate ? (const E*)p.z + b * p.sz.batch + d0 : nullptr;
+    E* yb = STATE ? nullptr : (E*)p.y + b * p.sy.batch + d0;
+    scalar_f32 row = as_scalar(p.bc + (b * p.L + t0) * (2 * NP));
 
-    const T* ub = (const T*)p.u + b * p.su.batch + d0;
-    const T* xb = (const T*)p.dt + b * p.sdt.batch + d0;
-    const T* zb = gate ? (const T*)p.z + b * p.sz.batch + d0 : nullptr;
-    T* yb = STATE ? nullptr : (T*)p.y + b * p.sy.batch + d0;
-    scalar_f32 bcb = as_scalar(p.bc + b * p.L * (2 * NP));
-
-    T un[TB], xn[TB], zn[TB];
-    auto fetch = [&](int64_t t) {
-#pragma unroll
-        for (int j = 0; j < TB; j++) {
-            const int64_t tt = min(t + j, t1 - 1);
-            un[j] = ub[tt * p.su.token + lane];
-            xn[j] = xb[tt * p.sdt.token + lane];
-            if (gate) zn[j] = zb[tt * p.sz.token + lane];
-        }
+    Raw8<E> raw[NS];
+    auto fetch = [&](int t) {
+        const int tt = min(t + pl.token, t1 - 1);
+        raw[0] = tile_load<E, VEC>(ub, p.su.token, tt, pl);
+        raw[1] = tile_load<E, VEC>(xb, p.sdt.token, tt, pl);
+        if (gate) raw[NS - 1] = tile_load<E, VEC>(zb, p.sz.token, tt, pl);
     };
     float sum = 0.f;
     if (t0 < t1) fetch(t0);
-    for (int64_t t = t0; t < t1; t += TB) {
-        float dl[TB], du[TB], uu[TB], zz[TB];
+    for (int t = t0; t < t1; t += TT) {
+        wave_lds_fence();
 #pragma unroll
-        for (int j = 0; j < TB; j++) {
-            const float x = (float)xn[j] + bias;
-            dl[j] = p.softplus ? softplus<false>(x, nullptr) : x;
-            uu[j] = (float)un[j];
-            du[j] = dl[j] * uu[j];
-            if (gate) zz[j] = (float)zn[j];
+        for (int i = 0; i < NS; i++)
+            if (i < 2 || gate) *lds_chunk(tile[i], pl) = raw[i];
+        wave_lds_fence();
+        float dl[TT], du[TT], out[TT];
+#pragma unroll
+        for (int j = 0; j < TT; j++) dl[j] = (float)tile[1][j * 64 + lane] + bias;
+        if (p.softplus) {
+#pragma unroll
+            for (int j = 0; j < TT; j++) dl[j] = softplus<false>(dl[j], nullptr);
         }
-        if (t + TB < t1) fetch(t + TB);
-        const int nt = (int)min((int64_t)TB, t1 - t);
 #pragma unroll
-        for (int j = 0; j < TB; j++) {
-            if (j < nt) {
-                scalar_f32 row = bcb + (t + j) * (2 * NP);
-                float acc[2] = {skip * uu[j], 0.f};
+        for (int j = 0; j < TT; j++) {
+            const float u = (float)tile[0][j * 64 + lane];
+            dl[j] = t + j < t1 ? dl[j] : 0.f;
+            du[j] = dl[j] * u;
+            out[j] = skip * u;
+        }
+        if (t + TT < t1) fetch(t + TT);
 #pragma unroll
-                for (int n = 0; n < NP; n++) {
-                    const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
-                    h[n] = fmaf(a, h[n], du[j] * row[n]);
-                    if (!STATE) acc[n & 1] = fmaf(row[NP + n], h[n], acc[n & 1]);
-                }
-                if (STATE) {
-                    sum += dl[j];
-                } else {
-                    float v = acc[0] + acc[1];
-                    if (gate) v *= zz[j] * sigmoid(zz[j]);
-                    if (live) io<T>::st(yb + (t + j) * p.sy.token + lane, v);
+        for (int j = 0; j < TT; j++) {
+            float acc = 0.f;
+#pragma unroll
+            for (int n = 0; n < NP; n++) {
+                const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
+                h[n] = fmaf(a, h[n], du[j] * row[n]);
+                if (!STATE) {
+                    if (n & 1) acc = fmaf(row[NP + n], h[n], acc);
+                    else out[j] = fmaf(row[NP + n], h[n], out[j]);
                 }
             }
+            if (STATE) sum += dl[j];
+            else out[j] += acc;
+            row += t + j + 1 < t1 ? 2 * NP : 0;
         }
+        if (STATE) continue;
+        if (gate) {
+#pragma unroll
+            for (int j = 0; j < TT; j++) {
+                const float z = (float)tile[2][j * 64 + lane];
+                out[j] *= z * sigmoid(z);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TT; j++) io<E>::st(tile[3] + j * 64 + lane, out[j]);
+        wave_lds_fence();
+        if (pl.in && t + pl.token < t1)
+            store8<VEC>(yb + (t + pl.token) * p.sy.token + pl.col, pl.n, *lds_chunk(tile[3], pl));
     }
     if (!live) return;
     if (STATE) {
@@ -154,14 +188,14 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
 // States entering the segments from the segments' own end states: slot 0 takes s_in, slot g + 1
 // (holding segment g's end state from zero) adds the decayed state that entered segment g.  A thread
 // owns one (b, n, d); its loads are issued PB segments ahead of the chain.
-constexpr int PB = 8;
-__global__ __launch_bounds__(256) void ssm_segments_kernel(const float* __restrict__ A, const float* __restrict__ s_in,
+constexpr int PB = 32;
+__global__ __launch_bounds__(256) void ssm_segments_kernel(const float* __restrict__ a2, const float* __restrict__ s_in,
                                                            const float* __restrict__ sumdt, float* __restrict__ part,
                                                            int64_t total, int64_t D, int N, int G) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= total) return;
     const int64_t d = i % D, n = i / D % N, b = i / (D * N);
-    const float a2 = A[d * N + n] * LOG2E;
+    const float rate = a2[n * D + d];
     float h = s_in ? s_in[i] : 0.f;
     float* pp = part + (b * G * N + n) * D + d;
     const float* sp = sumdt + b * G * D + d;
@@ -178,7 +212,7 @@ __global__ __launch_bounds__(256) void ssm_segments_kernel(const float* __restri
 #pragma unroll
         for (int j = 0; j < PB; j++)
             if (g0 + j < G) {
-                h = fmaf(__builtin_amdgcn_exp2f(a2 * s[j]), h, v[j]);
+                h = fmaf(__builtin_amdgcn_exp2f(rate * s[j]), h, v[j]);
                 pp[(g0 + j) * ps] = h;
             }
     }
@@ -186,35 +220,36 @@ __global__ __launch_bounds__(256) void ssm_segments_kernel(const float* __restri
 
 int np_for(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 24 ? 24 : N <= 32 ? 32 : N <= 48 ? 48 : 64; }
 
-// Segments: about 2048 waves, none under 64 tokens.
-SsmPlan fwd_plan(int64_t B, int64_t L, int64_t D) { return ssm_plan(B, L, D, 2048, 64, TB); }
+// Segments: about 4096 waves, none under 16 tokens.
+SsmPlan fwd_plan(int64_t B, int64_t L, int64_t D) { return ssm_plan(B, L, D, 4096, 16, TT); }
 
 struct FwdWs {
-    float *bc, *part, *sumdt;
+    float *bc, *a2, *part, *sumdt;
     size_t bytes;
 };
 FwdWs fwd_cut(void* base, int64_t B, int64_t L, int64_t D, int N, int G) {
     WsCut c{(char*)base};
     FwdWs w;
     w.bc = c.take((size_t)(B * L) * 2 * np_for(N));
+    w.a2 = c.take((size_t)np_for(N) * D);
     w.part = G > 1 ? c.take((size_t)(B * G) * N * D) : nullptr;
     w.sumdt = G > 1 ? c.take((size_t)(B * G) * D) : nullptr;
     w.bytes = c.used;
     return w;
 }
 
-template <typename T, int NP>
+template <typename T, int NP, bool VEC>
 void launch_np(const SsmArgs& a, FwdDev p, const SsmPlan& pl) {
     p.cb = (unsigned)((a.D + 63) / 64);
     if (pl.G > 1) {
         p.ng = pl.G - 1;
-        LA_TRACED(a.tr, "ssm_state", ssm_fwd_kernel<T, NP, true><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
+        LA_TRACED(a.tr, "ssm_state", ssm_fwd_kernel<T, NP, true, VEC><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
         const int64_t total = a.B * a.N * a.D;
         LA_TRACED(a.tr, "ssm_segments", ssm_segments_kernel<<<(unsigned)((total + 255) / 256), 256, 0, a.stream>>>(
-                                            a.A, a.s_in, p.sumdt, p.part, total, a.D, a.N, pl.G));
+                                            p.a2, a.s_in, p.sumdt, p.part, total, a.D, a.N, pl.G));
     }
     p.ng = pl.G;
-    LA_TRACED(a.tr, "ssm_out", ssm_fwd_kernel<T, NP, false><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
+    LA_TRACED(a.tr, "ssm_out", ssm_fwd_kernel<T, NP, false, VEC><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
 }
 
 template <typename T>
@@ -223,23 +258,28 @@ hipError_t launch_t(const SsmArgs& a) {
     const FwdWs w = fwd_cut(a.ws, a.B, a.L, a.D, a.N, pl.G);
     const int NP = np_for(a.N);
     FwdDev p;
-    p.u = a.u; p.dt = a.dt; p.z = a.z; p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
+    p.u = a.u; p.dt = a.dt; p.z = a.z; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
     p.bc = w.bc;
+    p.a2 = w.a2;
     p.hin = pl.G > 1 ? w.part : a.s_in;
     p.lengths = a.lengths; p.y = a.y; p.s_out = a.s_out;
     p.part = w.part; p.sumdt = w.sumdt;
     p.L = a.L; p.D = a.D; p.seglen = pl.seglen; p.N = a.N; p.G = pl.G;
     p.softplus = a.softplus;
     p.su = a.su; p.sdt = a.sdt; p.sz = a.sz; p.sy = a.sy;
-    launch_pack_bc(a, w.bc, NP);
+    launch_pack(a, w.bc, w.a2, NP);
+    const bool vec = a.D % 8 == 0 && rows16(a.u, a.su, sizeof(T)) && rows16(a.dt, a.sdt, sizeof(T)) &&
+                     rows16(a.z, a.sz, sizeof(T)) && rows16(a.y, a.sy, sizeof(T));
+#define LA_SSM_NP(n) (vec ? launch_np<T, n, true>(a, p, pl) : launch_np<T, n, false>(a, p, pl))
     switch (NP) {
-        case 8: launch_np<T, 8>(a, p, pl); break;
-        case 16: launch_np<T, 16>(a, p, pl); break;
-        case 24: launch_np<T, 24>(a, p, pl); break;
-        case 32: launch_np<T, 32>(a, p, pl); break;
-        case 48: launch_np<T, 48>(a, p, pl); break;
-        default: launch_np<T, 64>(a, p, pl); break;
+        case 8: LA_SSM_NP(8); break;
+        case 16: LA_SSM_NP(16); break;
+        case 24: LA_SSM_NP(24); break;
+        case 32: LA_SSM_NP(32); break;
+        case 48: LA_SSM_NP(48); break;
+        default: LA_SSM_NP(64); break;
     }
+#undef LA_SSM_NP
     return hipGetLastError();
 }
 
@@ -323,16 +363,18 @@ hipError_t step_t(const SsmArgs& a) {
 }
 
 template <typename T>
-void pack_t(const SsmArgs& a, float* bc, int NP) {
-    const int64_t n = a.B * a.L * 2 * NP;
-    if (n == 0) return;
-    LA_TRACED(a.tr, "ssm_pack", pack_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, a.stream>>>(
-                                    (const T*)a.Bm, (const T*)a.Cm, a.sb, a.sc, bc, a.B * a.L, a.L, a.N, NP));
+void pack_t(const SsmArgs& a, float* bc, float* a2, int NP) {
+    const unsigned nbc = (unsigned)((a.B * a.L * 2 * NP + 255) / 256), na = (unsigned)((a.D * NP + 255) / 256);
+    LA_TRACED(a.tr, "ssm_pack", pack_kernel<T><<<nbc + na, 256, 0, a.stream>>>((const T*)a.Bm, (const T*)a.Cm, a.A, a.sb,
+                                                                               a.sc, bc, a2, a.B * a.L, a.L, a.D, a.N, NP,
+                                                                               nbc));
 }
 
 }  // namespace
 
-void launch_pack_bc(const SsmArgs& a, float* bc, int NP) { a.bf16 ? pack_t<__bf16>(a, bc, NP) : pack_t<float>(a, bc, NP); }
+void launch_pack(const SsmArgs& a, float* bc, float* a2, int NP) {
+    a.bf16 ? pack_t<__bf16>(a, bc, a2, NP) : pack_t<float>(a, bc, a2, NP);
+}
 
 size_t ssm_fwd_ws(int64_t B, int64_t L, int64_t D, int N) {
     return fwd_cut(nullptr, B, L, D, N, fwd_plan(B, L, D).G).bytes;

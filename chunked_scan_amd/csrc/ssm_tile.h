@@ -1,0 +1,99 @@
+// ssm_tile.h -- token tiles of the selective scan: 8 tokens by 64 channels of one activation, moved by
+// one wave.  In memory order a lane holds 8 adjacent channels of one token (one 16-byte access per
+// activation in bf16, two in f32); in the arithmetic a lane owns one channel.  LDS turns one into the
+// other.  The LDS region belongs to one wave, whose LDS accesses execute in order: no barrier, only a
+// fence for the compiler.
+#pragma once
+#include "la_mixer.h"
+
+namespace la {
+
+constexpr int TT = 8;  // tokens per tile
+
+__device__ __forceinline__ void wave_lds_fence() { asm volatile("" ::: "memory"); }
+
+template <typename E> struct Raw8;
+template <> struct Raw8<__bf16> {
+    u32x4 a;
+};
+template <> struct Raw8<float> {
+    f32x4 a, b;
+};
+
+// 8 elements at p of which the first n (1..8) exist; VEC: all exist and p is 16-byte aligned.  Elements
+// that do not exist repeat the last one.
+template <bool VEC>
+__device__ __forceinline__ Raw8<__bf16> load8(const __bf16* p, int n) {
+    Raw8<__bf16> r;
+    if (VEC) {
+        r.a = *(const u32x4*)p;
+    } else {
+        const uint16_t* q = (const uint16_t*)p;
+#pragma unroll
+        for (int i = 0; i < 4; i++) r.a[i] = q[min(2 * i, n - 1)] | ((uint32_t)q[min(2 * i + 1, n - 1)] << 16);
+    }
+    return r;
+}
+template <bool VEC>
+__device__ __forceinline__ Raw8<float> load8(const float* p, int n) {
+    Raw8<float> r;
+    if (VEC) {
+        r.a = *(const f32x4*)p;
+        r.b = *((const f32x4*)p + 1);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            r.a[i] = p[min(i, n - 1)];
+            r.b[i] = p[min(i + 4, n - 1)];
+        }
+    }
+    return r;
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__bf16* p, int n, const Raw8<__bf16>& r) {
+    if (VEC) {
+        *(u32x4*)p = r.a;
+    } else {
+        uint16_t* q = (uint16_t*)p;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) q[i] = (uint16_t)(r.a[i >> 1] >> (16 * (i & 1)));
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, int n, const Raw8<float>& r) {
+    if (VEC) {
+        *(f32x4*)p = r.a;
+        *((f32x4*)p + 1) = r.b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < n) p[i] = i < 4 ? r.a[i & 3] : r.b[i & 3];
+    }
+}
+
+// A wave's place in the tiles of one 64-channel block starting at d0: lane = token * 8 + chunk of 8 channels.
+struct TilePlace {
+    int token, col, n;  // its token; its first channel in the block and how many of its 8 exist
+    bool in;            // whether any does (if not: the block's last chunk is repeated, nothing is stored)
+    __device__ __forceinline__ TilePlace(int64_t d0, int64_t D) {
+        const int lane = threadIdx.x & 63, left = (int)min((int64_t)64, D - d0), c = (lane & 7) * 8;
+        token = lane >> 3;
+        in = c < left;
+        col = in ? c : (left - 1) / 8 * 8;
+        n = min(8, left - col);
+    }
+};
+
+// One activation's tiles: p points at token 0, channel d0 of the sequence.
+template <typename E, bool VEC>
+__device__ __forceinline__ Raw8<E> tile_load(const E* p, int64_t stride, int t, const TilePlace& pl) {
+    return load8<VEC>(p + t * stride + pl.col, pl.n);
+}
+// The lane's 8 channels in an LDS tile [TT][64].
+template <typename E>
+__device__ __forceinline__ Raw8<E>* lds_chunk(E* tile, const TilePlace& pl) {
+    return reinterpret_cast<Raw8<E>*>(tile + (threadIdx.x & 63) * 8);
+}
+
+}  // namespace la
