@@ -515,48 +515,54 @@ def la_set_chain_spin_limit(limit: int) -> int:
 
 
 class _On:
-    """The device and stream of a call: makes both current while the call allocates and enqueues."""
+    """The device and stream of a call: makes both current while the call allocates and enqueues.  A call on
+    the current device and stream, the common case, enters no context."""
+
+    __slots__ = ("device", "stream", "handle", "_dev", "_st")
 
     def __init__(self, t: torch.Tensor, name: str, stream):
         if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         self.device = t.device
+        self.stream = stream
         if stream is not None and stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
-        self.stream = stream
 
     def __enter__(self):
-        self._dev = torch.cuda.device(self.device)
-        self._dev.__enter__()
-        self._st = torch.cuda.stream(self.stream)  # no-op for None
-        self._st.__enter__()
-        self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        i = self.device.index
+        if self.stream is None and torch.cuda.current_device() == i:
+            self._dev = self._st = None
+        else:
+            self._dev = torch.cuda.device(self.device)
+            self._dev.__enter__()
+            self._st = torch.cuda.stream(self.stream)  # no-op for None
+            self._st.__enter__()
+        self.handle = torch._C._cuda_getCurrentRawStream(i)
         return self
 
     def __exit__(self, *exc):
-        self._st.__exit__(*exc)
-        self._dev.__exit__(*exc)
+        if self._dev is not None:
+            self._st.__exit__(*exc)
+            self._dev.__exit__(*exc)
 
     def check(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
         """``t`` (or None) with that type and shape on the call's device; dense, or any strides with a
         contiguous last dim."""
         if t is None:
             return None
+        if t.shape == shape and t.dtype is dtype and t.device == self.device:
+            if t.is_contiguous() or (not dense and (t.numel() == 0 or shape[-1] <= 1 or t.stride(-1) == 1)):
+                return t
+            raise ValueError(f"{name} must be contiguous" if dense else f"{name}: the last dim must be contiguous")
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}, not {t.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if dense and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if not dense and t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}: the last dim must be contiguous")
-        return t
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
     def out(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
         if t is None:
-            return torch.empty(tuple(shape), dtype=dtype, device=self.device)
+            return torch.empty(shape, dtype=dtype, device=self.device)
         return self.check(t, name, dtype, shape, dense)
 
     def workspace(self, fn: str, nbytes: int) -> torch.Tensor:
@@ -565,17 +571,24 @@ class _On:
         return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
 
-def _rows(t: Optional[torch.Tensor]) -> Rows:
-    """The batch and token strides of a [B, L, D] tensor (or [B, D]: the batch stride)."""
-    if t is None or t.numel() == 0 or t.is_contiguous():
-        return Rows(0, 0)
-    if t.dim() == 2:
-        # {0, 0} would mean dense: one repeated row is told apart by its unused token stride
-        return Rows(t.stride(0), t.shape[1])
-    b, s = t.stride(0), t.stride(1)
-    if b == 0 and s == 0:
-        raise ValueError("a view that repeats one row over batch and tokens is not supported: make it contiguous")
-    return Rows(b, s)
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _strided(shape, **views) -> None:
+    """Sets the la_rows fields of the views that are not dense: the batch and token strides of a [B, L, D]
+    tensor, the batch stride of a [B, D] one."""
+    for field, t in views.items():
+        if t is None or t.is_contiguous() or t.numel() == 0:
+            continue  # {0, 0}: dense
+        if t.dim() == 2:
+            # one repeated row ({0, 0} would mean dense) is told apart by its unused token stride
+            setattr(shape, field, Rows(t.stride(0), t.shape[1]))
+            continue
+        b, s = t.stride(0), t.stride(1)
+        if b == 0 and s == 0:
+            raise ValueError("a view that repeats one row over batch and tokens is not supported: make it contiguous")
+        setattr(shape, field, Rows(b, s))
 
 
 def _dims(t: torch.Tensor, name: str, n: int):
@@ -616,9 +629,10 @@ def la_short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
         y = on.out(y, "y", x.dtype, (B, L, D), dense=False)
         if state_out is not None or want_state:
             state_out = on.out(state_out, "state_out", x.dtype, (B, W - 1, D))
-        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0, x=_rows(x), y=_rows(y)), on, timer)
-        _check("la_short_conv", lib().la_short_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(lengths),
-                                                    _ptr(y), _ptr(state_out), ctypes.byref(shp)))
+        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0), on, timer)
+        _strided(shp, x=x, y=y)
+        _check("la_short_conv", lib().la_short_conv(_at(x), _at(weight), _at(bias), _at(state_in), _at(lengths),
+                                                    _at(y), _at(state_out), ctypes.byref(shp)))
     return y, state_out
 
 
@@ -641,12 +655,13 @@ def la_short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, b
         dw = on.out(None, "d_weight", torch.float32, (D, W))
         db = on.out(None, "d_bias", torch.float32, (D,)) if bias is not None else None
         ds = on.out(None, "d_state_in", x.dtype, (B, W - 1, D)) if state_in is not None else None
-        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0, x=_rows(x), dy=_rows(dy), dx=_rows(dx)), on, timer)
+        shp = _finish(ConvShape(B, L, D, W, dt, int(silu), 0), on, timer)
+        _strided(shp, x=x, dy=dy, dx=dx)
         n = lib().la_short_conv_bwd_workspace(ctypes.byref(shp))
         ws = on.workspace("la_short_conv_bwd_workspace", n)
         _check("la_short_conv_bwd", lib().la_short_conv_bwd(
-            _ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), _ptr(lengths), _ptr(dy), _ptr(d_state_out), _ptr(dx),
-            _ptr(dw), _ptr(db), _ptr(ds), _ptr(ws), n, ctypes.byref(shp)))
+            _at(x), _at(weight), _at(bias), _at(state_in), _at(lengths), _at(dy), _at(d_state_out), _at(dx),
+            _at(dw), _at(db), _at(ds), _at(ws), n, ctypes.byref(shp)))
     return dx, dw, db, ds
 
 
@@ -665,22 +680,24 @@ def la_short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tenso
         on.check(state, "state", x.dtype, (S, W - 1, D))
         on.check(slots, "slots", torch.int32, (B,))
         y = on.out(y, "y", x.dtype, (B, D), dense=False)
-        shp = _finish(ConvShape(B, 1, D, W, dt, int(silu), S, x=_rows(x), y=_rows(y)), on, timer)
-        _check("la_short_conv_step", lib().la_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots),
-                                                              _ptr(y), ctypes.byref(shp)))
+        shp = _finish(ConvShape(B, 1, D, W, dt, int(silu), S), on, timer)
+        _strided(shp, x=x, y=y)
+        _check("la_short_conv_step", lib().la_short_conv_step(_at(x), _at(weight), _at(bias), _at(state), _at(slots),
+                                                              _at(y), ctypes.byref(shp)))
     return y
 
 
 def _ssm_common(on, u, dt, A, B_, C, D, z, dt_bias, rows, Dn, N):
-    e = u.dtype
-    on.check(u, "u", e, rows + (Dn,), dense=False)
-    on.check(dt, "dt", e, rows + (Dn,), dense=False)
-    on.check(A, "A", torch.float32, (Dn, N))
-    on.check(B_, "B", e, rows + (N,), dense=False)
-    on.check(C, "C", e, rows + (N,), dense=False)
-    on.check(D, "D", torch.float32, (Dn,))
-    on.check(z, "z", e, rows + (Dn,), dense=False)
-    on.check(dt_bias, "dt_bias", torch.float32, (Dn,))
+    e, f32, check = u.dtype, torch.float32, on.check
+    wide, narrow, per_channel = rows + (Dn,), rows + (N,), (Dn,)
+    check(u, "u", e, wide, False)
+    check(dt, "dt", e, wide, False)
+    check(A, "A", f32, (Dn, N))
+    check(B_, "B", e, narrow, False)
+    check(C, "C", e, narrow, False)
+    check(D, "D", f32, per_channel)
+    check(z, "z", e, wide, False)
+    check(dt_bias, "dt_bias", f32, per_channel)
 
 
 def la_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *,
@@ -703,13 +720,13 @@ def la_ssm_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
         y = on.out(y, "y", u.dtype, (Bn, L, Dn), dense=False)
         if s_out is not None or want_state:
             s_out = on.out(s_out, "s_out", torch.float32, (Bn, N, Dn))
-        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
-                               z=_rows(z), y=_rows(y)), on, timer)
+        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0), on, timer)
+        _strided(shp, u=u, dt=dt, b=B, c=C, z=z, y=y)
         n = lib().la_ssm_workspace(ctypes.byref(shp), 0)
         ws = on.workspace("la_ssm_workspace", n)
-        _check("la_ssm_scan", lib().la_ssm_scan(_ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                                _ptr(dt_bias), _ptr(s_in), _ptr(lengths), _ptr(y), _ptr(s_out),
-                                                _ptr(ws), n, ctypes.byref(shp)))
+        _check("la_ssm_scan", lib().la_ssm_scan(_at(u), _at(dt), _at(A), _at(B), _at(C), _at(D), _at(z),
+                                                _at(dt_bias), _at(s_in), _at(lengths), _at(y), _at(s_out),
+                                                _at(ws), n, ctypes.byref(shp)))
     return y, s_out
 
 
@@ -744,15 +761,14 @@ def la_ssm_scan_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
         dD = on.out(None, "dD", f32, (Dn,)) if D is not None else None
         dbias = on.out(None, "d_dt_bias", f32, (Dn,)) if dt_bias is not None else None
         ds_in = on.out(None, "ds_in", f32, (Bn, N, Dn)) if s_in is not None else None
-        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
-                               z=_rows(z), dy=_rows(dy), du=_rows(du), ddt=_rows(ddt), db=_rows(dB), dc=_rows(dC),
-                               dz=_rows(dz)), on, timer)
+        shp = _finish(SsmShape(Bn, L, Dn, N, code, int(softplus), 0), on, timer)
+        _strided(shp, u=u, dt=dt, b=B, c=C, z=z, dy=dy, du=du, ddt=ddt, db=dB, dc=dC, dz=dz)
         n = lib().la_ssm_workspace(ctypes.byref(shp), 1)
         ws = on.workspace("la_ssm_workspace", n)
         _check("la_ssm_scan_bwd", lib().la_ssm_scan_bwd(
-            _ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(s_in), _ptr(lengths),
-            _ptr(dy), _ptr(ds_out), _ptr(du), _ptr(ddt), _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz), _ptr(dbias),
-            _ptr(ds_in), _ptr(ws), n, ctypes.byref(shp)))
+            _at(u), _at(dt), _at(A), _at(B), _at(C), _at(D), _at(z), _at(dt_bias), _at(s_in), _at(lengths),
+            _at(dy), _at(ds_out), _at(du), _at(ddt), _at(dA), _at(dB), _at(dC), _at(dD), _at(dz), _at(dbias),
+            _at(ds_in), _at(ws), n, ctypes.byref(shp)))
     return du, ddt, dA, dB, dC, dD, dz, dbias, ds_in
 
 
@@ -771,15 +787,15 @@ def la_ssm_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
         on.check(state, "state", torch.float32, (S, N, Dn))
         on.check(slots, "slots", torch.int32, (Bn,))
         y = on.out(y, "y", u.dtype, (Bn, Dn), dense=False)
-        shp = _finish(SsmShape(Bn, 1, Dn, N, code, int(softplus), S, u=_rows(u), dt=_rows(dt), b=_rows(B), c=_rows(C),
-                               z=_rows(z), y=_rows(y)), on, timer)
-        _check("la_ssm_step", lib().la_ssm_step(_ptr(u), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                                _ptr(dt_bias), _ptr(state), _ptr(slots), _ptr(y), ctypes.byref(shp)))
+        shp = _finish(SsmShape(Bn, 1, Dn, N, code, int(softplus), S), on, timer)
+        _strided(shp, u=u, dt=dt, b=B, c=C, z=z, y=y)
+        _check("la_ssm_step", lib().la_ssm_step(_at(u), _at(dt), _at(A), _at(B), _at(C), _at(D), _at(z),
+                                                _at(dt_bias), _at(state), _at(slots), _at(y), ctypes.byref(shp)))
     return y
 
 
 def _row_stride(t: Optional[torch.Tensor], name: str) -> int:
-    if t is None or t.numel() == 0 or t.is_contiguous() or t.shape[0] == 1:
+    if t is None or t.is_contiguous() or t.numel() == 0 or t.shape[0] == 1:
         return 0
     if t.stride(0) == 0:
         raise ValueError(f"{name}: a view that repeats one row is not supported")
@@ -808,7 +824,7 @@ def la_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
         shp = _finish(NormShape(M, D, code, 0, eps, x_stride=_row_stride(x, "x"),
                                 residual_stride=_row_stride(residual, "residual"), y_stride=_row_stride(y, "y"),
                                 h_stride=_row_stride(h, "h")), on, timer)
-        _check("la_add_norm", lib().la_add_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(h), _ptr(rstd),
+        _check("la_add_norm", lib().la_add_norm(_at(x), _at(residual), _at(weight), _at(y), _at(h), _at(rstd),
                                                 ctypes.byref(shp)))
     return y, (h if want else x), rstd
 
@@ -832,8 +848,8 @@ def la_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
         shp = _finish(NormShape(M, D, code, group, eps, x_stride=_row_stride(x, "x"),
                                 residual_stride=_row_stride(residual, "residual"), h_stride=_row_stride(h, "h")), on,
                       timer)
-        _check("la_add_norm_q8", lib().la_add_norm_q8(_ptr(x), _ptr(residual), _ptr(weight), _ptr(q), _ptr(scale), _ptr(h),
-                                                      _ptr(rstd), ctypes.byref(shp)))
+        _check("la_add_norm_q8", lib().la_add_norm_q8(_at(x), _at(residual), _at(weight), _at(q), _at(scale), _at(h),
+                                                      _at(rstd), ctypes.byref(shp)))
     return q, scale, (h if want else x), rstd
 
 
@@ -856,6 +872,6 @@ def la_add_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
                                 dh_stride=_row_stride(dh, "dh"), dx_stride=_row_stride(dx, "dx")), on, timer)
         n = lib().la_add_norm_bwd_workspace(ctypes.byref(shp))
         ws = on.workspace("la_add_norm_bwd_workspace", n)
-        _check("la_add_norm_bwd", lib().la_add_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx),
-                                                        _ptr(dw), _ptr(ws), n, ctypes.byref(shp)))
+        _check("la_add_norm_bwd", lib().la_add_norm_bwd(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), _at(dx),
+                                                        _at(dw), _at(ws), n, ctypes.byref(shp)))
     return dx, dw
