@@ -162,6 +162,14 @@ __device__ __forceinline__ float softplus(float x, float* d) {
     return fmaf(s, p, fmaxf(x, 0.f));
 }
 
+// Two values rounded to bf16, nearest even, in one instruction; and eight.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+__device__ __forceinline__ u32x4 pack8_pairs(const float* f) {
+    return u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+}
+
 __device__ __forceinline__ int64_t seq_len(const int32_t* lengths, int64_t b, int64_t L) {
     if (!lengths) return L;
     const int64_t n = lengths[b];

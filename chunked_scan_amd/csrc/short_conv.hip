@@ -27,7 +27,21 @@ template <> struct Vec<__bf16, 8> {
             f[2 * i + 1] = bits_hi_bf16(r[i]);
         }
     }
-    static __device__ __forceinline__ void st(__bf16* p, const float* f) { *(u32x4*)p = pack8(f); }
+    static __device__ __forceinline__ void st(__bf16* p, const float* f) { *(u32x4*)p = pack8_pairs(f); }
+};
+template <> struct Vec<__bf16, 4> {
+    typedef u32x2 raw;
+    static __device__ __forceinline__ raw ld(const __bf16* p) { return *(const u32x2*)p; }
+    static __device__ __forceinline__ void get(raw r, float* f) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            f[2 * i] = bits_lo_bf16(r[i]);
+            f[2 * i + 1] = bits_hi_bf16(r[i]);
+        }
+    }
+    static __device__ __forceinline__ void st(__bf16* p, const float* f) {
+        *(u32x2*)p = u32x2{pack2(f[0], f[1]), pack2(f[2], f[3])};
+    }
 };
 template <> struct Vec<float, 4> {
     typedef f32x4 raw;
@@ -79,8 +93,19 @@ __device__ __forceinline__ void input_at(const ConvDev& c, int64_t b, int64_t po
     }
 }
 
+// The taps and the bias of VEC channels: W VEC adjacent floats.
+template <int W, int VEC>
+__device__ __forceinline__ void load_taps(const ConvDev& c, int64_t d, float (*w)[VEC], float* bias) {
+#pragma unroll
+    for (int v = 0; v < VEC; v++)
+#pragma unroll
+        for (int j = 0; j < W; j++) w[j][v] = c.weight[(d + v) * W + j];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) bias[v] = c.bias ? c.bias[d + v] : 0.f;
+}
+
 // A thread per (sequence, token tile, channel vector), channel vectors fastest; the sequence's last tile
-// also writes state_out.
+// also writes state_out.  Full blocks of TB tokens, the next block's loads in flight, then the tile's rest.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvDev c, unsigned total) {
     typedef Vec<E, VEC> V;
@@ -89,7 +114,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvDev c, unsigned total
     const int64_t d = (int64_t)(i % c.nvec) * VEC;
     const unsigned tile = i / c.nvec % c.tiles;
     const int64_t b = i / c.nvec / c.tiles;
-    const int64_t len = seq_len(c.lengths, b, c.L);
+    const int len = (int)seq_len(c.lengths, b, c.L);
     if (c.state_out && tile == c.tiles - 1) {
         for (int j = 0; j < W - 1; j++) {
             float f[VEC];
@@ -97,50 +122,56 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvDev c, unsigned total
             V::st((E*)c.state_out + (b * (W - 1) + j) * c.D + d, f);
         }
     }
-    const int64_t t0 = (int64_t)tile * c.TL, t1 = min(t0 + c.TL, len);
+    const int t0 = tile * c.TL, t1 = min(t0 + c.TL, len);
     if (t0 >= t1) return;
-    float w[W][VEC], bias[VEC], win[W - 1][VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; v++) {
-#pragma unroll
-        for (int j = 0; j < W; j++) w[j][v] = c.weight[(d + v) * W + j];
-        bias[v] = c.bias ? c.bias[d + v] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; j++) input_at<E, W, VEC>(c, b, t0 - (W - 1) + j, d, win[j]);
-    const E* xb = (const E*)c.x + b * c.sx.batch + d;
-    E* yb = (E*)c.y + b * c.sy.batch + d;
+    const E* xp = (const E*)c.x + b * c.sx.batch + t0 * c.sx.token + d;
+    E* yp = (E*)c.y + b * c.sy.batch + t0 * c.sy.token + d;
     typename V::raw nx[TB];
-    auto fetch = [&](int64_t t) {
+    auto fetch = [&]() {
 #pragma unroll
-        for (int j = 0; j < TB; j++) nx[j] = V::ld(xb + min(t + j, t1 - 1) * c.sx.token);
+        for (int j = 0; j < TB; j++) nx[j] = V::ld(xp + j * c.sx.token);
+        xp += TB * c.sx.token;
     };
-    fetch(t0);
-    for (int64_t t = t0; t < t1; t += TB) {
-        float x[W - 1 + TB][VEC];
+    if (t0 + TB <= t1) fetch();
+    float w[W][VEC], bias[VEC], x[W - 1 + TB][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) input_at<E, W, VEC>(c, b, t0 - (W - 1) + j, d, x[j]);
+    load_taps<W, VEC>(c, d, w, bias);
+    auto token = [&](int j) {
+        float o[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            float s = bias[v];
+#pragma unroll
+            for (int k = 0; k < W; k++) s = fmaf(w[k][v], x[j + k][v], s);
+            o[v] = s;
+        }
+        if (c.silu)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) o[v] *= sigmoid(o[v]);
+        V::st(yp, o);
+        yp += c.sy.token;
+    };
+    auto shift = [&](int n) {
 #pragma unroll
         for (int j = 0; j < W - 1; j++)
 #pragma unroll
-            for (int v = 0; v < VEC; v++) x[j][v] = win[j][v];
+            for (int v = 0; v < VEC; v++) x[j][v] = x[n + j][v];
+    };
+    int t = t0;
+    for (; t + TB <= t1; t += TB) {
 #pragma unroll
         for (int j = 0; j < TB; j++) V::get(nx[j], x[W - 1 + j]);
-        if (t + TB < t1) fetch(t + TB);
+        if (t + 2 * TB <= t1) fetch();
 #pragma unroll
-        for (int j = 0; j < TB; j++) {
-            float o[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                float s = bias[v];
-#pragma unroll
-                for (int k = 0; k < W; k++) s = fmaf(w[k][v], x[j + k][v], s);
-                o[v] = c.silu ? s * sigmoid(s) : s;
-            }
-            if (t + j < t1) V::st(yb + (t + j) * c.sy.token, o);
-        }
-#pragma unroll
-        for (int j = 0; j < W - 1; j++)
-#pragma unroll
-            for (int v = 0; v < VEC; v++) win[j][v] = x[TB + j][v];
+        for (int j = 0; j < TB; j++) token(j);
+        shift(TB);
+    }
+    for (; t < t1; t++) {
+        V::get(V::ld(xp), x[W - 1]);
+        xp += c.sx.token;
+        token(0);
+        shift(1);
     }
 }
 
@@ -148,7 +179,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvDev c, unsigned total
 //   dx_s = sum_j w[j] p_{s+W-1-j}  (+ d_state_out where s is one of the last W - 1 positions).
 // A thread walks its tile's tokens t = t0 .. t1-1 and W - 1 more: at t it knows x_{t-W+1..t}, so v_t and
 // p_t, and writes dx_{t-W+1}.  It owns p_t of its tile for the weight's sums; the tile that holds
-// position 0 also owns the W - 1 positions before it, which are the incoming state's.
+// position 0 also owns the W - 1 positions before it, which are the incoming state's.  Between the first
+// and the last W - 1 steps nothing is special and the loop is plain.
 template <typename E, int W, int VEC>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvDev c, unsigned total) {
     typedef Vec<E, VEC> V;
@@ -157,133 +189,150 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvDev c, unsigned total
     const int64_t d = (int64_t)(i % c.nvec) * VEC;
     const unsigned tile = i / c.nvec % c.tiles;
     const int64_t b = i / c.nvec / c.tiles;
-    const int64_t len = seq_len(c.lengths, b, c.L);
-    const int64_t t0 = (int64_t)tile * c.TL, te = min(t0 + c.TL, c.L), t1 = min(te, len);
-    float w[W][VEC], bias[VEC], dw[W][VEC], db[VEC], x[W][VEC], p[W][VEC];
+    const int len = (int)seq_len(c.lengths, b, c.L);
+    const int t0 = tile * c.TL, te = (int)min((int64_t)t0 + c.TL, c.L), t1 = min(te, len);
+    float w[W][VEC], bias[VEC], dw[W][VEC], db[VEC];
+    float x[W - 1 + TB][VEC], p[W - 1 + TB][VEC];  // x_{t-W+1..}, p_{t-W+1..}: the last W - 1 and the block's
+    load_taps<W, VEC>(c, d, w, bias);
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
 #pragma unroll
-        for (int j = 0; j < W; j++) {
-            w[j][v] = c.weight[(d + v) * W + j];
-            dw[j][v] = 0.f;
-            p[j][v] = 0.f;
-        }
-        bias[v] = c.bias ? c.bias[d + v] : 0.f;
+        for (int j = 0; j < W; j++) dw[j][v] = 0.f;
         db[v] = 0.f;
     }
     const E* xb = (const E*)c.x + b * c.sx.batch + d;
     const E* yb = (const E*)c.dy + b * c.sdy.batch + d;
     E* gb = (E*)c.dx + b * c.sdx.batch + d;
-    float zero[VEC];
+    // p of the block's token j, from x[j .. j + W - 1]
+    auto grad = [&](int j, typename V::raw dyr, bool in, bool own) {
+        float dyv[VEC];
+        V::get(dyr, dyv);
 #pragma unroll
-    for (int v = 0; v < VEC; v++) zero[v] = 0.f;
-    for (int64_t t = max(t0, len); t < te; t++) V::st(gb + t * c.sdx.token, zero);
-    // positions this tile writes: [s0, t1); tile 0 from -(W - 1)
-    const int64_t s0 = tile == 0 ? -(W - 1) : t0;
-    if (s0 < t1 || tile == 0) {
-        const int64_t s1 = max(t1, (int64_t)0);
-        // inputs x[1..W-1] = x_{s0-W+1 .. s0-1}; below -(W - 1) nothing reads them
+        for (int v = 0; v < VEC; v++) {
+            float g = dyv[v];
+            if (c.silu) {
+                float s = bias[v];
 #pragma unroll
-        for (int j = 1; j < W; j++) {
-            const int64_t pos = s0 - W + j;
-            if (pos >= -(W - 1))
-                input_at<E, W, VEC>(c, b, pos, d, x[j]);
-            else
+                for (int k = 0; k < W; k++) s = fmaf(w[k][v], x[j + k][v], s);
+                const float sg = sigmoid(s);
+                g *= sg * fmaf(s, 1.f - sg, 1.f);
+            }
+            g = in ? g : 0.f;
+            p[W - 1 + j][v] = g;
+            if (own) {
+                db[v] += g;
 #pragma unroll
-                for (int v = 0; v < VEC; v++) x[j][v] = 0.f;
+                for (int k = 0; k < W; k++) dw[k][v] = fmaf(g, x[j + k][v], dw[k][v]);
+            }
         }
-        typename V::raw nx[TB], ny[TB];
-        const int64_t tend = s1 + W - 1;  // walk t = s0 .. tend-1
-        auto fetch = [&](int64_t t) {
-            if (len > 0)
+    };
+    // dx of position t - (W - 1), t the block's token j: p[j + k] = p_{s + k} meets tap W - 1 - k
+    auto out = [&](int j, float* o) {
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            o[v] = 0.f;
+#pragma unroll
+            for (int k = 0; k < W; k++) o[v] = fmaf(w[W - 1 - k][v], p[j + k][v], o[v]);
+        }
+    };
+    auto shift = [&](int n) {
+#pragma unroll
+        for (int j = 0; j < W - 1; j++)
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                x[j][v] = x[n + j][v];
+                p[j][v] = p[n + j][v];
+            }
+    };
+    const int s0 = tile == 0 ? -(W - 1) : t0, s1 = max(t1, 0);  // positions this tile writes
+    // any token, one at a time
+    auto step = [&](int t) {
+        input_at<E, W, VEC>(c, b, min(t, len - 1), d, x[W - 1]);  // behind the end: any value, p is zero
+        const bool in = t >= 0 && t < len;
+        typename V::raw dyr = {};
+        if (in) dyr = V::ld(yb + t * c.sdy.token);
+        grad(0, dyr, in, in && t >= t0 && t < t1);
+        const int s = t - (W - 1);
+        if (s >= s0 && s < s1) {
+            float o[VEC];
+            out(0, o);
+            const int so = s - (len - (W - 1));
+            if (so >= 0 && c.d_state_out) {
+                float f[VEC];
+                V::get(V::ld((const E*)c.d_state_out + (b * (W - 1) + so) * c.D + d), f);
+#pragma unroll
+                for (int v = 0; v < VEC; v++) o[v] += f[v];
+            }
+            if (s >= 0)
+                V::st(gb + s * c.sdx.token, o);
+            else if (c.d_state_in)
+                V::st((E*)c.d_state_in + (b * (W - 1) + (W - 1 + s)) * c.D + d, o);
+        }
+        shift(1);
+    };
+    if (s0 < t1 || tile == 0) {
+        // x_{s0-W+1 .. s0-1}; below position -(W - 1) nothing reads them
+#pragma unroll
+        for (int j = 0; j < W - 1; j++) {
+            const int pos = s0 - (W - 1) + j;
+#pragma unroll
+            for (int v = 0; v < VEC; v++) x[j][v] = p[j][v] = 0.f;
+            if (pos >= -(W - 1)) input_at<E, W, VEC>(c, b, min(pos, len - 1), d, x[j]);
+        }
+        int t = s0;
+        const int ta = max(s0 + W - 1, W - 1);  // from here on t - (W - 1) is a position >= 0 of this tile
+        for (; t < min(ta, s1 + W - 1); t++) step(t);
+        if (t + TB <= t1) {
+            const E* xp = xb + t * c.sx.token;
+            const E* yp = yb + t * c.sdy.token;
+            E* gp = gb + (t - (W - 1)) * c.sdx.token;
+            typename V::raw nx[TB], ny[TB];
+            auto fetch = [&]() {
 #pragma unroll
                 for (int j = 0; j < TB; j++) {
-                    const int64_t tt = max((int64_t)0, min(t + j, len - 1));
-                    nx[j] = V::ld(xb + tt * c.sx.token);
-                    ny[j] = V::ld(yb + tt * c.sdy.token);
+                    nx[j] = V::ld(xp + j * c.sx.token);
+                    ny[j] = V::ld(yp + j * c.sdy.token);
                 }
-        };
-        fetch(s0);
-        for (int64_t t = s0; t < tend; t += TB) {
-            typename V::raw cx[TB], cy[TB];
+                xp += TB * c.sx.token;
+                yp += TB * c.sdy.token;
+            };
+            fetch();
+            for (; t + TB <= t1; t += TB) {
+                typename V::raw cy[TB];
 #pragma unroll
-            for (int j = 0; j < TB; j++) {
-                cx[j] = nx[j];
-                cy[j] = ny[j];
-            }
-            if (t + TB < tend) fetch(t + TB);
-#pragma unroll
-            for (int j = 0; j < TB; j++) {
-                const int64_t tt = t + j;
-#pragma unroll
-                for (int k = 0; k < W - 1; k++)
-#pragma unroll
-                    for (int v = 0; v < VEC; v++) {
-                        x[k][v] = x[k + 1][v];
-                        p[k][v] = p[k + 1][v];
-                    }
-                if (tt < 0)
-                    input_at<E, W, VEC>(c, b, tt, d, x[W - 1]);
-                else
-                    V::get(cx[j], x[W - 1]);
-                float dyv[VEC];
-                V::get(cy[j], dyv);
-                const bool in = tt >= 0 && tt < len;
-                const bool own = in && tt >= t0 && tt < t1;
-#pragma unroll
-                for (int v = 0; v < VEC; v++) {
-                    float s = bias[v];
-#pragma unroll
-                    for (int k = 0; k < W; k++) s = fmaf(w[k][v], x[k][v], s);
-                    float g = dyv[v];
-                    if (c.silu) {
-                        const float sg = sigmoid(s);
-                        g *= sg * fmaf(s, 1.f - sg, 1.f);
-                    }
-                    g = in ? g : 0.f;
-                    p[W - 1][v] = g;
-                    if (own) {
-                        db[v] += g;
-#pragma unroll
-                        for (int k = 0; k < W; k++) dw[k][v] = fmaf(g, x[k][v], dw[k][v]);
-                    }
+                for (int j = 0; j < TB; j++) {
+                    V::get(nx[j], x[W - 1 + j]);
+                    cy[j] = ny[j];
                 }
-                // position s = tt - (W - 1): p[k] = p_{s + k}, met by tap W - 1 - k
-                const int64_t s = tt - (W - 1);
-                if (s >= s0 && s < s1 && tt < tend) {
+                if (t + 2 * TB <= t1) fetch();
+#pragma unroll
+                for (int j = 0; j < TB; j++) {
+                    grad(j, cy[j], true, true);
                     float o[VEC];
-#pragma unroll
-                    for (int v = 0; v < VEC; v++) {
-                        o[v] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; k++) o[v] = fmaf(w[W - 1 - k][v], p[k][v], o[v]);
-                    }
-                    const int64_t so = s - (len - (W - 1));
-                    if (so >= 0 && c.d_state_out) {
-                        float f[VEC];
-                        V::get(V::ld((const E*)c.d_state_out + (b * (W - 1) + so) * c.D + d), f);
-#pragma unroll
-                        for (int v = 0; v < VEC; v++) o[v] += f[v];
-                    }
-                    if (s >= 0)
-                        V::st(gb + s * c.sdx.token, o);
-                    else if (c.d_state_in)
-                        V::st((E*)c.d_state_in + (b * (W - 1) + (W - 1 + s)) * c.D + d, o);
+                    out(j, o);
+                    V::st(gp, o);
+                    gp += c.sdx.token;
                 }
+                shift(TB);
             }
         }
+        for (; t < s1 + W - 1; t++) step(t);
+    }
+    for (int t = max(t0, len); t < te; t++) {  // behind the sequence's end
+        float zero[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) zero[v] = 0.f;
+        V::st(gb + t * c.sdx.token, zero);
     }
     float* part = c.part + ((b * c.tiles + tile) * (W + 1)) * c.D + d;
 #pragma unroll
-    for (int v = 0; v < VEC; v++) {
+    for (int k = 0; k <= W; k++)
 #pragma unroll
-        for (int k = 0; k < W; k++) part[k * c.D + v] = dw[k][v];
-        part[W * c.D + v] = db[v];
-    }
+        for (int v = 0; v < VEC; v++) part[k * c.D + v] = k < W ? dw[k][v] : db[v];
 }
 
-// d_weight [D, W] and d_bias [D] from the tiles' sums: 64 channels of one row (a tap or the bias) per
-// block, the tiles shared by 16 groups of 16 lanes... each lane sums its share of the tiles.
+// d_weight [D, W] and d_bias [D] from the tiles' sums: 16 channels of one tap (or the bias) per block, 16
+// threads to a channel, each a share of the tiles.
 __global__ __launch_bounds__(256) void conv_bwd_sums_kernel(const float* __restrict__ part, float* __restrict__ dw,
                                                             float* __restrict__ db, int64_t D, int W, int64_t rows) {
     __shared__ float sum[16][16];
@@ -353,18 +402,16 @@ bool rows16(const void* p, la_rows r, size_t es) {
     return !p || (aligned16(p) && (r.batch * es) % 16 == 0 && (r.token * es) % 16 == 0);
 }
 
-// Tokens per thread: enough threads for about eight waves per SIMD's worth of loads, tiles of 8 to
-// 64 tokens (each tile re-reads W - 1 rows of its neighbour).
-int fwd_tile(int64_t B, int64_t L, int64_t nvec) {
-    int TL = 64;
-    while (TL > 8 && B * ((L + TL - 1) / TL) * nvec < 256 * 2048) TL /= 2;
+// Tokens per thread: 16 in the forward and 32 in the backward (which writes W + 1 sums per channel and tile),
+// fewer where that leaves under 2048 waves, two per SIMD.  Each tile re-reads W - 1 rows and loads the taps:
+// 16384 x 2048 bf16, W = 4: 8 tokens 35 us, 16 30, 32 33, 64 33; backward of 8192 x 2048: 16 tokens 38 + 8 us
+// for the sums, 32 29 + 5, 64 32 + 4.
+int tile_tokens(int64_t B, int64_t L, int64_t nvec, int TL) {
+    while (TL > 8 && B * ((L + TL - 1) / TL) * nvec < 2048 * 64) TL /= 2;
     return TL;
 }
-int bwd_tile(int64_t B, int64_t L, int64_t nvec) {
-    int TL = 64;
-    while (TL > 16 && B * ((L + TL - 1) / TL) * nvec < 256 * 1024) TL /= 2;
-    return TL;
-}
+int fwd_tile(int64_t B, int64_t L, int64_t nvec) { return tile_tokens(B, L, nvec, 16); }
+int bwd_tile(int64_t B, int64_t L, int64_t nvec) { return tile_tokens(B, L, nvec, 32); }
 
 template <typename E, int W, int VEC>
 hipError_t fwd_w(const ConvArgs& a, ConvDev c) {
@@ -404,7 +451,11 @@ hipError_t step_w(const ConvArgs& a) {
 enum What { FWD, BWD, STEP };
 template <typename E, int W, int VEC>
 hipError_t run_w(What what, const ConvArgs& a, const ConvDev& c) {
-    return what == FWD ? fwd_w<E, W, VEC>(a, c) : what == BWD ? bwd_w<E, W, VEC>(a, c) : step_w<E, W, VEC>(a);
+    if constexpr (VEC == 1 || VEC == 4)
+        if (what == BWD) return bwd_w<E, W, VEC>(a, c);
+    if constexpr (VEC == 1 || VEC == 16 / sizeof(E))
+        return what == FWD ? fwd_w<E, W, VEC>(a, c) : step_w<E, W, VEC>(a);
+    return hipErrorInvalidValue;  // not reached
 }
 template <typename E, int VEC>
 hipError_t run_v(What what, const ConvArgs& a, const ConvDev& c) {
@@ -419,12 +470,14 @@ hipError_t run(What what, const ConvArgs& a) {
     c.d_state_in = a.d_state_in; c.part = (float*)a.ws;
     c.L = a.L; c.D = a.D; c.silu = a.silu;
     c.sx = a.sx; c.sy = a.sy; c.sdy = a.sdy; c.sdx = a.sdx;
+    // 16 bytes a lane; the backward, with four times the registers per channel, 4 channels
     constexpr int VEC = 16 / sizeof(E);
     const size_t es = sizeof(E);
     const bool vec = a.D % VEC == 0 && rows16(a.x, a.sx, es) && rows16(a.y, a.sy, es) && rows16(a.dy, a.sdy, es) &&
                      rows16(a.dx, a.sdx, es) && aligned16(a.state_in) && aligned16(a.state_out) &&
                      aligned16(a.d_state_out) && aligned16(a.d_state_in) && aligned16(a.state);
-    return vec ? run_v<E, VEC>(what, a, c) : run_v<E, 1>(what, a, c);
+    if (!vec) return run_v<E, 1>(what, a, c);
+    return what == BWD ? run_v<E, 4>(what, a, c) : run_v<E, VEC>(what, a, c);
 }
 hipError_t run(What what, const ConvArgs& a) { return a.bf16 ? run<__bf16>(what, a) : run<float>(what, a); }
 
@@ -433,7 +486,7 @@ hipError_t run(What what, const ConvArgs& a) { return a.bf16 ? run<__bf16>(what,
 // One row of W + 1 sums per token tile; the scalar form has the most threads and the longest tiles, so
 // the vector form's count bounds both.
 size_t short_conv_bwd_ws(int64_t B, int64_t L, int64_t D, int width, bool bf16) {
-    const int64_t nvec = std::max<int64_t>(1, D / (bf16 ? 8 : 4));
+    const int64_t nvec = std::max<int64_t>(1, D / 4);
     const int TL = bwd_tile(B, L, nvec);
     return (size_t)(B * std::max<int64_t>(1, (L + TL - 1) / TL) * (width + 1) * D) * sizeof(float);
 }

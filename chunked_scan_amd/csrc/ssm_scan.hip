@@ -284,70 +284,122 @@ hipError_t launch_t(const SsmArgs& a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// One token per sequence.  A lane owns one channel of one row; it reads and writes the state of its
-// slot once, 256 contiguous bytes per wave and key dim.  B and C are loaded once per wave, lane n
-// holding B[n] and C[n], and broadcast by lane reads.  `first_use`: rows that name a slot an earlier
-// row names are padding, so that no two rows write one state.
+// One token per sequence.  A lane owns one channel and reads and writes its state once, 256 contiguous bytes
+// per wave and key dim; with many rows a wave takes R of them one after the other, the next row's loads in
+// flight, so that its rates (A's rows, N floats apart from lane to lane) are loaded once for all of them.
+// B and C are loaded once per wave and row, lane n holding B[n] and C[n], and broadcast by lane reads.
+// Rows that name a slot an earlier row names are padding, so that no two rows write one state.
 __device__ __forceinline__ bool earlier_row_has(const int32_t* slots, int64_t b, int32_t s) {
     bool dup = false;
     for (int64_t i = threadIdx.x & 63; i < b; i += 64) dup |= slots[i] == s;
     return __any(dup);
 }
 
-template <typename T, int NP>
-__global__ __launch_bounds__(64) void ssm_step_kernel(const T* __restrict__ u, const T* __restrict__ dt,
-                                                      const float* __restrict__ A, const T* __restrict__ Bm,
-                                                      const T* __restrict__ Cm, const float* __restrict__ Dskip,
-                                                      const T* __restrict__ z, const float* __restrict__ dt_bias,
-                                                      float* __restrict__ state, const int32_t* __restrict__ slots,
-                                                      T* __restrict__ y, int64_t su, int64_t sdt, int64_t sb, int64_t sc,
-                                                      int64_t sz, int64_t sy, int64_t D, unsigned cb, int N, int nslots, bool sp) {
-    const int64_t b = blockIdx.x / cb;
-    const int64_t d0 = (int64_t)(blockIdx.x % cb) * 64;
-    const bool live = d0 + threadIdx.x < D;
-    const int64_t d = live ? d0 + threadIdx.x : d0;
-    const int64_t slot = slots ? slots[b] : b;
-    if (slot < 0 || slot >= nslots) return;
-    const int n0 = threadIdx.x < N ? threadIdx.x : N - 1;
-    const float bl = (float)Bm[b * sb + n0], cl = (float)Cm[b * sc + n0];
-    float* st = state + slot * N * D + d;
-    float h[NP], a2[NP];
+struct StepDev {
+    const void* u;
+    const void* dt;
+    const void* Bm;
+    const void* Cm;
+    const void* z;
+    const float* A;
+    const float* Dskip;
+    const float* dt_bias;
+    float* state;
+    const int32_t* slots;
+    void* y;
+    int64_t su, sdt, sb, sc, sz, sy, B, D;
+    unsigned cb;
+    int N, nslots, R;
+    bool softplus;
+};
+
+// A4: A's rows are 16-byte aligned (N a multiple of 4).
+template <typename T, int NP, bool A4>
+__global__ __launch_bounds__(64) void ssm_step_kernel(StepDev p) {
+    const int64_t d0 = (int64_t)(blockIdx.x % p.cb) * 64;
+    const bool live = d0 + threadIdx.x < p.D;
+    const int64_t d = live ? d0 + threadIdx.x : p.D - 1;
+    const int64_t b0 = (int64_t)(blockIdx.x / p.cb) * p.R, b1 = min(b0 + p.R, p.B);
+    const int n0 = threadIdx.x < p.N ? threadIdx.x : p.N - 1;
+
+    float h[NP], nb, nc, nu, nx, nz = 0.f;
+    int slot;
+    auto fetch = [&](int64_t b) {
+        slot = p.slots ? uniform(p.slots[b]) : (int)b;
+        const bool ok = slot >= 0 && slot < p.nslots;
+        const float* st = p.state + (int64_t)(ok ? slot : 0) * p.N * p.D + d;
+        if (ok)
 #pragma unroll
-    for (int n = 0; n < NP; n++) {
-        h[n] = n < N ? st[(int64_t)n * D] : 0.f;
-        a2[n] = n < N ? A[d * N + n] * LOG2E : 0.f;
-    }
-    const float uu = (float)u[b * su + d];
-    const float x = (float)dt[b * sdt + d] + (dt_bias ? dt_bias[d] : 0.f);
-    const float zz = z ? (float)z[b * sz + d] : 0.f;
-    float acc = Dskip ? Dskip[d] * uu : 0.f;
-    const float delta = sp ? softplus<false>(x, nullptr) : x;
-    const float du = delta * uu;
+            for (int n = 0; n < NP; n++) h[n] = st[min(n, p.N - 1) * p.D];
+        nb = (float)((const T*)p.Bm)[b * p.sb + n0];
+        nc = (float)((const T*)p.Cm)[b * p.sc + n0];
+        nu = (float)((const T*)p.u)[b * p.su + d];
+        nx = (float)((const T*)p.dt)[b * p.sdt + d];
+        if (p.z) nz = (float)((const T*)p.z)[b * p.sz + d];
+    };
+    fetch(b0);
+    float a2[NP];
+    const float* ar = p.A + d * p.N;
 #pragma unroll
-    for (int n = 0; n < NP; n++)
-        if (n < N) {
-            const float bn = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bl), n));
-            const float cn = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cl), n));
-            h[n] = fmaf(__builtin_amdgcn_exp2f(delta * a2[n]), h[n], du * bn);
-            acc = fmaf(cn, h[n], acc);
+    for (int n = 0; n < NP; n += 4) {
+        if (A4) {
+            const f32x4 v = *(const f32x4*)(ar + min(n, p.N - 4));
+#pragma unroll
+            for (int i = 0; i < 4; i++) a2[n + i] = v[i] * LOG2E;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) a2[n + i] = ar[min(n + i, p.N - 1)] * LOG2E;
         }
-    if (slots && earlier_row_has(slots, b, (int32_t)slot)) return;
-    if (!live) return;
+    }
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.Dskip ? p.Dskip[d] : 0.f;
+    for (int64_t b = b0; b < b1; b++) {
+        float cur[NP];
 #pragma unroll
-    for (int n = 0; n < NP; n++)
-        if (n < N) st[(int64_t)n * D] = h[n];
-    if (z) acc *= zz * sigmoid(zz);
-    io<T>::st(y + b * sy + d, acc);
+        for (int n = 0; n < NP; n++) cur[n] = h[n];
+        const float bl = nb, cl = nc, u = nu, x = nx + bias, z = nz;
+        const int s = slot;
+        if (b + 1 < b1) fetch(b + 1);
+        if (s < 0 || s >= p.nslots) continue;
+        if (p.slots && earlier_row_has(p.slots, b, s)) continue;
+        const float delta = p.softplus ? softplus<false>(x, nullptr) : x;
+        const float du = delta * u;
+        float acc = skip * u;
+#pragma unroll
+        for (int n = 0; n < NP; n++)
+            if (n < p.N) {
+                const float bn = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bl), n));
+                const float cn = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cl), n));
+                cur[n] = fmaf(__builtin_amdgcn_exp2f(delta * a2[n]), cur[n], du * bn);
+                acc = fmaf(cn, cur[n], acc);
+            }
+        if (p.z) acc *= z * sigmoid(z);
+        if (live) {
+            float* st = p.state + (int64_t)s * p.N * p.D + d;
+#pragma unroll
+            for (int n = 0; n < NP; n++)
+                if (n < p.N) st[(int64_t)n * p.D] = cur[n];
+            io<T>::st((T*)p.y + b * p.sy + d, acc);
+        }
+    }
 }
+
+// Rows per wave: one until there are 4096 waves, then up to 4 (256 rows x 4096, N = 16: 1 row 30.4 us, 2 29.4,
+// 4 30.1, 8 33.8, 16 46).
+int step_rows(int64_t B, int64_t cb) { return (int)std::min<int64_t>(4, std::max<int64_t>(1, B * cb / 4096)); }
 
 template <typename T, int NP>
 void step_np(const SsmArgs& a) {
-    const unsigned cb = (unsigned)((a.D + 63) / 64);
-    LA_TRACED(a.tr, "ssm_step",
-              ssm_step_kernel<T, NP><<<cb * (unsigned)a.B, 64, 0, a.stream>>>(
-                  (const T*)a.u, (const T*)a.dt, a.A, (const T*)a.Bm, (const T*)a.Cm, a.Dskip, (const T*)a.z, a.dt_bias,
-                  a.state, a.slots, (T*)a.y, a.su.batch, a.sdt.batch, a.sb.batch, a.sc.batch, a.sz.batch, a.sy.batch, a.D, cb,
-                  a.N, a.nslots, a.softplus));
+    StepDev p;
+    p.u = a.u; p.dt = a.dt; p.Bm = a.Bm; p.Cm = a.Cm; p.z = a.z; p.A = a.A; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
+    p.state = a.state; p.slots = a.slots; p.y = a.y;
+    p.su = a.su.batch; p.sdt = a.sdt.batch; p.sb = a.sb.batch; p.sc = a.sc.batch; p.sz = a.sz.batch; p.sy = a.sy.batch;
+    p.B = a.B; p.D = a.D; p.cb = (unsigned)((a.D + 63) / 64); p.N = a.N; p.nslots = a.nslots; p.softplus = a.softplus;
+    p.R = step_rows(a.B, p.cb);
+    const unsigned blocks = p.cb * (unsigned)((a.B + p.R - 1) / p.R);
+    if (a.N % 4 == 0 && (uintptr_t)a.A % 16 == 0)
+        LA_TRACED(a.tr, "ssm_step", ssm_step_kernel<T, NP, true><<<blocks, 64, 0, a.stream>>>(p));
+    else
+        LA_TRACED(a.tr, "ssm_step", ssm_step_kernel<T, NP, false><<<blocks, 64, 0, a.stream>>>(p));
 }
 template <typename T>
 hipError_t step_t(const SsmArgs& a) {

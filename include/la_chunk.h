@@ -382,7 +382,7 @@ la_status la_cumdecay(const float* decay, float* cumdecay, float* total, const l
  * _workspace call returns for the same shape), so calls that may overlap in time need separate
  * ones.  Calls may be captured into graphs; a graph keeps using the workspace it was captured with.
  *
- * Limits.  B <= 2^20, B * L <= 2^24 tokens, B * D <= 2^25, B * L * D <= 2^36 elements; the norm M <= 2^25
+ * Limits.  B <= 2^20, B * L <= 2^24 tokens, B * D <= 2^25, B * L * D <= 2^35 elements; the norm M <= 2^25
  * rows and M * D <= 2^34; beyond them LA_ERR_UNSUPPORTED.  A view's strides may span 2^42 elements
  * in all; beyond it LA_ERR_SHAPE.
  *
