@@ -131,6 +131,13 @@ struct WsCut {
 // A float array read through the scalar cache (uniform addresses, data that no launch in flight writes).
 typedef const __attribute__((address_space(4))) float* scalar_f32;
 __device__ __forceinline__ scalar_f32 as_scalar(const float* p) { return (scalar_f32)(uintptr_t)p; }
+// The same for an address that the compiler does not see to be uniform (one that depends on the wave's number).
+__device__ __forceinline__ scalar_f32 as_scalar_uniform(const float* p) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+    return (scalar_f32)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
 
 // A value that is the same in all lanes, moved to a scalar register.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -144,9 +151,8 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + __builtin_a
 // delta = log(1 + e^x) = max(x, 0) + log1p(y), y = e^-|x| in [0, 1].  Step sizes of 1e-3 are ordinary,
 // so log1p needs its relative accuracy near y = 0, which log2(1 + y) loses (2^-24 / y).  With
 // s = y / (2 + y) <= 1/3, log1p(y) = 2 atanh(s) = s P(s^2); the degree-4 P below was fitted at the
-// Chebyshev nodes of s^2 in [0, 1/9] and is within 8e-9 of it in fp32.  *d = d delta / d x = 1 / (1 + e^-x).
-template <bool DERIV>
-__device__ __forceinline__ float softplus(float x, float* d) {
+// Chebyshev nodes of s^2 in [0, 1/9] and is within 8e-9 of it in fp32.
+__device__ __forceinline__ float softplus(float x) {
     const float y = __builtin_amdgcn_exp2f(-fabsf(x) * LOG2E);
     const float s = y * rcp(2.f + y);
     const float v = s * s;
@@ -155,10 +161,6 @@ __device__ __forceinline__ float softplus(float x, float* d) {
     p = fmaf(p, v, 0x1.99dac0p-2f);
     p = fmaf(p, v, 0x1.5554e0p-1f);
     p = fmaf(p, v, 2.f);
-    if (DERIV) {
-        const float r = rcp(1.f + y);
-        *d = x >= 0.f ? r : y * r;
-    }
     return fmaf(s, p, fmaxf(x, 0.f));
 }
 

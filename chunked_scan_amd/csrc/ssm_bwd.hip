@@ -16,11 +16,12 @@
 //      then the adjoint walked back through them.
 //   4. sums: dB and dC over the channel blocks' partial sums, dA, dD and d dt_bias over the segments'.
 //
-// A lane owns a channel as in the forward, so the sums over channels cross lanes: 32 values a token (16
-// key dims of dB and of dC) over 64 lanes, by halving: every exchange adds two registers into one, and
-// after five of them each pair of lanes holds one value (about 70 instructions against 350 of the
-// recurrence).  The main pass takes 16 key dims at a time; with more, the sums over n that du, d delta and dz
-// need are carried in the workspace from one group of 16 to the next.
+// A lane owns a channel as in the forward.  The main pass needs a token's states again on the way back,
+// which costs registers: a workgroup is NP / 8 waves on the same 64 channels, 8 key dims each, so that the
+// 8 x 8 states of a tile fit beside the rest at three waves per SIMD.  What concerns a token and not a key dim (step
+// size, gate, the finished gradients) is computed by one of the waves per token and passed through LDS.
+// The sums over channels cross lanes: 16 values a token and wave (8 key dims of dB and of dC) over 64 lanes, by
+// halving: every exchange adds two registers into one (about 35 instructions against 170 of the recurrence).
 #include "la_mixer.h"
 #include "ssm_common.h"
 #include "ssm_tile.h"
@@ -28,9 +29,8 @@
 namespace la {
 namespace {
 
-constexpr int T = TT;      // tokens per tile: the states at their starts are kept
-constexpr int TH = T / 2;  // tokens whose states are recomputed into registers together
-constexpr int NC = 16;  // key dims per group
+constexpr int T = TT;  // tokens per tile: the states at their starts are kept
+constexpr int NW8 = 8;  // key dims per wave of the main pass
 
 struct BwdDev {
     const void* u;
@@ -48,10 +48,9 @@ struct BwdDev {
     float* sumdt;     // [B, G, D]
     float* kept;      // [B, nk, NP, D]: states from the segment's start, every T tokens
     float* keptdt;    // [B, nk, D]
-    float* acc;       // NP > 16: [3][B, L, D] sums over the groups so far
     float* dbc;       // [cb, B, L, 2 NP]
     float* dap;       // [B, G, NP, D]
-    float* ddp;       // [B, G, 2, D]: dD, d dt_bias
+    float* ddp;       // [B, G, NP / 8, 2, D]: dD, d dt_bias
     float* ds_in;
     void* du;
     void* ddt;
@@ -63,9 +62,36 @@ struct BwdDev {
     la_rows su, sdt, sz, sdy, sdu, sddt, sdz;
 };
 
-// Pass 1.  blockIdx.x: channel block fastest, then group of 16 key dims, segment, sequence.  Tiles as in the
+// The kernel's arguments, read again from memory where they are used: held over the token loops they would
+// push each other and the rows of B and C out of the scalar registers.
+typedef const __attribute__((address_space(4))) BwdDev* BwdArgsPtr;
+__device__ __forceinline__ BwdArgsPtr bwd_args() {
+    BwdArgsPtr q = (BwdArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(q));
+    return q;
+}
+
+// The same value, waited for here and unknown to the compiler from here on: the wait comes before the next
+// token's loads are issued and not after them, and exponentials of the way forwards are not held on to for the
+// way back, for which there are no registers.
+__device__ __forceinline__ float arrived(float x) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+v"(x));
+    __builtin_amdgcn_sched_barrier(0);
+    return x;
+}
+
+// The same for a value in a scalar register.
+__device__ __forceinline__ void arrived_row(float& x) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+s"(x));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Pass 1.  blockIdx.x: channel block fastest, then group of NC key dims, segment, sequence.  Tiles as in the
 // forward: tokens behind the segment's end have delta = ds = 0.
-template <typename E, bool VEC>
+// NC: key dims per group, 8 or 16.
+template <typename E, int NC, bool VEC>
 __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
     __shared__ __align__(16) E tile[4][T * 64];  // u, dt, dy, z
     const unsigned ngr = p.NP / NC;
@@ -90,24 +116,20 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
         adj[n] = 0.f;
     }
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
-    const bool gate = p.z;
-    const E* ub = (const E*)p.u + b * p.su.batch + d0;
-    const E* xb = (const E*)p.dt + b * p.sdt.batch + d0;
-    const E* yb = (const E*)p.dy + b * p.sdy.batch + d0;
-    const E* zb = gate ? (const E*)p.z + b * p.sz.batch + d0 : nullptr;
-    scalar_f32 row = as_scalar(p.bc + (b * p.L + t0) * (2 * p.NP) + nb);
+    const bool gate = p.z, sp = p.softplus;
+    const int NP = p.NP;
+    scalar_f32 rowp = as_scalar(p.bc + (b * p.L + t0) * (2 * NP) + nb);
 
     Raw8<E> raw[4];
     auto fetch = [&](int t) {
+        const BwdArgsPtr q = bwd_args();
         const int tt = min(t + pl.token, t1 - 1);
-        raw[0] = tile_load<E, VEC>(ub, p.su.token, tt, pl);
-        raw[1] = tile_load<E, VEC>(xb, p.sdt.token, tt, pl);
-        raw[2] = tile_load<E, VEC>(yb, p.sdy.token, tt, pl);
-        if (gate) raw[3] = tile_load<E, VEC>(zb, p.sz.token, tt, pl);
+        raw[0] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
+        raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
+        raw[2] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
+        if (gate) raw[3] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
     };
     float sum = 0.f;
-    float* kp = p.kept + ((b * p.nk + t0 / T) * p.NP + nb) * p.D + d;
-    float* kd = p.keptdt + (b * p.nk + t0 / T) * p.D + d;
     if (t0 < t1) fetch(t0);
     for (int t = t0; t < t1; t += T) {
         wave_lds_fence();
@@ -118,9 +140,9 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
         float dl[T], du[T], ds[T];
 #pragma unroll
         for (int j = 0; j < T; j++) dl[j] = (float)tile[1][j * 64 + lane] + bias;
-        if (p.softplus) {
+        if (sp) {
 #pragma unroll
-            for (int j = 0; j < T; j++) dl[j] = softplus<false>(dl[j], nullptr);
+            for (int j = 0; j < T; j++) dl[j] = softplus(dl[j]);
         }
 #pragma unroll
         for (int j = 0; j < T; j++) {
@@ -138,95 +160,79 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
         }
         if (t + T < t1) fetch(t + T);
         if (t > t0 && live) {
+            const BwdArgsPtr q = bwd_args();
+            const int64_t k = b * q->nk + t / T, D = q->D;
+            float* kp = q->kept + (k * NP + nb) * D + d0;
 #pragma unroll
-            for (int n = 0; n < NC; n++) kp[n * p.D] = h[n];
-            if (nb == 0) *kd = sum;
+            for (int n = 0; n < NC; n++) (kp + n * D)[lane] = h[n];
+            if (nb == 0) (q->keptdt + k * D + d0)[lane] = sum;
         }
-        kp += (int64_t)p.NP * p.D;
-        kd += p.D;
+        // rows of B and C, one token ahead of their use
+        float row[2][2 * NC];
+        auto load_row = [&](int j) {
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                row[j & 1][n] = rowp[n];
+                row[j & 1][NC + n] = rowp[NP + n];
+            }
+            rowp += t + j + 1 < t1 ? 2 * NP : 0;
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        load_row(0);
 #pragma unroll
         for (int j = 0; j < T; j++) {
+            arrived_row(row[j & 1][0]);
+            if (j + 1 < T) load_row(j + 1);
+            const float* rw = row[j & 1];
 #pragma unroll
             for (int n = 0; n < NC; n++) {
                 const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
-                h[n] = fmaf(a, h[n], du[j] * row[n]);
+                h[n] = fmaf(a, h[n], du[j] * rw[n]);
                 q[n] *= a;
-                adj[n] = fmaf(q[n], ds[j] * row[p.NP + n], adj[n]);
+                adj[n] = fmaf(q[n], ds[j] * rw[NC + n], adj[n]);
             }
             sum += dl[j];
-            row += t + j + 1 < t1 ? 2 * p.NP : 0;
         }
     }
     if (!live) return;
+    const BwdArgsPtr e = bwd_args();
+    const int64_t D = e->D, seg = b * e->G + g;
 #pragma unroll
     for (int n = 0; n < NC; n++) {
-        if (g + 1 < p.G) p.hin[((b * p.G + g + 1) * p.NP + nb + n) * p.D + d] = h[n];
-        p.gout[((b * p.G + g) * p.NP + nb + n) * p.D + d] = adj[n];
+        if (g + 1 < e->G) (e->hin + ((seg + 1) * NP + nb + n) * D + d0)[lane] = h[n];
+        (e->gout + (seg * NP + nb + n) * D + d0)[lane] = adj[n];
     }
-    if (nb == 0) p.sumdt[(b * p.G + g) * p.D + d] = sum;
+    if (nb == 0) (e->sumdt + seg * D + d0)[lane] = sum;
 }
 
-// Pass 2.  A thread owns one (b, n, d): states forwards, adjoints backwards.  hin[0] takes s_in and
-// hin[g] the state entering segment g; gout[g] becomes the adjoint at segment g's end.
-constexpr int PB = 32;
-__global__ __launch_bounds__(256) void ssm_bwd_segments_kernel(const float* __restrict__ a2, const float* __restrict__ s_in,
-                                                               const float* __restrict__ ds_out,
-                                                               const float* __restrict__ sumdt, float* __restrict__ hin,
-                                                               float* __restrict__ gout, int64_t total, int64_t D, int N,
+// Pass 2, per (b, n, d): states forwards (blockIdx.y = 0), adjoints backwards.  hin[0] takes s_in and hin[g]
+// the state entering segment g; gout[g] becomes the adjoint at segment g's end.
+template <int PARTS>
+__global__ __launch_bounds__(64 * PARTS) void ssm_bwd_segments_kernel(const float* __restrict__ a2, const float* __restrict__ s_in,
+                                                               const float* __restrict__ ds_out, const float* sumdt,
+                                                               float* hin, float* gout, int64_t total, int64_t D, int N,
                                                                int NP, int G) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
+    const int64_t i0 = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const bool on = i0 < total;
+    const int64_t i = on ? i0 : 0;
     const int64_t d = i % D, n = i / D % NP, b = i / (D * NP);
-    const bool on = n < N;
-    const int64_t io = (b * N + n) * D + d;
+    const int64_t io = (b * N + n) * D + d, ps = (int64_t)NP * D;
     const float rate = a2[n * D + d];
-    const int64_t ps = (int64_t)NP * D;
     const float* sp = sumdt + b * G * D + d;
     if (blockIdx.y == 0) {
-        float h = on && s_in ? s_in[io] : 0.f;
+        const float x0 = n < N && s_in ? s_in[io] : 0.f;
         float* pp = hin + (b * G * NP + n) * D + d;
-        pp[0] = h;
-        for (int g0 = 1; g0 < G; g0 += PB) {
-            float v[PB], s[PB];
-#pragma unroll
-            for (int j = 0; j < PB; j++) {
-                const int g = min(g0 + j, G - 1);
-                v[j] = pp[g * ps];
-                s[j] = sp[(g - 1) * D];
-            }
-#pragma unroll
-            for (int j = 0; j < PB; j++)
-                if (g0 + j < G) {
-                    h = fmaf(__builtin_amdgcn_exp2f(rate * s[j]), h, v[j]);
-                    pp[(g0 + j) * ps] = h;
-                }
-        }
+        if (on && threadIdx.x < 64) pp[0] = x0;
+        segment_chain<PARTS>(
+            G - 1, x0, rate, on, [&](int k) { return pp + (k + 1) * ps; }, [&](int k) { return sp + k * D; },
+            [&](int k, float, float next) { pp[(k + 1) * ps] = next; });
     } else {
-        float x = on && ds_out ? ds_out[io] : 0.f;
+        const float x0 = n < N && ds_out ? ds_out[io] : 0.f;
         float* pp = gout + (b * G * NP + n) * D + d;
-        for (int g0 = G - 1; g0 >= 0; g0 -= PB) {
-            float v[PB], s[PB];
-#pragma unroll
-            for (int j = 0; j < PB; j++) {
-                const int g = max(g0 - j, 0);
-                v[j] = pp[g * ps];
-                s[j] = sp[g * D];
-            }
-#pragma unroll
-            for (int j = 0; j < PB; j++)
-                if (g0 - j >= 0) {
-                    pp[(g0 - j) * ps] = x;
-                    x = fmaf(__builtin_amdgcn_exp2f(rate * s[j]), x, v[j]);
-                }
-        }
+        segment_chain<PARTS>(
+            G, x0, rate, on, [&](int k) { return pp + (G - 1 - k) * ps; }, [&](int k) { return sp + (G - 1 - k) * D; },
+            [&](int k, float cur, float) { pp[(G - 1 - k) * ps] = cur; });
     }
-}
-
-// The same value, unknown to the compiler: keeps it from holding on to exponentials of one phase for the next,
-// for which there are no registers.
-__device__ __forceinline__ float opaque(float x) {
-    asm("" : "+v"(x));
-    return x;
 }
 
 template <int CTRL>
@@ -260,230 +266,235 @@ __device__ __forceinline__ float wave_sums16(float* v) {
     return s + dpp<0xb1>(s);            // quad_perm [1, 0, 3, 2]
 }
 
-// Pass 3.  blockIdx.x: channel block fastest, then segment, sequence.  MULTI: more than one group of 16 key dims.
-// A wave per segment and channel block, at most 256 registers (two waves per SIMD): the T states of 16 key
-// dims take 128 of them, so what is used once per token waits in LDS.
-template <typename E, bool MULTI, bool VEC>
-__global__ __launch_bounds__(64, 2) void ssm_bwd_main_kernel(BwdDev p) {
-    __shared__ __align__(16) E tile[4][T * 64];  // u; dt, then d dt; dy, then du; z, then dz
-    __shared__ float slope[T * 64];              // d delta / d dt
-    __shared__ float hin[NC * 64], h0[NC * 64];  // the states entering the segment and the tile
+// Pass 3.  A workgroup of NP / 8 waves per channel block (fastest), segment and sequence.  ONE: a single wave.
+// Per tile, from the segment's last: the inputs to LDS | per token (shared out over the waves): step size
+// and gate | every wave: forwards to its states, backwards through them, its share of the sums over key dims
+// to LDS | per token: the finished gradients.  The bars are workgroup barriers.
+template <typename E, bool VEC, bool ONE>
+__global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev p) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int NC = NW8, SLOT = T * 64;
+    E* const rawt = reinterpret_cast<E*>(lds);  // [2][4][SLOT], alternating: u; dt, then d dt; dy, then du; z, then dz
+    float* const dls = reinterpret_cast<float*>(lds + 2 * 4 * SLOT * sizeof(E));  // [SLOT] each:
+    float* const dus = dls + SLOT;    // delta u
+    float* const dss = dus + SLOT;    // ds
+    float* const sums = dss + SLOT;  // [waves][3][SLOT]: sum G B, sum G W A, sum C S
+    const int nw = ONE ? 1 : p.NP / NC;
+    const bool sp = p.softplus;
+    const int w = ONE ? 0 : uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const unsigned r = blockIdx.x / p.cb;
     const unsigned cbi = blockIdx.x % p.cb;
     const int64_t d0 = (int64_t)cbi * 64;
     const int g = (int)(r % p.G);
     const int64_t b = r / p.G;
-    const int lane = threadIdx.x;
     const bool live = d0 + lane < p.D;
-    const int64_t d = live ? d0 + lane : p.D - 1;
+    const int ln = live ? lane : (int)(p.D - 1 - d0);  // lanes behind the last channel repeat it
+    const int64_t d = d0 + ln;
     const TilePlace pl(d0, p.D);
     const int len = uniform((int)seq_len(p.lengths, b, p.L));
     const int t0 = (int)(g * p.seglen), te = (int)min(t0 + p.seglen, p.L), t1 = min(te, len);
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     const float skip = p.Dskip ? p.Dskip[d] : 0.f;
     const bool gate = p.z;
-    const E* ub = (const E*)p.u + b * p.su.batch + d0;
-    const E* xb = (const E*)p.dt + b * p.sdt.batch + d0;
-    const E* yb = (const E*)p.dy + b * p.sdy.batch + d0;
-    const E* zb = gate ? (const E*)p.z + b * p.sz.batch + d0 : nullptr;
-    E* dub = (E*)p.du + b * p.sdu.batch + d0;
-    E* dxb = (E*)p.ddt + b * p.sddt.batch + d0;
-    E* dzb = gate ? (E*)p.dz + b * p.sdz.batch + d0 : nullptr;
 
     if (pl.in) {  // gradients behind the sequence's end
         const Raw8<E> zero = {};
-        for (int t = max(t0, len) + pl.token; t < te; t += T) {
-            store8<VEC>(dub + t * p.sdu.token + pl.col, pl.n, zero);
-            store8<VEC>(dxb + t * p.sddt.token + pl.col, pl.n, zero);
-            if (gate) store8<VEC>(dzb + t * p.sdz.token + pl.col, pl.n, zero);
+        for (int t = max(t0, len) + w * T + pl.token; t < te; t += nw * T) {
+            store8<VEC>((E*)p.du + b * p.sdu.batch + d0 + t * p.sdu.token + pl.col, pl.n, zero);
+            store8<VEC>((E*)p.ddt + b * p.sddt.batch + d0 + t * p.sddt.token + pl.col, pl.n, zero);
+            if (gate) store8<VEC>((E*)p.dz + b * p.sdz.batch + d0 + t * p.sdz.token + pl.col, pl.n, zero);
         }
     }
 
-    const int64_t plane = p.B * p.L * p.D;
+    const int nb = w * NC;
+    const int64_t sg = ((b * p.G + g) * p.NP + nb) * p.D + d0;
+    float A2[NC], adj[NC], dA[NC], kept[NC], hin[NC], keptdt = 0.f;
+#pragma unroll
+    for (int n = 0; n < NC; n++) {
+        A2[n] = (p.a2 + (nb + n) * p.D + d0)[ln];
+        adj[n] = (p.gout + sg + n * p.D)[ln];
+        hin[n] = (p.hin + sg + n * p.D)[ln];
+        dA[n] = 0.f;
+        kept[n] = 0.f;
+    }
+    // a wave loads the activations w, w + nw, .. of u, dt, dy, z
+    Raw8<E> raw[ONE ? 4 : 2];
+    auto fetch = [&](int t) {
+        const BwdArgsPtr q = bwd_args();
+        const int tt = min(t + pl.token, t1 - 1);
+#pragma unroll
+        for (int k = 0; k < (ONE ? 4 : 2); k++) {
+            const int i = w + k * nw;
+            if (i == 0) raw[k] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
+            if (i == 1) raw[k] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
+            if (i == 2) raw[k] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
+            if (i == 3 && gate) raw[k] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
+        }
+    };
+    auto fetch_kept = [&](int t) {
+        if (t <= t0) {
+#pragma unroll
+            for (int n = 0; n < NC; n++) kept[n] = 0.f;
+            keptdt = 0.f;
+            return;
+        }
+        const BwdArgsPtr q = bwd_args();
+        const int64_t kk = b * q->nk + t / T, D = q->D;
+        const float* kp = q->kept + (kk * q->NP + nb) * D + d0;
+#pragma unroll
+        for (int n = 0; n < NC; n++) kept[n] = (kp + n * D)[ln];
+        keptdt = (q->keptdt + kk * D + d0)[ln];
+    };
+    auto barrier = [&]() {
+        if (ONE) wave_lds_fence();
+        else lds_barrier();
+    };
+    const int NP = nw * NC;
+    scalar_f32 bcb = as_scalar_uniform(p.bc + b * p.L * (2 * NP) + nb);
+    // where lane 4 i of the wave adds the i-th of its 16 sums over channels
+    float* const dbcb = p.dbc + (cbi * p.B + b) * p.L * (2 * NP) + nb;
+    const int dbco = (lane >> 2) < NC ? lane >> 2 : NP + (lane >> 2) - NC;
     float dDsum = 0.f, dbsum = 0.f;
-    const int groups = MULTI ? p.NP / NC : 1;
-    for (int gr = 0; gr < groups; gr++) {
-        const int nb = gr * NC;
-        const bool first = gr == 0, last = gr == groups - 1;
-        float A2[NC], adj[NC], dA[NC], kept[NC], keptdt = 0.f;
-        const int64_t sg = ((b * p.G + g) * p.NP + nb) * p.D + d;
+    const int tl = t0 + (t1 - 1 - t0) / T * T;  // the segment's last tile
+    int par = 0;
+    if (t0 < t1) {
+        fetch(tl);
+        fetch_kept(tl);
+    }
+    for (int t = tl; t >= t0 && t0 < t1; t -= T, par ^= 1) {
+        E* const tile = rawt + par * 4 * SLOT;
+#pragma unroll
+        for (int k = 0; k < (ONE ? 4 : 2); k++) {
+            const int i = w + k * nw;
+            if (i < 3 || (i == 3 && gate)) *lds_chunk(tile + i * SLOT, pl) = raw[k];
+        }
+        barrier();
+        for (int j = w; j < T; j += nw) {
+            const int at = j * 64 + lane;
+            float dl = (float)tile[SLOT + at] + bias;
+            if (sp) dl = softplus(dl);
+            float ds = (float)tile[2 * SLOT + at];
+            if (gate) {
+                const float z = (float)tile[3 * SLOT + at];
+                ds *= z * sigmoid(z);
+            }
+            const bool in = t + j < t1 && live;  // the others change no state and add nothing to a sum
+            dl = in ? dl : 0.f;
+            dls[at] = dl;
+            dus[at] = dl * (float)tile[at];
+            dss[at] = in ? ds : 0.f;
+        }
+        barrier();
+        // the state entering the tile, then the tile's states
+        float hs[T][NC], h[NC];
+#pragma unroll
+        for (int n = 0; n < NC; n++) h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * keptdt), hin[n], kept[n]);
+        if (t > t0) {
+            fetch(t - T);
+            fetch_kept(t - T);
+        }
+        // a token's row of B and C and its step size, one token ahead of their use (the fences keep the loads
+        // from sinking to it)
+        float row[2][2 * NC], dl_[2], du_[2], ds_[2];
+        auto load_token = [&](int j, bool back) {
+            scalar_f32 q = bcb + min(t + j, t1 - 1) * (2 * NP);
+            const int k = j & 1;
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                row[k][n] = q[n];
+                row[k][NC + n] = q[NP + n];
+            }
+            dl_[k] = dls[j * 64 + lane];
+            du_[k] = dus[j * 64 + lane];
+            if (back) ds_[k] = dss[j * 64 + lane];
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        load_token(0, false);
+#pragma unroll
+        for (int j = 0; j < T; j++) {
+            const float dl = arrived(dl_[j & 1]), du = du_[j & 1];
+            if (j + 1 < T) load_token(j + 1, j + 2 == T);
+            const float* rw = row[j & 1];
+            float inner = 0.f;
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                h[n] = fmaf(__builtin_amdgcn_exp2f(dl * A2[n]), h[n], du * rw[n]);
+                hs[j][n] = h[n];
+                inner = fmaf(rw[NC + n], h[n], inner);
+            }
+            if (gate) sums[(w * 3 + 2) * SLOT + j * 64 + lane] = inner;
+        }
+        // and back through them
+#pragma unroll
+        for (int j = T - 1; j >= 0; j--) {
+            const float* rw = row[j & 1];
+            const float dl = arrived(dl_[j & 1]), du = du_[j & 1], ds = ds_[j & 1];
+            if (j > 0) load_token(j - 1, true);
+            float s1 = 0.f, s2 = 0.f, v[2 * NC];
+#pragma unroll
+            for (int n = 0; n < NC; n++) {
+                const float gn = fmaf(ds, rw[NC + n], adj[n]);
+                const float gw = gn * fmaf(-du, rw[n], hs[j][n]);
+                s1 = fmaf(gn, rw[n], s1);
+                s2 = fmaf(gw, A2[n], s2);
+                dA[n] = fmaf(gw, dl, dA[n]);
+                v[n] = gn * du;
+                v[NC + n] = ds * hs[j][n];
+                adj[n] = gn * __builtin_amdgcn_exp2f(dl * A2[n]);
+            }
+            sums[(w * 3) * SLOT + j * 64 + lane] = s1;
+            sums[(w * 3 + 1) * SLOT + j * 64 + lane] = s2;
+            const float s = wave_sums16(v);
+            if (t + j < t1 && (lane & 3) == 0) (dbcb + (int64_t)(t + j) * (2 * NP))[dbco] = s;
+        }
+        barrier();
+        for (int j = w; j < T; j += nw) {
+            const int at = j * 64 + lane;
+            float s1 = 0.f, s2 = 0.f, inner = 0.f;
+            for (int k = 0; k < nw; k++) {
+                s1 += sums[(k * 3) * SLOT + at];
+                s2 += sums[(k * 3 + 1) * SLOT + at];
+                if (gate) inner += sums[(k * 3 + 2) * SLOT + at];
+            }
+            const float u = (float)tile[at], dl = dls[at], ds = dss[at];
+            float dd = t + j < t1 && live ? fmaf(u, s1, s2 * LN2) : 0.f;
+            if (sp) dd *= sigmoid((float)tile[SLOT + at] + bias);  // d delta / d dt
+            if (gate) {
+                const float z = (float)tile[3 * SLOT + at], sz = sigmoid(z), dyv = (float)tile[2 * SLOT + at];
+                io<E>::st(tile + 3 * SLOT + at, dyv * fmaf(skip, u, inner) * sz * fmaf(z, 1.f - sz, 1.f));
+            }
+            io<E>::st(tile + 2 * SLOT + at, fmaf(ds, skip, dl * s1));
+            io<E>::st(tile + SLOT + at, dd);
+            dDsum = fmaf(ds, u, dDsum);
+            dbsum += dd;
+        }
         wave_lds_fence();
-#pragma unroll
-        for (int n = 0; n < NC; n++) {
-            A2[n] = p.a2[(nb + n) * p.D + d];
-            adj[n] = p.gout[sg + n * p.D];
-            hin[n * 64 + lane] = p.hin[sg + n * p.D];
-            dA[n] = 0.f;
-            kept[n] = 0.f;
+        const int tt = t + pl.token;
+        if (pl.in && tt < t1 && (ONE || pl.token % nw == w)) {  // the wave's own tokens
+            const BwdArgsPtr q = bwd_args();
+            store8<VEC>((E*)q->du + b * q->sdu.batch + d0 + tt * q->sdu.token + pl.col, pl.n, *lds_chunk(tile + 2 * SLOT, pl));
+            store8<VEC>((E*)q->ddt + b * q->sddt.batch + d0 + tt * q->sddt.token + pl.col, pl.n, *lds_chunk(tile + SLOT, pl));
+            if (gate)
+                store8<VEC>((E*)q->dz + b * q->sdz.batch + d0 + tt * q->sdz.token + pl.col, pl.n, *lds_chunk(tile + 3 * SLOT, pl));
         }
-        Raw8<E> raw[4];
-        auto fetch = [&](int t) {
-            const int tt = min(t + pl.token, t1 - 1);
-            raw[0] = tile_load<E, VEC>(ub, p.su.token, tt, pl);
-            raw[1] = tile_load<E, VEC>(xb, p.sdt.token, tt, pl);
-            raw[2] = tile_load<E, VEC>(yb, p.sdy.token, tt, pl);
-            if (gate) raw[3] = tile_load<E, VEC>(zb, p.sz.token, tt, pl);
-        };
-        auto fetch_kept = [&](int t) {
-            const int64_t kk = b * p.nk + t / T;
-#pragma unroll
-            for (int n = 0; n < NC; n++) kept[n] = t > t0 ? p.kept[(kk * p.NP + nb + n) * p.D + d] : 0.f;
-            keptdt = t > t0 ? p.keptdt[kk * p.D + d] : 0.f;
-        };
-        scalar_f32 bcb = as_scalar(p.bc + b * p.L * (2 * p.NP) + nb);
-        const int tl = t0 + (t1 - 1 - t0) / T * T;  // the segment's last tile
-        if (t0 < t1) {
-            fetch(tl);
-            fetch_kept(tl);
-        }
-        for (int t = tl; t >= t0 && t0 < t1; t -= T) {
-            wave_lds_fence();
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                if (i < 3 || gate) *lds_chunk(tile[i], pl) = raw[i];
-            wave_lds_fence();
-            float dl[T], ds[T], hs[TH][NC], h[NC];
-#pragma unroll
-            for (int j = 0; j < T; j++) dl[j] = (float)tile[1][j * 64 + lane] + bias;
-            if (p.softplus) {
-#pragma unroll
-                for (int j = 0; j < T; j++) {
-                    float sl;
-                    dl[j] = softplus<true>(dl[j], &sl);
-                    slope[j * 64 + lane] = sl;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < T; j++) slope[j * 64 + lane] = 1.f;
-            }
-#pragma unroll
-            for (int j = 0; j < T; j++) {
-                const bool in = t + j < t1 && live;  // the others change no state and add nothing to a sum
-                dl[j] = in ? dl[j] : 0.f;
-                ds[j] = in ? (float)tile[2][j * 64 + lane] : 0.f;
-            }
-            // the state entering the tile
-#pragma unroll
-            for (int n = 0; n < NC; n++) {
-                h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * keptdt), hin[n * 64 + lane], kept[n]);
-                h0[n * 64 + lane] = h[n];
-            }
-            // the tile's halves from the end: forwards to the half's states, then backwards through them
-#pragma unroll
-            for (int j0 = T - TH; j0 >= 0; j0 -= TH) {
-#pragma unroll
-                for (int j = 0; j < j0; j++) {
-                    const float du = dl[j] * (float)tile[0][j * 64 + lane];
-                    scalar_f32 row = bcb + min(t + j, t1 - 1) * (2 * p.NP);
-                    const float dlj = opaque(dl[j]);
-#pragma unroll
-                    for (int n = 0; n < NC; n++) h[n] = fmaf(__builtin_amdgcn_exp2f(dlj * A2[n]), h[n], du * row[n]);
-                }
-                if (j0 == 0) {
-#pragma unroll
-                    for (int n = 0; n < NC; n++) h[n] = h0[n * 64 + lane];
-                }
-#pragma unroll
-                for (int k = 0; k < TH; k++) {
-                    const int j = j0 + k;
-                    const float u = (float)tile[0][j * 64 + lane], du = dl[j] * u;
-                    scalar_f32 row = bcb + min(t + j, t1 - 1) * (2 * p.NP);
-                    float inner = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NC; n++) {
-                        h[n] = fmaf(__builtin_amdgcn_exp2f(dl[j] * A2[n]), h[n], du * row[n]);
-                        hs[k][n] = h[n];
-                        inner = fmaf(row[p.NP + n], h[n], inner);
-                    }
-                    if (gate) {
-                        const float z = (float)tile[3][j * 64 + lane], sz = sigmoid(z), dyv = ds[j];
-                        ds[j] *= z * sz;
-                        if (MULTI) {
-                            float* ap = p.acc + 2 * plane + (b * p.L + min(t + j, t1 - 1)) * p.D + d;
-                            if (!first) inner += *ap;
-                            if (!last && live && t + j < t1) *ap = inner;
-                        }
-                        if (last)
-                            io<E>::st(tile[3] + j * 64 + lane, dyv * fmaf(skip, u, inner) * sz * fmaf(z, 1.f - sz, 1.f));
-                    }
-                }
-                if (j0 == 0 && t > t0) {
-                    fetch(t - T);
-                    fetch_kept(t - T);
-                }
-#pragma unroll
-                for (int k = TH - 1; k >= 0; k--) {
-                    const int j = j0 + k;
-                    const int tt = min(t + j, t1 - 1);
-                    scalar_f32 row = bcb + tt * (2 * p.NP);
-                    const float u = (float)tile[0][j * 64 + lane];
-                    const float du = dl[j] * u;
-                    const float dlj = opaque(dl[j]);
-                    float s1 = 0.f, s2 = 0.f, v[NC];
-#pragma unroll
-                    for (int n = 0; n < NC; n++) v[n] = ds[j] * hs[k][n];
-                    const float sc = wave_sums16(v);
-#pragma unroll
-                    for (int n = 0; n < NC; n++) {
-                        const float gn = fmaf(ds[j], row[p.NP + n], adj[n]);
-                        const float gw = gn * fmaf(-du, row[n], hs[k][n]);
-                        s1 = fmaf(gn, row[n], s1);
-                        s2 = fmaf(gw, A2[n], s2);
-                        dA[n] = fmaf(gw, dl[j], dA[n]);
-                        v[n] = gn * du;
-                        adj[n] = gn * __builtin_amdgcn_exp2f(dlj * A2[n]);
-                    }
-                    const float sb = wave_sums16(v);
-                    // lanes 4 i and 4 i + 1 write the sums of dB and dC of key dim i
-                    if (t + j < t1 && (lane & 2) == 0)
-                        p.dbc[((cbi * p.B + b) * p.L + tt) * (2 * p.NP) + nb + (lane >> 2) + (lane & 1) * p.NP] =
-                            lane & 1 ? sc : sb;
-                    if (MULTI) {
-                        float* ap = p.acc + (b * p.L + tt) * p.D + d;
-                        if (!first) {
-                            s1 += ap[0];
-                            s2 += ap[plane];
-                        }
-                        if (!last && live && t + j < t1) {
-                            ap[0] = s1;
-                            ap[plane] = s2;
-                        }
-                    }
-                    if (last) {
-                        const float dd = t + j < t1 && live ? fmaf(u, s1, s2 * LN2) * slope[j * 64 + lane] : 0.f;
-                        io<E>::st(tile[2] + j * 64 + lane, fmaf(ds[j], skip, dl[j] * s1));
-                        io<E>::st(tile[1] + j * 64 + lane, dd);
-                        dDsum = fmaf(ds[j], u, dDsum);
-                        dbsum += dd;
-                    }
-                }
-            }
-            if (last) {
-                wave_lds_fence();
-                const int tt = t + pl.token;
-                if (pl.in && tt < t1) {
-                    store8<VEC>(dub + tt * p.sdu.token + pl.col, pl.n, *lds_chunk(tile[2], pl));
-                    store8<VEC>(dxb + tt * p.sddt.token + pl.col, pl.n, *lds_chunk(tile[1], pl));
-                    if (gate) store8<VEC>(dzb + tt * p.sdz.token + pl.col, pl.n, *lds_chunk(tile[3], pl));
-                }
-            }
-        }
-        if (live) {
-#pragma unroll
-            for (int n = 0; n < NC; n++) {
-                p.dap[sg + n * p.D] = dA[n];
-                if (g == 0 && p.ds_in && nb + n < p.N) p.ds_in[(b * p.N + nb + n) * p.D + d] = adj[n];
-            }
-        }
+        if (ONE) wave_lds_fence();
     }
-    if (live) {
-        p.ddp[((b * p.G + g) * 2) * p.D + d] = dDsum;
-        p.ddp[((b * p.G + g) * 2 + 1) * p.D + d] = dbsum;
+    if (!live) return;
+    const BwdArgsPtr e = bwd_args();
+    const int64_t D = e->D, seg = b * e->G + g;
+    const int N = e->N;
+#pragma unroll
+    for (int n = 0; n < NC; n++) {
+        (e->dap + (seg * NP + nb + n) * D + d0)[lane] = dA[n];
+        if (g == 0 && e->ds_in && nb + n < N) (e->ds_in + (b * N + nb + n) * D + d0)[lane] = adj[n];
     }
+    float* dd = e->ddp + ((seg * nw + w) * 2) * D + d0;
+    dd[lane] = dDsum;
+    (dd + D)[lane] = dbsum;
 }
 
 // Pass 4.  The first `nbc` blocks: dB and dC, a thread per (b, t, n) of each; the others: dA, dD and
-// d dt_bias, a thread per (n or one of the two, d).
+// d dt_bias, 16 channels of one n (or of one of the two) per block, 16 threads to a channel.
 template <typename E>
 __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restrict__ dbc, const float* __restrict__ dap,
                                                            const float* __restrict__ ddp, const int32_t* lengths,
@@ -511,15 +522,25 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
             io<E>::st(dC + b * sdc.batch + t * sdc.token + n, s);
         return;
     }
-    const int64_t i = (int64_t)(blockIdx.x - nbc) * 256 + threadIdx.x;
-    const int64_t n = i / D, d = i % D;
-    if (n >= N + 2) return;
+    __shared__ float part[16][17];
+    const int64_t blocks = (D + 15) / 16, k = blockIdx.x - nbc;
+    const int64_t n = k / blocks;
+    const int dl = threadIdx.x & 15, share = threadIdx.x >> 4;
+    const int64_t d = k % blocks * 16 + dl;
     const bool isA = n < N;
-    const float* src = isA ? dap + n * D + d : ddp + (n - N) * D + d;
-    const int64_t step = isA ? (int64_t)NP * D : 2 * D;
+    const int64_t step = isA ? (int64_t)NP * D : 2 * D, rows = isA ? B * G : B * G * (NP / NW8);
     float s = 0.f;
-#pragma unroll 8
-    for (int64_t k = 0; k < B * G; k++) s += src[k * step];
+    if (d < D) {
+        const float* src = isA ? dap + n * D + d : ddp + (n - N) * D + d;
+#pragma unroll 4
+        for (int64_t r = share; r < rows; r += 16) s += src[r * step];
+    }
+    part[share][dl] = s;
+    __syncthreads();
+    if (share != 0 || d >= D) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i++) s += part[i][dl];
     if (isA)
         dA[d * N + n] = s;
     else if (n == N) {
@@ -528,13 +549,15 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
         dbias[d] = s;
 }
 
-int np_for(int N) { return (N + NC - 1) / NC * NC; }
+int np_for(int N) { return (N + NW8 - 1) / NW8 * NW8; }
 
-// Segments: about 2048 waves in the main pass, none under 16 tokens.
-SsmPlan bwd_plan(int64_t B, int64_t L, int64_t D) { return ssm_plan(B, L, D, 2048, 16, T); }
+// Segments: about 6144 waves in the main pass (NP / 8 to a channel block), two rounds of what fits the device
+// at once, none under 16 tokens.  2 x 4096 tokens x 2048 channels, N = 16, main and first pass: 3072 waves 302 +
+// 143 us, 6144 304 + 104, 9216 299 + 98 (and 4 us more in the sums over segments).
+SsmPlan bwd_plan(int64_t B, int64_t L, int64_t D, int NP) { return ssm_plan(B, L, D, 6144 / (NP / NW8), 16, T); }
 
 struct BwdWs {
-    float *bc, *a2, *hin, *gout, *sumdt, *kept, *keptdt, *acc, *dbc, *dap, *ddp;
+    float *bc, *a2, *hin, *gout, *sumdt, *kept, *keptdt, *dbc, *dap, *ddp;
     int64_t nk;
     size_t bytes;
 };
@@ -551,23 +574,22 @@ BwdWs bwd_cut(void* base, int64_t B, int64_t L, int64_t D, int N, int G) {
     w.sumdt = c.take(seg);
     w.kept = c.take((size_t)(B * w.nk) * NP * D);
     w.keptdt = c.take((size_t)(B * w.nk) * D);
-    w.acc = NP > NC ? c.take(tok * D * 3) : nullptr;
     w.dbc = c.take(tok * 2 * NP * ((D + 63) / 64));
     w.dap = c.take(seg * NP);
-    w.ddp = c.take(seg * 2);
+    w.ddp = c.take(seg * 2 * (NP / NW8));
     w.bytes = c.used;
     return w;
 }
 
 template <typename E>
 hipError_t launch_e(const SsmArgs& a) {
-    const SsmPlan pl = bwd_plan(a.B, a.L, a.D);
+    const SsmPlan pl = bwd_plan(a.B, a.L, a.D, np_for(a.N));
     const BwdWs w = bwd_cut(a.ws, a.B, a.L, a.D, a.N, pl.G);
     BwdDev p;
     p.u = a.u; p.dt = a.dt; p.z = a.z; p.dy = a.dy; p.a2 = w.a2; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
     p.ds_out = a.ds_out; p.lengths = a.lengths;
     p.bc = w.bc; p.hin = w.hin; p.gout = w.gout; p.sumdt = w.sumdt; p.kept = w.kept; p.keptdt = w.keptdt;
-    p.acc = w.acc; p.dbc = w.dbc; p.dap = w.dap; p.ddp = w.ddp;
+    p.dbc = w.dbc; p.dap = w.dap; p.ddp = w.ddp;
     p.ds_in = a.ds_in; p.du = a.du; p.ddt = a.ddt; p.dz = a.dz;
     p.B = a.B; p.L = a.L; p.D = a.D; p.seglen = pl.seglen; p.nk = w.nk;
     p.N = a.N; p.NP = np_for(a.N); p.G = pl.G;
@@ -581,27 +603,40 @@ hipError_t launch_e(const SsmArgs& a) {
         const bool vec = a.D % 8 == 0 && rows16(a.u, a.su, es) && rows16(a.dt, a.sdt, es) && rows16(a.z, a.sz, es) &&
                          rows16(a.dy, a.sdy, es) && rows16(a.du, a.sdu, es) && rows16(a.ddt, a.sddt, es) &&
                          rows16(a.dz, a.sdz, es);
-        if (vec)
-            LA_TRACED(a.tr, "ssm_bwd_states", ssm_bwd_states_kernel<E, true><<<blocks * (p.NP / NC), 64, 0, a.stream>>>(p));
-        else
-            LA_TRACED(a.tr, "ssm_bwd_states", ssm_bwd_states_kernel<E, false><<<blocks * (p.NP / NC), 64, 0, a.stream>>>(p));
-        const int64_t total = a.B * p.NP * a.D;
-        LA_TRACED(a.tr, "ssm_bwd_segments",
-                  ssm_bwd_segments_kernel<<<dim3((unsigned)((total + 255) / 256), 2), 256, 0, a.stream>>>(
-                      w.a2, a.s_in, a.ds_out, w.sumdt, w.hin, w.gout, total, a.D, a.N, p.NP, pl.G));
-#define LA_SSM_MAIN(M, V) \
-    LA_TRACED(a.tr, "ssm_bwd_main", ssm_bwd_main_kernel<E, M, V><<<blocks, 64, 0, a.stream>>>(p))
-        if (p.NP > NC) {
-            if (vec) LA_SSM_MAIN(true, true);
-            else LA_SSM_MAIN(true, false);
+#define LA_SSM_STATES(n, V)                                                                                    \
+    LA_TRACED(a.tr, "ssm_bwd_states",                                                                          \
+              ssm_bwd_states_kernel<E, n, V><<<blocks * (unsigned)(p.NP / n), 64, 0, a.stream>>>(p))
+        if (p.NP % 16) {
+            if (vec) LA_SSM_STATES(8, true);
+            else LA_SSM_STATES(8, false);
         } else {
-            if (vec) LA_SSM_MAIN(false, true);
+            if (vec) LA_SSM_STATES(16, true);
+            else LA_SSM_STATES(16, false);
+        }
+#undef LA_SSM_STATES
+        const int64_t total = a.B * p.NP * a.D;
+        const dim3 grid((unsigned)((total + 63) / 64), 2);
+#define LA_SSM_SEGMENTS(n)                                                                                       \
+    LA_TRACED(a.tr, "ssm_bwd_segments", ssm_bwd_segments_kernel<n><<<grid, 64 * n, 0, a.stream>>>(               \
+                                            w.a2, a.s_in, a.ds_out, w.sumdt, w.hin, w.gout, total, a.D, a.N, p.NP, pl.G))
+        if (segment_parts(total) == 16) LA_SSM_SEGMENTS(16);
+        else LA_SSM_SEGMENTS(4);
+#undef LA_SSM_SEGMENTS
+        const int nw = p.NP / NW8;
+        const size_t lds = T * 64 * (2 * 4 * es + (3 + 3 * nw) * sizeof(float));
+#define LA_SSM_MAIN(V, O) \
+    LA_TRACED(a.tr, "ssm_bwd_main", ssm_bwd_main_kernel<E, V, O><<<blocks, 64 * nw, lds, a.stream>>>(p))
+        if (nw == 1) {
+            if (vec) LA_SSM_MAIN(true, true);
+            else LA_SSM_MAIN(false, true);
+        } else {
+            if (vec) LA_SSM_MAIN(true, false);
             else LA_SSM_MAIN(false, false);
         }
 #undef LA_SSM_MAIN
     }
     const unsigned nbc = (unsigned)((a.B * a.L * 2 * p.NP + 255) / 256);
-    const unsigned nd = (unsigned)((a.D * (a.N + 2) + 255) / 256);
+    const unsigned nd = (unsigned)((a.D + 15) / 16 * (a.N + 2));
     if (nbc + nd > 0)
         LA_TRACED(a.tr, "ssm_bwd_sums",
                   ssm_bwd_sums_kernel<E><<<nbc + nd, 256, 0, a.stream>>>(w.dbc, w.dap, w.ddp, a.lengths, (E*)a.dB, (E*)a.dC,
@@ -613,7 +648,7 @@ hipError_t launch_e(const SsmArgs& a) {
 }  // namespace
 
 size_t ssm_bwd_ws(int64_t B, int64_t L, int64_t D, int N) {
-    return bwd_cut(nullptr, B, L, D, N, bwd_plan(B, L, D).G).bytes;
+    return bwd_cut(nullptr, B, L, D, N, bwd_plan(B, L, D, np_for(N)).G).bytes;
 }
 
 hipError_t launch_ssm_scan_bwd(const SsmArgs& a) { return a.bf16 ? launch_e<__bf16>(a) : launch_e<float>(a); }

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
         for (int j = 0; j < TT; j++) dl[j] = (float)tile[1][j * 64 + lane] + bias;
         if (p.softplus) {
 #pragma unroll
-            for (int j = 0; j < TT; j++) dl[j] = softplus<false>(dl[j], nullptr);
+            for (int j = 0; j < TT; j++) dl[j] = softplus(dl[j]);
         }
 #pragma unroll
         for (int j = 0; j < TT; j++) {
@@ -186,36 +186,23 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
 }
 
 // States entering the segments from the segments' own end states: slot 0 takes s_in, slot g + 1
-// (holding segment g's end state from zero) adds the decayed state that entered segment g.  A thread
-// owns one (b, n, d); its loads are issued PB segments ahead of the chain.
-constexpr int PB = 32;
-__global__ __launch_bounds__(256) void ssm_segments_kernel(const float* __restrict__ a2, const float* __restrict__ s_in,
-                                                           const float* __restrict__ sumdt, float* __restrict__ part,
-                                                           int64_t total, int64_t D, int N, int G) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
+// (holding segment g's end state from zero) adds the decayed state that entered segment g.
+template <int PARTS>
+__global__ __launch_bounds__(64 * PARTS) void ssm_segments_kernel(const float* __restrict__ a2, const float* __restrict__ s_in,
+                                                           const float* sumdt, float* part, int64_t total, int64_t D,
+                                                           int N, int G) {
+    const int64_t i0 = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const bool on = i0 < total;
+    const int64_t i = on ? i0 : 0;
     const int64_t d = i % D, n = i / D % N, b = i / (D * N);
-    const float rate = a2[n * D + d];
-    float h = s_in ? s_in[i] : 0.f;
+    const float x0 = s_in ? s_in[i] : 0.f;
     float* pp = part + (b * G * N + n) * D + d;
     const float* sp = sumdt + b * G * D + d;
     const int64_t ps = (int64_t)N * D;
-    pp[0] = h;
-    for (int g0 = 1; g0 < G; g0 += PB) {
-        float v[PB], s[PB];
-#pragma unroll
-        for (int j = 0; j < PB; j++) {
-            const int g = min(g0 + j, G - 1);
-            v[j] = pp[g * ps];
-            s[j] = sp[(g - 1) * D];
-        }
-#pragma unroll
-        for (int j = 0; j < PB; j++)
-            if (g0 + j < G) {
-                h = fmaf(__builtin_amdgcn_exp2f(rate * s[j]), h, v[j]);
-                pp[(g0 + j) * ps] = h;
-            }
-    }
+    if (on && threadIdx.x < 64) pp[0] = x0;
+    segment_chain<PARTS>(
+        G - 1, x0, a2[n * D + d], on, [&](int k) { return pp + (k + 1) * ps; }, [&](int k) { return sp + k * D; },
+        [&](int k, float, float next) { pp[(k + 1) * ps] = next; });
 }
 
 int np_for(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 24 ? 24 : N <= 32 ? 32 : N <= 48 ? 48 : 64; }
@@ -245,8 +232,12 @@ void launch_np(const SsmArgs& a, FwdDev p, const SsmPlan& pl) {
         p.ng = pl.G - 1;
         LA_TRACED(a.tr, "ssm_state", ssm_fwd_kernel<T, NP, true, VEC><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
         const int64_t total = a.B * a.N * a.D;
-        LA_TRACED(a.tr, "ssm_segments", ssm_segments_kernel<<<(unsigned)((total + 255) / 256), 256, 0, a.stream>>>(
-                                            p.a2, a.s_in, p.sumdt, p.part, total, a.D, a.N, pl.G));
+#define LA_SSM_SEGMENTS(n)                                                                                    \
+    LA_TRACED(a.tr, "ssm_segments", ssm_segments_kernel<n><<<(unsigned)((total + 63) / 64), 64 * n, 0, a.stream>>>( \
+                                        p.a2, a.s_in, p.sumdt, p.part, total, a.D, a.N, pl.G))
+        if (segment_parts(total) == 16) LA_SSM_SEGMENTS(16);
+        else LA_SSM_SEGMENTS(4);
+#undef LA_SSM_SEGMENTS
     }
     p.ng = pl.G;
     LA_TRACED(a.tr, "ssm_out", ssm_fwd_kernel<T, NP, false, VEC><<<p.cb * p.ng * (unsigned)a.B, 64, 0, a.stream>>>(p));
@@ -361,7 +352,7 @@ __global__ __launch_bounds__(64) void ssm_step_kernel(StepDev p) {
         if (b + 1 < b1) fetch(b + 1);
         if (s < 0 || s >= p.nslots) continue;
         if (p.slots && earlier_row_has(p.slots, b, s)) continue;
-        const float delta = p.softplus ? softplus<false>(x, nullptr) : x;
+        const float delta = p.softplus ? softplus(x) : x;
         const float du = delta * u;
         float acc = skip * u;
 #pragma unroll
