@@ -173,7 +173,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _check(fn: str, status: int) -> None:
-    if status != 0:
+    if status:
         raise LaError(fn, status, lib().la_status_str(status).decode())
 
 
@@ -518,57 +518,58 @@ class _On:
     """The device and stream of a call: makes both current while the call allocates and enqueues.  A call on
     the current device and stream, the common case, enters no context."""
 
-    __slots__ = ("device", "stream", "handle", "_dev", "_st")
+    __slots__ = ("like", "index", "stream", "handle", "ctx")
 
     def __init__(self, t: torch.Tensor, name: str, stream):
+        self.like, self.stream = t, stream
+        self.index = t.get_device()  # -1 on the host
         if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
-        self.device = t.device
-        self.stream = stream
         if stream is not None and stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
 
     def __enter__(self):
-        i = self.device.index
-        if self.stream is None and torch.cuda.current_device() == i:
-            self._dev = self._st = None
+        i = self.index
+        if self.stream is None and torch._C._cuda_getDevice() == i:
+            self.ctx = None
         else:
-            self._dev = torch.cuda.device(self.device)
-            self._dev.__enter__()
-            self._st = torch.cuda.stream(self.stream)  # no-op for None
-            self._st.__enter__()
+            self.ctx = (torch.cuda.device(i), torch.cuda.stream(self.stream))  # stream(None) is a no-op
+            for c in self.ctx:
+                c.__enter__()
         self.handle = torch._C._cuda_getCurrentRawStream(i)
         return self
 
     def __exit__(self, *exc):
-        if self._dev is not None:
-            self._st.__exit__(*exc)
-            self._dev.__exit__(*exc)
+        if self.ctx is not None:
+            for c in reversed(self.ctx):
+                c.__exit__(*exc)
 
     def check(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
         """``t`` (or None) with that type and shape on the call's device; dense, or any strides with a
         contiguous last dim."""
         if t is None:
             return None
-        if t.shape == shape and t.dtype is dtype and t.device == self.device:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == self.index:
             if t.is_contiguous() or (not dense and (t.numel() == 0 or shape[-1] <= 1 or t.stride(-1) == 1)):
                 return t
             raise ValueError(f"{name} must be contiguous" if dense else f"{name}: the last dim must be contiguous")
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, not {t.device}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name} must be on {self.like.device}, not {t.device}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
     def out(self, t: Optional[torch.Tensor], name: str, dtype, shape, dense=True):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        return self.check(t, name, dtype, shape, dense)
+        if t is not None:
+            return self.check(t, name, dtype, shape, dense)
+        if dtype is self.like.dtype:
+            return self.like.new_empty(*shape)
+        return self.like.new_empty(shape, dtype=dtype)
 
     def workspace(self, fn: str, nbytes: int) -> torch.Tensor:
         if nbytes < 0:
             _check(fn, nbytes)
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return self.like.new_empty(nbytes, dtype=torch.uint8)
 
 
 def _at(t: Optional[torch.Tensor]):

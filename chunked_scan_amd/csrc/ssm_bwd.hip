@@ -71,23 +71,6 @@ __device__ __forceinline__ BwdArgsPtr bwd_args() {
     return q;
 }
 
-// The same value, waited for here and unknown to the compiler from here on: the wait comes before the next
-// token's loads are issued and not after them, and exponentials of the way forwards are not held on to for the
-// way back, for which there are no registers.
-__device__ __forceinline__ float arrived(float x) {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" : "+v"(x));
-    __builtin_amdgcn_sched_barrier(0);
-    return x;
-}
-
-// The same for a value in a scalar register.
-__device__ __forceinline__ void arrived_row(float& x) {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" : "+s"(x));
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // Pass 1.  blockIdx.x: channel block fastest, then group of NC key dims, segment, sequence.  Tiles as in the
 // forward: tokens behind the segment's end have delta = ds = 0.
 // NC: key dims per group, 8 or 16.

@@ -72,6 +72,15 @@ __global__ __launch_bounds__(256) void pack_kernel(const T* __restrict__ Bm, con
     bc[i] = v;
 }
 
+// The kernel's arguments, read again from memory where they are used: held over the token loop they would push
+// each other and the rows of B and C out of the scalar registers (5 x 777 x 1000 fp32, N = 24: 29 -> 24 us a pass).
+typedef const __attribute__((address_space(4))) FwdDev* FwdArgsPtr;
+__device__ __forceinline__ FwdArgsPtr fwd_args() {
+    FwdArgsPtr q = (FwdArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(q));
+    return q;
+}
+
 // STATE: the first pass (a segment's end state from zero and its sum of delta), else the second.  VEC: rows are
 // 16-byte aligned and whole 8-channel chunks.  Tokens of a tile behind the segment's end repeat its last row
 // with delta = 0 (decay 1, input 0): they leave the state alone and are not stored.
@@ -106,18 +115,16 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
     const float skip = !STATE && p.Dskip ? p.Dskip[d] : 0.f;
     const int t0 = (int)(g * p.seglen), t1 = min(t0 + (int)p.seglen, uniform((int)seq_len(p.lengths, b, p.L)));
     const bool gate = !STATE && p.z;
-    const E* ub = (const E*)p.u + b * p.su.batch + d0;
-    const E* xb = (const E*)p.dt + b * p.sdt.batch + d0;
-    const E* zb = gate ? (const E*)p.z + b * p.sz.batch + d0 : nullptr;
-    E* yb = STATE ? nullptr : (E*)p.y + b * p.sy.batch + d0;
-    scalar_f32 row = as_scalar(p.bc + (b * p.L + t0) * (2 * NP));
+    const bool sp = p.softplus;
+    scalar_f32 rowp = as_scalar(p.bc + (b * p.L + t0) * (2 * NP));
 
     Raw8<E> raw[NS];
     auto fetch = [&](int t) {
+        const FwdArgsPtr q = fwd_args();
         const int tt = min(t + pl.token, t1 - 1);
-        raw[0] = tile_load<E, VEC>(ub, p.su.token, tt, pl);
-        raw[1] = tile_load<E, VEC>(xb, p.sdt.token, tt, pl);
-        if (gate) raw[NS - 1] = tile_load<E, VEC>(zb, p.sz.token, tt, pl);
+        raw[0] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
+        raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
+        if (gate) raw[NS - 1] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
     };
     float sum = 0.f;
     if (t0 < t1) fetch(t0);
@@ -130,7 +137,7 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
         float dl[TT], du[TT], out[TT];
 #pragma unroll
         for (int j = 0; j < TT; j++) dl[j] = (float)tile[1][j * 64 + lane] + bias;
-        if (p.softplus) {
+        if (sp) {
 #pragma unroll
             for (int j = 0; j < TT; j++) dl[j] = softplus(dl[j]);
         }
@@ -142,21 +149,36 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
             out[j] = skip * u;
         }
         if (t + TT < t1) fetch(t + TT);
+        // The first pass takes rows of B one token ahead of their use (16384 x 2048, N = 16: 129 -> 127 us); in the
+        // second the fences cost registers and with them a wave per SIMD (144 -> 155 us).
+        constexpr bool AHEAD = STATE && NP <= 32;
+        float row[2][AHEAD ? NP : 1];
+        auto load_row = [&](int j) {
+#pragma unroll
+            for (int n = 0; n < NP; n++) row[j & 1][n] = rowp[n];
+            rowp += t + j + 1 < t1 ? 2 * NP : 0;
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if constexpr (AHEAD) load_row(0);
 #pragma unroll
         for (int j = 0; j < TT; j++) {
+            if constexpr (AHEAD) {
+                arrived_row(row[j & 1][0]);
+                if (j + 1 < TT) load_row(j + 1);
+            }
             float acc = 0.f;
 #pragma unroll
             for (int n = 0; n < NP; n++) {
                 const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
-                h[n] = fmaf(a, h[n], du[j] * row[n]);
+                h[n] = fmaf(a, h[n], du[j] * (AHEAD ? row[j & 1][AHEAD ? n : 0] : rowp[n]));
                 if (!STATE) {
-                    if (n & 1) acc = fmaf(row[NP + n], h[n], acc);
-                    else out[j] = fmaf(row[NP + n], h[n], out[j]);
+                    if (n & 1) acc = fmaf(rowp[NP + n], h[n], acc);
+                    else out[j] = fmaf(rowp[NP + n], h[n], out[j]);
                 }
             }
             if (STATE) sum += dl[j];
             else out[j] += acc;
-            row += t + j + 1 < t1 ? 2 * NP : 0;
+            if constexpr (!AHEAD) rowp += t + j + 1 < t1 ? 2 * NP : 0;
         }
         if (STATE) continue;
         if (gate) {
@@ -169,19 +191,27 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
 #pragma unroll
         for (int j = 0; j < TT; j++) io<E>::st(tile[3] + j * 64 + lane, out[j]);
         wave_lds_fence();
-        if (pl.in && t + pl.token < t1)
-            store8<VEC>(yb + (t + pl.token) * p.sy.token + pl.col, pl.n, *lds_chunk(tile[3], pl));
+        if (pl.in && t + pl.token < t1) {
+            const FwdArgsPtr q = fwd_args();
+            store8<VEC>((E*)q->y + b * q->sy.batch + d0 + (t + pl.token) * q->sy.token + pl.col, pl.n,
+                        *lds_chunk(tile[3], pl));
+        }
     }
     if (!live) return;
+    const FwdArgsPtr e = fwd_args();
+    const int64_t D = e->D;
+    const int N = e->N;
     if (STATE) {
+        float* part = e->part + (b * e->G + g + 1) * N * D + d0;
 #pragma unroll
         for (int n = 0; n < NP; n++)
-            if (n < p.N) p.part[((b * p.G + g + 1) * p.N + n) * p.D + d] = h[n];
-        p.sumdt[(b * p.G + g) * p.D + d] = sum;
-    } else if (p.s_out && g == p.G - 1) {
+            if (n < N) (part + n * D)[lane] = h[n];
+        (e->sumdt + (b * e->G + g) * D + d0)[lane] = sum;
+    } else if (e->s_out && g == e->G - 1) {
+        float* so = e->s_out + b * N * D + d0;
 #pragma unroll
         for (int n = 0; n < NP; n++)
-            if (n < p.N) p.s_out[(b * p.N + n) * p.D + d] = h[n];
+            if (n < N) (so + n * D)[lane] = h[n];
     }
 }
 

@@ -96,4 +96,21 @@ __device__ __forceinline__ Raw8<E>* lds_chunk(E* tile, const TilePlace& pl) {
     return reinterpret_cast<Raw8<E>*>(tile + (threadIdx.x & 63) * 8);
 }
 
+// The same value, waited for here and unknown to the compiler from here on: the wait comes before the next
+// token's loads are issued and not after them, and exponentials of the way forwards are not held on to for the
+// way back, for which there are no registers.
+__device__ __forceinline__ float arrived(float x) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+v"(x));
+    __builtin_amdgcn_sched_barrier(0);
+    return x;
+}
+
+// The same for a value in a scalar register.
+__device__ __forceinline__ void arrived_row(float& x) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" : "+s"(x));
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 }  // namespace la
