@@ -33,14 +33,27 @@ correction.
                      and one scan entry, at the price of a local forward that needs S_recv.
 ``segmented_forward`` -- P devices emulated on one GPU: the local forward of all P segments in
                      one launch, the P-entry state scan, and the correction of segments 1..P-1.
+
+The selective state space layer, whose decay comes from an input-dependent step size, is sequenced likewise
+around the caller's two projections (which are not part of the library):
+
+``selective_prompt`` -- residual norm, projection to the mixer's input and gate, short convolution, projection
+                     to step size, B and C, selective scan, for a (padded) batch of prompts or for the next
+                     piece of one.
+``selective_token``  -- the same for one token of each of several running sequences, whose convolution and scan
+                     states live in pools.
+``selective_backward`` -- the prompt's operators in reverse, the projections' own backward left to the caller.
 """
 from __future__ import annotations
 
-from typing import Optional
+from dataclasses import dataclass
+from typing import Callable, Optional, Tuple
 
 import torch
 
-from .binding import la_chunk_fwd, la_chunk_fwd_decayed, la_cumdecay, la_state_correct, la_state_scan
+from .binding import (la_add_norm, la_add_norm_bwd, la_add_norm_q8, la_chunk_fwd, la_chunk_fwd_decayed, la_cumdecay,
+                      la_short_conv, la_short_conv_bwd, la_short_conv_step, la_ssm_scan, la_ssm_scan_bwd, la_ssm_step,
+                      la_state_correct, la_state_scan)
 
 
 def _tile_flags(B, H, L, nseg, dev):
@@ -212,3 +225,84 @@ def segmented_forward(q, k, v, decay, s_in, *, mode: str, nseg: int, chunk: int 
     """Returns (o, out_states [B,H,P,dk,dv]); out_states[:, :, -1] is the final state."""
     return SegmentedForward(q, k, v, decay, s_in, mode=mode, nseg=nseg, chunk=chunk, gate_norm=gate_norm,
                             subseg_chunks=subseg_chunks).run()
+
+
+@dataclass
+class SelectiveParams:
+    """A selective layer's own parameters, all float32: norm_weight [Dm]; conv_weight [D, W], conv_bias [D] or
+    None; A [D, N]; skip [D] or None; dt_bias [D] or None.  q8_group: None (the norm's output in the
+    activations' type) or the elements per scale of an 8-bit output (la_add_norm_q8's group)."""
+    norm_weight: torch.Tensor
+    conv_weight: torch.Tensor
+    conv_bias: Optional[torch.Tensor]
+    A: torch.Tensor
+    skip: Optional[torch.Tensor] = None
+    dt_bias: Optional[torch.Tensor] = None
+    eps: float = 1e-5
+    q8_group: Optional[int] = None
+
+
+def _norm_in(p: SelectiveParams, x, residual):
+    """(what the input projection takes, h, rstd): the normed rows, or (q, scale) in 8 bits."""
+    if p.q8_group is None:
+        return la_add_norm(x, p.norm_weight, residual, eps=p.eps)
+    q, scale, h, rstd = la_add_norm_q8(x, p.norm_weight, residual, eps=p.eps, group=p.q8_group)
+    return (q, scale), h, rstd
+
+
+def selective_prompt(p: SelectiveParams, x: torch.Tensor, residual: Optional[torch.Tensor],
+                     project_in: Callable, project_dbc: Callable, *, conv_state: Optional[torch.Tensor] = None,
+                     s_in: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                     saved: Optional[dict] = None) -> Tuple[torch.Tensor, ...]:
+    """One layer over x [B, L, Dm] (residual the same or None).  project_in maps the normed rows [B L, Dm] (or
+    (q, scale)) to (u, z): two [B L, D] tensors, the gate z possibly None, usually the halves of one
+    product.  project_dbc maps the convolved [B, L, D] to (dt, B, C): [B, L, D], [B, L, N], [B, L, N].
+    conv_state [B, W-1, D] and s_in [B, N, D]: states of the tokens before, or None.  Returns (y [B, L, D],
+    zero behind a sequence's length, h [B, L, Dm] the residual stream, conv_state, s_out).  `saved`, a dict, receives what
+    selective_backward takes."""
+    B, L, Dm = x.shape
+    rows = lambda t: None if t is None else t.reshape(B * L, -1)  # noqa: E731
+    y, h, rstd = _norm_in(p, rows(x), rows(residual))
+    u, z = (None if t is None else t.unflatten(0, (B, L)) for t in project_in(y))
+    # rows behind a sequence's length are not written: they are zero here, so that a product over all rows
+    # (the projections' weight derivatives) stays finite
+    blank = lambda: None if lengths is None else torch.zeros(u.shape, dtype=u.dtype, device=u.device)  # noqa: E731
+    v, conv_out = la_short_conv(u, p.conv_weight, p.conv_bias, conv_state, lengths=lengths, y=blank(), want_state=True)
+    dt, Bm, C = project_dbc(v)
+    o, s_out = la_ssm_scan(v, dt, p.A, Bm, C, D=p.skip, z=z, dt_bias=p.dt_bias, s_in=s_in, lengths=lengths, y=blank())
+    if saved is not None:
+        saved.update(h=h, rstd=rstd, u=u, z=z, v=v, dt=dt, B=Bm, C=C, conv_state=conv_state, s_in=s_in, lengths=lengths)
+    return o, h.view(B, L, Dm), conv_out, s_out
+
+
+def selective_backward(p: SelectiveParams, saved: dict, dy: torch.Tensor, dbc_backward: Callable,
+                       in_backward: Callable, *, dh: Optional[torch.Tensor] = None,
+                       d_conv_state: Optional[torch.Tensor] = None, ds_out: Optional[torch.Tensor] = None) -> dict:
+    """Backward of selective_prompt from dy [B, L, D], dh [B, L, Dm] (the residual stream's derivative) and those of
+    the returned states.  dbc_backward maps (ddt, dB, dC) to the convolved tensor's part of the derivative
+    [B, L, D]; in_backward maps (du, dz) to the normed rows' [B L, Dm].  Returns dx (of x and residual
+    alike) and the parameters' and incoming states' derivatives by name."""
+    s = saved
+    B, L, _ = s["u"].shape
+    dv, ddt, dA, dB, dC, dskip, dz, d_dt_bias, ds_in = la_ssm_scan_bwd(
+        s["v"], s["dt"], p.A, s["B"], s["C"], dy, D=p.skip, z=s["z"], dt_bias=p.dt_bias, s_in=s["s_in"], ds_out=ds_out,
+        lengths=s["lengths"])
+    dv += dbc_backward(ddt, dB, dC)
+    du, dcw, dcb, d_conv = la_short_conv_bwd(s["u"], p.conv_weight, dv, p.conv_bias, s["conv_state"], d_conv_state,
+                                             lengths=s["lengths"])
+    dn = in_backward(du, dz)
+    dx, dnw = la_add_norm_bwd(dn, s["h"], p.norm_weight, s["rstd"], None if dh is None else dh.reshape(B * L, -1))
+    return dict(dx=dx.view(B, L, -1), norm_weight=dnw, conv_weight=dcw, conv_bias=dcb, A=dA, skip=dskip,
+                dt_bias=d_dt_bias, conv_state=d_conv, s_in=ds_in)
+
+
+def selective_token(p: SelectiveParams, x: torch.Tensor, residual: Optional[torch.Tensor], project_in: Callable,
+                    project_dbc: Callable, conv_pool: torch.Tensor, state_pool: torch.Tensor,
+                    slots: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One layer over one token of each of B sequences, x [B, Dm]; conv_pool [S, W-1, D] and state_pool
+    [S, N, D] are updated in place at the rows' slots.  Returns (y [B, D], h [B, Dm])."""
+    y, h, _ = _norm_in(p, x, residual)
+    u, z = project_in(y)
+    v = la_short_conv_step(u, p.conv_weight, conv_pool, p.conv_bias, slots=slots)
+    dt, Bm, C = project_dbc(v)
+    return la_ssm_step(v, dt, p.A, Bm, C, state_pool, D=p.skip, z=z, dt_bias=p.dt_bias, slots=slots), h

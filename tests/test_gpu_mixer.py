@@ -8,6 +8,7 @@ multiplies a state by a decay whose exponent carries about 8 roundings, so after
 for the step size, the gate and the sum over the state (64 terms at most, in fp32); sums over D channels
 or B L tokens add one rounding a term.  Norm: D / 8 for a lane's share of a row's sum, plus 32.
 """
+import dataclasses
 import itertools
 
 import numpy as np
@@ -16,6 +17,7 @@ import torch
 
 import mixer_ref as R
 from chunked_scan_amd import binding as la
+from chunked_scan_amd import pipeline
 from gpu_util import note
 
 pytestmark = pytest.mark.gpu
@@ -301,6 +303,74 @@ def test_scan_backward_against_differences():
         assert abs(diff - want) <= 1e-2 * scale / np.sqrt(v.numel()) + 1e-3 * scale, (k, diff, want, scale)
 
 
+def test_gradients_into_slices_of_wide_buffers():
+    """du and dz as the halves of one buffer, ddt, dB and dC as slices of another: the same values as dense outputs,
+    and nothing beside the slices is touched."""
+    note("gradient slices")
+    case = (2, 75, 72, 16, [75, 20], False, True, True, True, True, True)
+    a, n = scan_inputs(case, BF, 31)
+    kw = dict(D=a["D"], z=a["z"], dt_bias=a["dt_bias"], s_in=a["s_in"], ds_out=a["ds_out"], lengths=ints(n))
+    args = [a[k] for k in ("u", "dt", "A", "B", "C", "dy")]
+    ref = la.la_ssm_scan_bwd(*args, **kw)
+    B, L, D, N = 2, 75, 72, 16
+    xz = torch.full((B, L, 2 * D + 8), SENTINEL, dtype=BF, device="cuda")
+    dbc = torch.full((B, L, D + 2 * N + 8), SENTINEL, dtype=BF, device="cuda")
+    got = la.la_ssm_scan_bwd(*args, **kw, du=xz[..., :D], dz=xz[..., D : 2 * D], ddt=dbc[..., :D], dB=dbc[..., D : D + N],
+                             dC=dbc[..., D + N : D + 2 * N])
+    for r, t in zip(ref, got):
+        assert torch.equal(r, t)
+    assert (xz[..., 2 * D :] == SENTINEL).all() and (dbc[..., D + 2 * N :] == SENTINEL).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Sequences, rows and slots more than 2^32 bytes and 2^31 elements apart give what they give close together."""
+    note("large offsets")
+    far = (1 << 31) + 64
+    g = Draw(71)
+    L, D, N = 20, 64, 16
+    buf = torch.empty(far + L * D + D * N, dtype=BF, device="cuda")
+
+    def spread(t):
+        """t [2, ...] with its second entry far behind the first."""
+        inner = t[0].numel()
+        v = buf.as_strided(t.shape, (far,) + tuple(t[0].stride()))
+        assert inner <= buf.numel() - far
+        v.copy_(t)
+        return v
+
+    x, w = g.normal(2, L, D, dtype=BF), g.normal(D, 4, std=0.5)
+    want, _ = la.la_short_conv(x, w)
+    got, _ = la.la_short_conv(spread(x), w)
+    assert torch.equal(want, got)
+    out = buf.as_strided(x.shape, (far, D, 1))
+    buf.zero_()
+    la.la_short_conv(x, w, y=out)
+    assert torch.equal(want, out)
+    a, _ = scan_inputs((2, L, D, N, None, False, False, True, True, False, True), BF, 72)
+    args = lambda u: (u, a["dt"], a["A"], a["B"], a["C"])  # noqa: E731
+    kw = dict(D=a["D"], dt_bias=a["dt_bias"])
+    want = la.la_ssm_scan(*args(a["u"]), **kw)
+    got = la.la_ssm_scan(*args(spread(a["u"])), **kw)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    want = la.la_ssm_scan_bwd(*args(a["u"]), a["dy"], **kw)
+    got = la.la_ssm_scan_bwd(*args(spread(a["u"])), a["dy"], **kw)
+    for r, t in zip(want, got):
+        assert r is None or torch.equal(r, t)
+    rows, nw = g.normal(2, 512, dtype=BF), 1 + g.normal(512, std=0.1)
+    want = la.la_add_norm(rows, nw)
+    got = la.la_add_norm(spread(rows), nw)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[2], got[2])
+    del buf, got, out
+    S = (1 << 31) // (N * D) + 3  # the last slots start behind 2^31 elements
+    pool = torch.empty(S, N, D, device="cuda")
+    st = g.normal(2, N, D)
+    pool[0], pool[S - 1] = st[0], st[1]
+    one = [v[:, 0] if v.dim() == 3 else v for v in args(a["u"])]
+    y0 = la.la_ssm_step(*one, st, **kw)
+    y1 = la.la_ssm_step(*one, pool, slots=ints([0, S - 1]), **kw)
+    assert torch.equal(y0, y1) and torch.equal(pool[S - 1], st[1]) and torch.equal(pool[0], st[0])
+
+
 # ------------------------------------------------------------------------------------ norm
 
 NORM = [(1, 8, False), (3, 64, False), (5, 1000, False), (2, 7, False), (4, 130, True), (9, 2048, False), (2, 2056, True),
@@ -394,38 +464,25 @@ def test_norm_nonfinite_rows_stay_apart():
 # ------------------------------------------------------------------------------------ together
 
 
-def layer(D, N, W, seed, dtype):
-    """Weights of one layer: norm, projection to x, z; convolution; projection to dt, B, C; scan."""
+def layer(D, N, W, seed, q8=None):
+    """(params, project_in, project_dbc, weights): a layer whose two projections are fp32 products."""
     g = Draw(seed)
-    return dict(w=1 + g.normal(D, std=0.1), cw=g.normal(D, W, std=0.5), cb=g.normal(D, std=0.1), A=-g.uniform(D, N, lo=0.5, hi=8.0),
-                D=g.normal(D), bias=g.uniform(D, lo=-5.0, hi=-2.0), wx=g.normal(D, 2 * D, std=D ** -0.5),
-                wp=g.normal(D, D + 2 * N, std=D ** -0.5), N=N, dtype=dtype)
+    p = pipeline.SelectiveParams(1 + g.normal(D, std=0.1), g.normal(D, W, std=0.5), g.normal(D, std=0.1),
+                                 -g.uniform(D, N, lo=0.5, hi=8.0), g.normal(D), g.uniform(D, lo=-5.0, hi=-2.0), q8_group=q8)
+    wx, wp = g.normal(D, 2 * D, std=D ** -0.5), g.normal(D, D + 2 * N, std=D ** -0.5)
 
+    def project_in(y):
+        if q8 is not None:  # dequantised: value times its group's scale
+            q, scale = y
+            y = (q.float().view(q.shape[0], scale.shape[1], -1) * scale[:, :, None]).view(q.shape)
+        xz = (y.float() @ wx).to(torch.bfloat16 if q8 is not None else y.dtype)
+        return xz[..., :D], xz[..., D:]
 
-def project(t, w):
-    return (t.float() @ w).to(t.dtype)
+    def project_dbc(v):
+        t = (v.float() @ wp).to(v.dtype)
+        return t[..., :D], t[..., D : D + N], t[..., D + N :]
 
-
-def prompt(p, x, res, conv_state, s, lengths=None):
-    B, L, D = x.shape
-    N = p["N"]
-    y, h, _ = la.la_add_norm(x.reshape(-1, D), p["w"], res.reshape(-1, D))
-    xz = project(y, p["wx"]).view(B, L, 2 * D)
-    v, cs = la.la_short_conv(xz[..., :D], p["cw"], p["cb"], conv_state, lengths=lengths, want_state=True)
-    dbc = project(v, p["wp"])
-    o, so = la.la_ssm_scan(v, dbc[..., :D], p["A"], dbc[..., D : D + N], dbc[..., D + N :], D=p["D"], z=xz[..., D:],
-                           dt_bias=p["bias"], s_in=s, lengths=lengths)
-    return o, h.view(B, L, D), cs, so
-
-
-def token(p, x, res, conv_pool, pool, slots):
-    D, N = x.shape[1], p["N"]
-    y, h, _ = la.la_add_norm(x, p["w"], res)
-    xz = project(y, p["wx"])
-    v = la.la_short_conv_step(xz[:, :D], p["cw"], conv_pool, p["cb"], slots=slots)
-    dbc = project(v, p["wp"])
-    return la.la_ssm_step(v, dbc[:, :D], p["A"], dbc[:, D : D + N], dbc[:, D + N :], pool, D=p["D"], z=xz[:, D:],
-                          dt_bias=p["bias"], slots=slots), h
+    return p, project_in, project_dbc, wx, wp
 
 
 def test_layer_prompt_then_tokens_equals_one_prompt():
@@ -434,11 +491,11 @@ def test_layer_prompt_then_tokens_equals_one_prompt():
     again for each of the two fp32 projections between (sums of D = 64)."""
     note("layer: prompts, then tokens")
     B, L, D, N, W, T = 3, 150, 64, 16, 4, 6
-    p = layer(D, N, W, 40, F32)
+    p, pin, pdbc, _, _ = layer(D, N, W, 40)
     g = Draw(41)
     x, res = g.normal(B, L + T, D), g.normal(B, L + T, D)
     lens = [150, 3, 97]
-    o, _, cs, so = prompt(p, x[:, :L].contiguous(), res[:, :L].contiguous(), None, None, ints(lens))
+    o, _, cs, so = pipeline.selective_prompt(p, x[:, :L].contiguous(), res[:, :L].contiguous(), pin, pdbc, lengths=ints(lens))
     conv_pool, pool = torch.zeros(5, W - 1, D, device="cuda"), torch.zeros(5, N, D, device="cuda")
     at = torch.tensor([4, 0, 2], device="cuda")
     conv_pool[at], pool[at] = cs, so
@@ -447,10 +504,10 @@ def test_layer_prompt_then_tokens_equals_one_prompt():
     for k in range(T):
         xt = torch.stack([x[i, lens[i] + k] for i in range(B)])
         rt = torch.stack([res[i, lens[i] + k] for i in range(B)])
-        rows.append(token(p, xt, rt, conv_pool, pool, slots)[0])
+        rows.append(pipeline.selective_token(p, xt, rt, pin, pdbc, conv_pool, pool, slots)[0])
     for i in range(B):
         n = lens[i] + T
-        one, _, c1, s1 = prompt(p, x[i : i + 1, :n].contiguous(), res[i : i + 1, :n].contiguous(), None, None)
+        one, _, c1, s1 = pipeline.selective_prompt(p, x[i : i + 1, :n].contiguous(), res[i : i + 1, :n].contiguous(), pin, pdbc)
         tol = 3 * (8 * n + 64) * R.U * float(one.abs().max()) * 8
         assert float((one[0, : lens[i]] - o[i, : lens[i]]).abs().max()) <= tol
         for k in range(T):
@@ -459,27 +516,84 @@ def test_layer_prompt_then_tokens_equals_one_prompt():
         assert float((c1[0] - conv_pool[at[i]]).abs().max()) <= 64 * 3 * R.U * float(c1.abs().max()) * 8
 
 
+def test_layer_in_pieces_equals_one_prompt():
+    """A prompt in two pieces, the second from the first's states, against the whole; 8-bit norm output.  Rows are
+    normed, quantised and projected one by one, so only the scan's order of sums differs: in bf16 a state that
+    differs by a rounding of fp32 may move an output to the neighbouring bf16 value, one step of 2^-7 relative."""
+    note("layer: pieces, 8 bits")
+    B, L, D, N, W = 2, 260, 128, 16, 4
+    p, pin, pdbc, _, _ = layer(D, N, W, 44, q8=32)
+    g = Draw(45)
+    x, res = g.normal(B, L, D, dtype=BF), g.normal(B, L, D, dtype=BF)
+    o, h, cs, so = pipeline.selective_prompt(p, x, res, pin, pdbc)
+    k = 101
+    a = pipeline.selective_prompt(p, x[:, :k].contiguous(), res[:, :k].contiguous(), pin, pdbc)
+    b = pipeline.selective_prompt(p, x[:, k:].contiguous(), res[:, k:].contiguous(), pin, pdbc, conv_state=a[2], s_in=a[3])
+    got = torch.cat([a[0], b[0]], 1).double()
+    ref = o.double()
+    assert ((got - ref).abs() <= 2.0 ** -7 * ref.abs() + 3 * (8 * L + 64) * R.U * float(ref.abs().max()) * 8).all()
+    assert torch.equal(torch.cat([a[1], b[1]], 1), h) and torch.equal(b[2], cs)
+    assert float((b[3] - so).abs().max()) <= 3 * (8 * L + 64) * R.U * float(so.abs().max()) * 8
+
+
+def test_layer_gradients_against_differences():
+    """selective_backward's gradients of a scalar against differences of selective_prompt itself, in fp32, along one
+    random direction per argument (the step and the bound as in the scan's own test)."""
+    note("layer: gradients")
+    B, L, D, N, W = 2, 70, 64, 16, 4
+    p, pin, pdbc, wx, wp = layer(D, N, W, 47)
+    g = Draw(48)
+    lens = ints([70, 33])
+    a = dict(x=g.normal(B, L, D), res=g.normal(B, L, D), cs=g.normal(B, W - 1, D), s=g.normal(B, N, D))
+    live = (torch.arange(L, device="cuda")[None] < lens[:, None])[..., None]
+    dy, dh = g.normal(B, L, D) * live, g.normal(B, L, D)
+    dcs, ds = g.normal(B, W - 1, D), g.normal(B, N, D)
+    names = dict(norm_weight="norm_weight", conv_weight="conv_weight", conv_bias="conv_bias", A="A", skip="skip", dt_bias="dt_bias")
+
+    def loss(a, p):
+        o, h, c, s = pipeline.selective_prompt(p, a["x"], a["res"], pin, pdbc, conv_state=a["cs"], s_in=a["s"], lengths=lens)
+        o = torch.where(live, o, torch.zeros_like(o))
+        return float(sum((t.double() * d.double()).sum() for t, d in ((o, dy), (h, dh), (c, dcs), (s, ds))))
+
+    saved = {}
+    pipeline.selective_prompt(p, a["x"], a["res"], pin, pdbc, conv_state=a["cs"], s_in=a["s"], lengths=lens, saved=saved)
+    gr = pipeline.selective_backward(
+        p, saved, dy, lambda ddt, dB, dC: torch.cat([ddt, dB, dC], -1) @ wp.t(),
+        lambda du, dz: torch.cat([du, dz], -1).view(B * L, -1) @ wx.t(), dh=dh, d_conv_state=dcs, ds_out=ds)
+    want = dict(x=gr["dx"], res=gr["dx"], cs=gr["conv_state"], s=gr["s_in"])
+    e = 2.0 ** -7
+    for k in list(a) + list(names):
+        base = a[k] if k in a else getattr(p, k)
+        grad = want[k] if k in a else gr[names[k]]
+        v = g.normal(*base.shape)
+        vals = []
+        for sign in (1, -1):
+            if k in a:
+                vals.append(loss(dict(a, **{k: base + sign * e * v}), p))
+            else:
+                vals.append(loss(a, dataclasses.replace(p, **{k: base + sign * e * v})))
+        diff = (vals[0] - vals[1]) / (2 * e)
+        dot = float((grad.double() * v.double()).sum())
+        scale = float((grad.double().abs() * v.double().abs()).sum())
+        assert abs(diff - dot) <= 1e-2 * scale / np.sqrt(v.numel()) + 1e-3 * scale, (k, diff, dot, scale)
+
+
 def test_layer_in_a_graph_and_on_two_streams():
     """The layer captured and replayed with new inputs, eager work between the replays; and on two streams at once."""
     note("layer: graph and streams")
     B, L, D, N, W = 2, 300, 128, 16, 4
-    p = layer(D, N, W, 50, BF)
+    p, pin, pdbc, wx, wp = layer(D, N, W, 50)
     g = Draw(51)
     xs = [(g.normal(B, L, D, dtype=BF), g.normal(B, L, D, dtype=BF), g.normal(B, L, D, dtype=BF)) for _ in range(4)]
     zero = torch.zeros(B, N, D, device="cuda")
 
     def both(x, res, dy):
-        o, h, cs, so = prompt(p, x, res, None, zero)
-        N_ = p["N"]
-        y, _, r = la.la_add_norm(x.view(-1, D), p["w"], res.view(-1, D))
-        xz = project(y, p["wx"]).view(B, L, 2 * D)
-        v, _ = la.la_short_conv(xz[..., :D], p["cw"], p["cb"])
-        dbc = project(v, p["wp"])
-        gr = la.la_ssm_scan_bwd(v, dbc[..., :D], p["A"], dbc[..., D : D + N_], dbc[..., D + N_ :], dy, D=p["D"], z=xz[..., D:],
-                                dt_bias=p["bias"], s_in=zero)
-        gc = la.la_short_conv_bwd(xz[..., :D], p["cw"], gr[0], p["cb"])
-        gn = la.la_add_norm_bwd(gr[0].view(-1, D), h.view(-1, D), p["w"], r, gr[6].view(-1, D))
-        return [o, h, cs, so] + [t for t in gr + gc + gn if t is not None]
+        saved = {}
+        out = pipeline.selective_prompt(p, x, res, pin, pdbc, s_in=zero, saved=saved)
+        gr = pipeline.selective_backward(
+            p, saved, dy, lambda ddt, dB, dC: (torch.cat([ddt, dB, dC], -1).float() @ wp.t()).to(BF),
+            lambda du, dz: (torch.cat([du, dz], -1).view(B * L, -1).float() @ wx.t()).to(BF), dh=x)
+        return list(out) + [t for t in gr.values() if t is not None]
 
     eager = [both(*x) for x in xs]
     torch.cuda.synchronize()
