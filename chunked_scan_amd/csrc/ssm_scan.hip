@@ -85,8 +85,9 @@ __device__ __forceinline__ FwdArgsPtr fwd_args() {
 // 16-byte aligned and whole 8-channel chunks.  Tokens of a tile behind the segment's end repeat its last row
 // with delta = 0 (decay 1, input 0): they leave the state alone and are not stored.
 template <typename E, int NP, bool STATE, bool VEC>
-__global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
+__global__ __launch_bounds__(64, 2) void ssm_fwd_kernel(FwdDev p) {
     constexpr int NS = STATE ? 2 : 3;
+    constexpr int BV = TT * NP / 64;
     __shared__ __align__(16) E tile[STATE ? 2 : 4][TT * 64];  // u, dt, z, y
     // blocks: channel block fastest, then segment, then sequence
     const unsigned r = blockIdx.x / p.cb;
@@ -98,17 +99,19 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
     const int64_t d = live ? d0 + lane : p.D - 1;  // lanes behind the last channel repeat it
     const TilePlace pl(d0, p.D);
 
-    float h[NP], A2[NP];
+    // key dim 4 q + i is element i of h[q]
+    f32x4 h[NP / 4];
+    float A2[NP];
 #pragma unroll
     for (int n = 0; n < NP; n++) {
         A2[n] = p.a2[n * p.D + d];
-        h[n] = 0.f;
+        h[n / 4][n % 4] = 0.f;
     }
     if (!STATE && p.hin) {
 #pragma unroll
         for (int n = 0; n < NP; n++) {
             const float v = p.hin[((b * p.G + g) * p.N + min(n, p.N - 1)) * p.D + d];
-            h[n] = n < p.N ? v : 0.f;
+            h[n / 4][n % 4] = n < p.N ? v : 0.f;
         }
     }
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
@@ -116,15 +119,22 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
     const int t0 = (int)(g * p.seglen), t1 = min(t0 + (int)p.seglen, uniform((int)seq_len(p.lengths, b, p.L)));
     const bool gate = !STATE && p.z;
     const bool sp = p.softplus;
-    scalar_f32 rowp = as_scalar(p.bc + (b * p.L + t0) * (2 * NP));
+    const float* const bcb = p.bc + b * p.L * (2 * NP);
+    scalar_f32 rowc = as_scalar(bcb + t0 * (2 * NP) + NP);
 
     Raw8<E> raw[NS];
+    float br[BV], bn[BV];  // B of the tile's tokens, value j NP + n in lane (j NP + n) % 64, and the next tile's
     auto fetch = [&](int t) {
         const FwdArgsPtr q = fwd_args();
         const int tt = min(t + pl.token, t1 - 1);
         raw[0] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
         raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
         if (gate) raw[NS - 1] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
+#pragma unroll
+        for (int v = 0; v < BV; v++) {
+            const int e = v * 64 + lane;
+            bn[v] = bcb[min(t + e / NP, t1 - 1) * (2 * NP) + e % NP];
+        }
     };
     float sum = 0.f;
     if (t0 < t1) fetch(t0);
@@ -148,38 +158,31 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
             du[j] = dl[j] * u;
             out[j] = skip * u;
         }
+#pragma unroll
+        for (int v = 0; v < BV; v++) br[v] = bn[v];
         if (t + TT < t1) fetch(t + TT);
-        // The first pass takes rows of B one token ahead of their use (16384 x 2048, N = 16: 129 -> 127 us); in the
-        // second the fences cost registers and with them a wave per SIMD (144 -> 155 us).
-        constexpr bool AHEAD = STATE && NP <= 32;
-        float row[2][AHEAD ? NP : 1];
-        auto load_row = [&](int j) {
+        static_for<TT>([&](auto J) {
+            constexpr int j = J;
+            static_for<NP / 4>([&](auto Q) {
+                constexpr int q = Q;
+                f32x4 c;
 #pragma unroll
-            for (int n = 0; n < NP; n++) row[j & 1][n] = rowp[n];
-            rowp += t + j + 1 < t1 ? 2 * NP : 0;
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        if constexpr (AHEAD) load_row(0);
+                for (int i = 0; i < 4; i++) c[i] = __builtin_amdgcn_exp2f(dl[j] * A2[4 * q + i]) * h[q][i];
+                h[q] = outer4<j * NP + 4 * q>(br, du[j], c);
+            });
+            if (STATE) {
+                sum += dl[j];
+            } else {
+                float acc = 0.f;
 #pragma unroll
-        for (int j = 0; j < TT; j++) {
-            if constexpr (AHEAD) {
-                arrived_row(row[j & 1][0]);
-                if (j + 1 < TT) load_row(j + 1);
-            }
-            float acc = 0.f;
-#pragma unroll
-            for (int n = 0; n < NP; n++) {
-                const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
-                h[n] = fmaf(a, h[n], du[j] * (AHEAD ? row[j & 1][AHEAD ? n : 0] : rowp[n]));
-                if (!STATE) {
-                    if (n & 1) acc = fmaf(rowp[NP + n], h[n], acc);
-                    else out[j] = fmaf(rowp[NP + n], h[n], out[j]);
+                for (int n = 0; n < NP; n++) {
+                    if (n & 1) acc = fmaf(rowc[n], h[n / 4][n % 4], acc);
+                    else out[j] = fmaf(rowc[n], h[n / 4][n % 4], out[j]);
                 }
+                out[j] += acc;
+                rowc += t + j + 1 < t1 ? 2 * NP : 0;
             }
-            if (STATE) sum += dl[j];
-            else out[j] += acc;
-            if constexpr (!AHEAD) rowp += t + j + 1 < t1 ? 2 * NP : 0;
-        }
+        });
         if (STATE) continue;
         if (gate) {
 #pragma unroll
@@ -205,13 +208,13 @@ __global__ __launch_bounds__(64) void ssm_fwd_kernel(FwdDev p) {
         float* part = e->part + (b * e->G + g + 1) * N * D + d0;
 #pragma unroll
         for (int n = 0; n < NP; n++)
-            if (n < N) (part + n * D)[lane] = h[n];
+            if (n < N) (part + n * D)[lane] = h[n / 4][n % 4];
         (e->sumdt + (b * e->G + g) * D + d0)[lane] = sum;
     } else if (e->s_out && g == e->G - 1) {
         float* so = e->s_out + b * N * D + d0;
 #pragma unroll
         for (int n = 0; n < NP; n++)
-            if (n < N) (so + n * D)[lane] = h[n];
+            if (n < N) (so + n * D)[lane] = h[n / 4][n % 4];
     }
 }
 

@@ -4,6 +4,8 @@
 // other.  The LDS region belongs to one wave, whose LDS accesses execute in order: no barrier, only a
 // fence for the compiler.
 #pragma once
+#include <utility>
+
 #include "la_mixer.h"
 
 namespace la {
@@ -111,6 +113,26 @@ __device__ __forceinline__ void arrived_row(float& x) {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" : "+s"(x));
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// f(0), .., f(N - 1) with the index as a compile-time constant.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// c + x y^T for 4 key dims and the wave's 64 channels: key dim i is element i, the lane's channel has y.  x is in
+// lanes E % 64 + i of register x[E / 64].  It is the matrix cores' 4 x 4 x 1 fp32 product: its 16 blocks of 4
+// lanes are the 64 channels, and the block of x is broadcast to all of them.  One instruction in place of
+// four on the vector units, which bound these kernels.
+template <int E>
+__device__ __forceinline__ f32x4 outer4(const float* x, float y, f32x4 c) {
+    static_assert(E % 4 == 0, "a block of four lanes");
+    return __builtin_amdgcn_mfma_f32_4x4x1f32(x[E / 64], y, c, 4, E % 64 / 4, 0);
 }
 
 }  // namespace la
