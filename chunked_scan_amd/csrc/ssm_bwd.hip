@@ -75,7 +75,7 @@ __device__ __forceinline__ BwdArgsPtr bwd_args() {
 // forward: tokens behind the segment's end have delta = ds = 0.
 // NC: key dims per group, 8 or 16.
 template <typename E, int NC, bool VEC>
-__global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
+__global__ __launch_bounds__(64, 2) void ssm_bwd_states_kernel(BwdDev p) {
     __shared__ __align__(16) E tile[4][T * 64];  // u, dt, dy, z
     const unsigned ngr = p.NP / NC;
     unsigned r = blockIdx.x / p.cb;
@@ -90,19 +90,24 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
     const TilePlace pl(d0, p.D);
     const int t0 = (int)(g * p.seglen), t1 = min(t0 + (int)p.seglen, uniform((int)seq_len(p.lengths, b, p.L)));
 
-    float h[NC], A2[NC], q[NC], adj[NC];
+    // key dim nb + 4 q + i is element i of h[q]
+    f32x4 h[NC / 4], q[NC / 4], adj[NC / 4];
+    float A2[NC];
 #pragma unroll
     for (int n = 0; n < NC; n++) {
         A2[n] = p.a2[(nb + n) * p.D + d];
-        h[n] = 0.f;
-        q[n] = 1.f;
-        adj[n] = 0.f;
+        h[n / 4][n % 4] = 0.f;
+        q[n / 4][n % 4] = 1.f;
+        adj[n / 4][n % 4] = 0.f;
     }
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     const bool gate = p.z, sp = p.softplus;
     const int NP = p.NP;
-    scalar_f32 rowp = as_scalar(p.bc + (b * p.L + t0) * (2 * NP) + nb);
+    const float* const bcb = p.bc + b * p.L * (2 * NP) + nb;
 
+    // B and C of the tile's tokens, value j NC + n in lane (j NC + n) % 64, and the next tile's
+    constexpr int BV = T * NC / 64;
+    float br[BV], cr[BV], bn[BV], cn[BV];
     Raw8<E> raw[4];
     auto fetch = [&](int t) {
         const BwdArgsPtr q = bwd_args();
@@ -111,6 +116,13 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
         raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
         raw[2] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
         if (gate) raw[3] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
+#pragma unroll
+        for (int v = 0; v < BV; v++) {
+            const int e = v * 64 + lane;
+            const float* r = bcb + min(t + e / NC, t1 - 1) * (2 * NP) + e % NC;
+            bn[v] = r[0];
+            cn[v] = r[NP];
+        }
     };
     float sum = 0.f;
     if (t0 < t1) fetch(t0);
@@ -141,49 +153,46 @@ __global__ __launch_bounds__(64) void ssm_bwd_states_kernel(BwdDev p) {
                 ds[j] *= z * sigmoid(z);
             }
         }
+#pragma unroll
+        for (int v = 0; v < BV; v++) {
+            br[v] = bn[v];
+            cr[v] = cn[v];
+        }
         if (t + T < t1) fetch(t + T);
         if (t > t0 && live) {
             const BwdArgsPtr q = bwd_args();
             const int64_t k = b * q->nk + t / T, D = q->D;
             float* kp = q->kept + (k * NP + nb) * D + d0;
 #pragma unroll
-            for (int n = 0; n < NC; n++) (kp + n * D)[lane] = h[n];
+            for (int n = 0; n < NC; n++) (kp + n * D)[lane] = h[n / 4][n % 4];
             if (nb == 0) (q->keptdt + k * D + d0)[lane] = sum;
         }
-        // rows of B and C, one token ahead of their use
-        float row[2][2 * NC];
-        auto load_row = [&](int j) {
+        static_for<T>([&](auto J) {
+            constexpr int j = J;
+            static_for<NC / 4>([&](auto Q) {
+                constexpr int k = Q;
+                f32x4 c;
 #pragma unroll
-            for (int n = 0; n < NC; n++) {
-                row[j & 1][n] = rowp[n];
-                row[j & 1][NC + n] = rowp[NP + n];
-            }
-            rowp += t + j + 1 < t1 ? 2 * NP : 0;
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        load_row(0);
+                for (int i = 0; i < 4; i++) {
+                    const float a = __builtin_amdgcn_exp2f(dl[j] * A2[4 * k + i]);
+                    c[i] = a * h[k][i];
+                    q[k][i] *= a;
+                }
+                h[k] = outer4<j * NC + 4 * k>(br, du[j], c);
+                const f32x4 x = outer4<j * NC + 4 * k>(cr, ds[j], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int j = 0; j < T; j++) {
-            arrived_row(row[j & 1][0]);
-            if (j + 1 < T) load_row(j + 1);
-            const float* rw = row[j & 1];
-#pragma unroll
-            for (int n = 0; n < NC; n++) {
-                const float a = __builtin_amdgcn_exp2f(dl[j] * A2[n]);
-                h[n] = fmaf(a, h[n], du[j] * rw[n]);
-                q[n] *= a;
-                adj[n] = fmaf(q[n], ds[j] * rw[NC + n], adj[n]);
-            }
+                for (int i = 0; i < 4; i++) adj[k][i] = fmaf(q[k][i], x[i], adj[k][i]);
+            });
             sum += dl[j];
-        }
+        });
     }
     if (!live) return;
     const BwdArgsPtr e = bwd_args();
     const int64_t D = e->D, seg = b * e->G + g;
 #pragma unroll
     for (int n = 0; n < NC; n++) {
-        if (g + 1 < e->G) (e->hin + ((seg + 1) * NP + nb + n) * D + d0)[lane] = h[n];
-        (e->gout + (seg * NP + nb + n) * D + d0)[lane] = adj[n];
+        if (g + 1 < e->G) (e->hin + ((seg + 1) * NP + nb + n) * D + d0)[lane] = h[n / 4][n % 4];
+        (e->gout + (seg * NP + nb + n) * D + d0)[lane] = adj[n / 4][n % 4];
     }
     if (nb == 0) (e->sumdt + seg * D + d0)[lane] = sum;
 }
@@ -291,16 +300,21 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
 
     const int nb = w * NC;
     const int64_t sg = ((b * p.G + g) * p.NP + nb) * p.D + d0;
-    float A2[NC], adj[NC], dA[NC], kept[NC], hin[NC], keptdt = 0.f;
+    // key dim nb + 4 q + i is element i of adj[q], hs[.][q]
+    f32x4 adj[NC / 4];
+    float A2[NC], dA[NC], kept[NC], hin[NC], keptdt = 0.f;
 #pragma unroll
     for (int n = 0; n < NC; n++) {
         A2[n] = (p.a2 + (nb + n) * p.D + d0)[ln];
-        adj[n] = (p.gout + sg + n * p.D)[ln];
+        adj[n / 4][n % 4] = (p.gout + sg + n * p.D)[ln];
         hin[n] = (p.hin + sg + n * p.D)[ln];
         dA[n] = 0.f;
         kept[n] = 0.f;
     }
     // a wave loads the activations w, w + nw, .. of u, dt, dy, z
+    const int NP = nw * NC;
+    const float* const bcv = p.bc + b * p.L * (2 * NP) + nb;
+    float bn, cn;  // B and C of the next tile's tokens, token j and key dim n in lane 8 j + n
     Raw8<E> raw[ONE ? 4 : 2];
     auto fetch = [&](int t) {
         const BwdArgsPtr q = bwd_args();
@@ -313,6 +327,9 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
             if (i == 2) raw[k] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
             if (i == 3 && gate) raw[k] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
         }
+        const float* r = bcv + min(t + lane / NC, t1 - 1) * (2 * NP) + lane % NC;
+        bn = r[0];
+        cn = r[NP];
     };
     auto fetch_kept = [&](int t) {
         if (t <= t0) {
@@ -332,8 +349,7 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
         if (ONE) wave_lds_fence();
         else lds_barrier();
     };
-    const int NP = nw * NC;
-    scalar_f32 bcb = as_scalar_uniform(p.bc + b * p.L * (2 * NP) + nb);
+    scalar_f32 bcb = as_scalar_uniform(bcv);
     // where lane 4 i of the wave adds the i-th of its 16 sums over channels
     float* const dbcb = p.dbc + (cbi * p.B + b) * p.L * (2 * NP) + nb;
     const int dbco = (lane >> 2) < NC ? lane >> 2 : NP + (lane >> 2) - NC;
@@ -369,67 +385,75 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
         }
         barrier();
         // the state entering the tile, then the tile's states
-        float hs[T][NC], h[NC];
+        f32x4 hs[T][NC / 4], h[NC / 4];
 #pragma unroll
-        for (int n = 0; n < NC; n++) h[n] = fmaf(__builtin_amdgcn_exp2f(A2[n] * keptdt), hin[n], kept[n]);
+        for (int n = 0; n < NC; n++) h[n / 4][n % 4] = fmaf(__builtin_amdgcn_exp2f(A2[n] * keptdt), hin[n], kept[n]);
+        const float br[1] = {bn}, cr[1] = {cn};
         if (t > t0) {
             fetch(t - T);
             fetch_kept(t - T);
         }
-        // a token's row of B and C and its step size, one token ahead of their use (the fences keep the loads
-        // from sinking to it)
-        float row[2][2 * NC], dl_[2], du_[2], ds_[2];
+        // a token's step size and the row of C (forwards) or B (back), one token ahead of their use (the fences
+        // keep the loads from sinking to it)
+        float row[2][NC], dl_[2], du_[2], ds_[2];
         auto load_token = [&](int j, bool back) {
-            scalar_f32 q = bcb + min(t + j, t1 - 1) * (2 * NP);
+            scalar_f32 q = bcb + min(t + j, t1 - 1) * (2 * NP) + (back ? 0 : NP);
             const int k = j & 1;
 #pragma unroll
-            for (int n = 0; n < NC; n++) {
-                row[k][n] = q[n];
-                row[k][NC + n] = q[NP + n];
-            }
+            for (int n = 0; n < NC; n++) row[k][n] = q[n];
             dl_[k] = dls[j * 64 + lane];
             du_[k] = dus[j * 64 + lane];
             if (back) ds_[k] = dss[j * 64 + lane];
             __builtin_amdgcn_sched_barrier(0);
         };
         load_token(0, false);
-#pragma unroll
-        for (int j = 0; j < T; j++) {
+        static_for<T>([&](auto J) {
+            constexpr int j = J;
             const float dl = arrived(dl_[j & 1]), du = du_[j & 1];
-            if (j + 1 < T) load_token(j + 1, j + 2 == T);
+            if (j + 1 < T) load_token(j + 1, false);
             const float* rw = row[j & 1];
             float inner = 0.f;
+            static_for<NC / 4>([&](auto Q) {
+                constexpr int k = Q;
+                f32x4 c;
 #pragma unroll
-            for (int n = 0; n < NC; n++) {
-                h[n] = fmaf(__builtin_amdgcn_exp2f(dl * A2[n]), h[n], du * rw[n]);
-                hs[j][n] = h[n];
-                inner = fmaf(rw[NC + n], h[n], inner);
-            }
+                for (int i = 0; i < 4; i++) c[i] = __builtin_amdgcn_exp2f(dl * A2[4 * k + i]) * h[k][i];
+                h[k] = outer4<j * NC + 4 * k>(br, du, c);
+                hs[j][k] = h[k];
+#pragma unroll
+                for (int i = 0; i < 4; i++) inner = fmaf(rw[4 * k + i], h[k][i], inner);
+            });
             if (gate) sums[(w * 3 + 2) * SLOT + j * 64 + lane] = inner;
-        }
+        });
         // and back through them
-#pragma unroll
-        for (int j = T - 1; j >= 0; j--) {
+        load_token(T - 1, true);
+        static_for<T>([&](auto J) {
+            constexpr int j = T - 1 - J;
             const float* rw = row[j & 1];
             const float dl = arrived(dl_[j & 1]), du = du_[j & 1], ds = ds_[j & 1];
             if (j > 0) load_token(j - 1, true);
             float s1 = 0.f, s2 = 0.f, v[2 * NC];
+            static_for<NC / 4>([&](auto Q) {
+                constexpr int k = Q;
+                const f32x4 gn = outer4<j * NC + 4 * k>(cr, ds, adj[k]);
+                const f32x4 wv = outer4<j * NC + 4 * k>(br, -du, hs[j][k]);  // a S_{t-1}
 #pragma unroll
-            for (int n = 0; n < NC; n++) {
-                const float gn = fmaf(ds, rw[NC + n], adj[n]);
-                const float gw = gn * fmaf(-du, rw[n], hs[j][n]);
-                s1 = fmaf(gn, rw[n], s1);
-                s2 = fmaf(gw, A2[n], s2);
-                dA[n] = fmaf(gw, dl, dA[n]);
-                v[n] = gn * du;
-                v[NC + n] = ds * hs[j][n];
-                adj[n] = gn * __builtin_amdgcn_exp2f(dl * A2[n]);
-            }
+                for (int i = 0; i < 4; i++) {
+                    const int n = 4 * k + i;
+                    const float gw = gn[i] * wv[i];
+                    s1 = fmaf(gn[i], rw[n], s1);
+                    s2 = fmaf(gw, A2[n], s2);
+                    dA[n] = fmaf(gw, dl, dA[n]);
+                    v[n] = gn[i] * du;
+                    v[NC + n] = ds * hs[j][k][i];
+                    adj[k][i] = gn[i] * __builtin_amdgcn_exp2f(dl * A2[n]);
+                }
+            });
             sums[(w * 3) * SLOT + j * 64 + lane] = s1;
             sums[(w * 3 + 1) * SLOT + j * 64 + lane] = s2;
             const float s = wave_sums16(v);
             if (t + j < t1 && (lane & 3) == 0) (dbcb + (int64_t)(t + j) * (2 * NP))[dbco] = s;
-        }
+        });
         barrier();
         for (int j = w; j < T; j += nw) {
             const int at = j * 64 + lane;
@@ -469,7 +493,7 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
 #pragma unroll
     for (int n = 0; n < NC; n++) {
         (e->dap + (seg * NP + nb + n) * D + d0)[lane] = dA[n];
-        if (g == 0 && e->ds_in && nb + n < N) (e->ds_in + (b * N + nb + n) * D + d0)[lane] = adj[n];
+        if (g == 0 && e->ds_in && nb + n < N) (e->ds_in + (b * N + nb + n) * D + d0)[lane] = adj[n / 4][n % 4];
     }
     float* dd = e->ddp + ((seg * nw + w) * 2) * D + d0;
     dd[lane] = dDsum;
