@@ -11,7 +11,7 @@
 
 namespace {
 
-// The limits keep every launch below 2^32 threads and every byte offset far below 2^63.
+// The limits keep every launch below 2^32 threads in each dimension and every byte offset far below 2^63.
 constexpr int64_t kMaxB = 1 << 20, kMaxTokens = 1 << 24, kMaxChannels = 1 << 25, kMaxElems = (int64_t)1 << 35;
 constexpr int64_t kMaxNormRows = 1 << 25, kMaxNormElems = (int64_t)1 << 34, kMaxSpan = (int64_t)1 << 42;
 

@@ -197,6 +197,13 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_states_kernel(BwdDev p) {
     if (nb == 0) (e->sumdt + seg * D + d0)[lane] = sum;
 }
 
+// Blocks along x and z, so that the threads along one dimension stay below 2^32 (many channels and key dims).
+dim3 wide_grid(int64_t blocks, unsigned y) {
+    const int64_t x = std::min<int64_t>(blocks, 1 << 20);
+    return dim3((unsigned)x, y, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t wide_block() { return (int64_t)blockIdx.z * gridDim.x + blockIdx.x; }
+
 // Pass 2, per (b, n, d): states forwards (blockIdx.y = 0), adjoints backwards.  hin[0] takes s_in and hin[g]
 // the state entering segment g; gout[g] becomes the adjoint at segment g's end.
 template <int PARTS>
@@ -204,7 +211,7 @@ __global__ __launch_bounds__(64 * PARTS) void ssm_bwd_segments_kernel(const floa
                                                                const float* __restrict__ ds_out, const float* sumdt,
                                                                float* hin, float* gout, int64_t total, int64_t D, int N,
                                                                int NP, int G) {
-    const int64_t i0 = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int64_t i0 = wide_block() * 64 + (threadIdx.x & 63);
     const bool on = i0 < total;
     const int64_t i = on ? i0 : 0;
     const int64_t d = i % D, n = i / D % NP, b = i / (D * NP);
@@ -509,8 +516,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
                                                            float* __restrict__ dD, float* __restrict__ dbias, la_rows sdb,
                                                            la_rows sdc, int64_t B, int64_t L, int64_t D, int N, int NP, int G,
                                                            unsigned cb, unsigned nbc) {
-    if (blockIdx.x < nbc) {
-        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t block = wide_block();
+    if (block < nbc) {
+        const int64_t i = block * 256 + threadIdx.x;
         const int64_t row = i / (2 * NP);
         const int j = (int)(i % (2 * NP));
         if (row >= B * L) return;
@@ -530,8 +538,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
         return;
     }
     __shared__ float part[16][17];
-    const int64_t blocks = (D + 15) / 16, k = blockIdx.x - nbc;
+    const int64_t blocks = (D + 15) / 16, k = block - nbc;
     const int64_t n = k / blocks;
+    if (n >= N + 2) return;
     const int dl = threadIdx.x & 15, share = threadIdx.x >> 4;
     const int64_t d = k % blocks * 16 + dl;
     const bool isA = n < N;
@@ -622,7 +631,7 @@ hipError_t launch_e(const SsmArgs& a) {
         }
 #undef LA_SSM_STATES
         const int64_t total = a.B * p.NP * a.D;
-        const dim3 grid((unsigned)((total + 63) / 64), 2);
+        const dim3 grid = wide_grid((total + 63) / 64, 2);
 #define LA_SSM_SEGMENTS(n)                                                                                       \
     LA_TRACED(a.tr, "ssm_bwd_segments", ssm_bwd_segments_kernel<n><<<grid, 64 * n, 0, a.stream>>>(               \
                                             w.a2, a.s_in, a.ds_out, w.sumdt, w.hin, w.gout, total, a.D, a.N, p.NP, pl.G))
@@ -643,10 +652,10 @@ hipError_t launch_e(const SsmArgs& a) {
 #undef LA_SSM_MAIN
     }
     const unsigned nbc = (unsigned)((a.B * a.L * 2 * p.NP + 255) / 256);
-    const unsigned nd = (unsigned)((a.D + 15) / 16 * (a.N + 2));
+    const int64_t nd = (a.D + 15) / 16 * (a.N + 2);
     if (nbc + nd > 0)
         LA_TRACED(a.tr, "ssm_bwd_sums",
-                  ssm_bwd_sums_kernel<E><<<nbc + nd, 256, 0, a.stream>>>(w.dbc, w.dap, w.ddp, a.lengths, (E*)a.dB, (E*)a.dC,
+                  ssm_bwd_sums_kernel<E><<<wide_grid(nbc + nd, 1), 256, 0, a.stream>>>(w.dbc, w.dap, w.ddp, a.lengths, (E*)a.dB, (E*)a.dC,
                                                                          a.dA, a.dD, a.d_dt_bias, a.sdb, a.sdc, a.B, a.L,
                                                                          a.D, a.N, p.NP, pl.G, p.cb, nbc));
     return hipGetLastError();

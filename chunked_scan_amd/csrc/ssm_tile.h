@@ -108,13 +108,6 @@ __device__ __forceinline__ float arrived(float x) {
     return x;
 }
 
-// The same for a value in a scalar register.
-__device__ __forceinline__ void arrived_row(float& x) {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" : "+s"(x));
-    __builtin_amdgcn_sched_barrier(0);
-}
-
 // f(0), .., f(N - 1) with the index as a compile-time constant.
 template <typename F, int... I>
 __device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {

@@ -261,7 +261,7 @@ def selective_prompt(p: SelectiveParams, x: torch.Tensor, residual: Optional[tor
     zero behind a sequence's length, h [B, L, Dm] the residual stream, conv_state, s_out).  `saved`, a dict, receives what
     selective_backward takes."""
     B, L, Dm = x.shape
-    rows = lambda t: None if t is None else t.reshape(B * L, -1)  # noqa: E731
+    rows = lambda t: None if t is None else t.reshape(B * L, Dm)  # noqa: E731
     y, h, rstd = _norm_in(p, rows(x), rows(residual))
     u, z = (None if t is None else t.unflatten(0, (B, L)) for t in project_in(y))
     # rows behind a sequence's length are not written: they are zero here, so that a product over all rows
@@ -291,8 +291,8 @@ def selective_backward(p: SelectiveParams, saved: dict, dy: torch.Tensor, dbc_ba
     du, dcw, dcb, d_conv = la_short_conv_bwd(s["u"], p.conv_weight, dv, p.conv_bias, s["conv_state"], d_conv_state,
                                              lengths=s["lengths"])
     dn = in_backward(du, dz)
-    dx, dnw = la_add_norm_bwd(dn, s["h"], p.norm_weight, s["rstd"], None if dh is None else dh.reshape(B * L, -1))
-    return dict(dx=dx.view(B, L, -1), norm_weight=dnw, conv_weight=dcw, conv_bias=dcb, A=dA, skip=dskip,
+    dx, dnw = la_add_norm_bwd(dn, s["h"], p.norm_weight, s["rstd"], None if dh is None else dh.reshape(dn.shape))
+    return dict(dx=dx.view(B, L, dn.shape[1]), norm_weight=dnw, conv_weight=dcw, conv_bias=dcb, A=dA, skip=dskip,
                 dt_bias=d_dt_bias, conv_state=d_conv, s_in=ds_in)
 
 
@@ -300,7 +300,8 @@ def selective_token(p: SelectiveParams, x: torch.Tensor, residual: Optional[torc
                     project_dbc: Callable, conv_pool: torch.Tensor, state_pool: torch.Tensor,
                     slots: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """One layer over one token of each of B sequences, x [B, Dm]; conv_pool [S, W-1, D] and state_pool
-    [S, N, D] are updated in place at the rows' slots.  Returns (y [B, D], h [B, Dm])."""
+    [S, N, D] are updated in place at the rows' slots.  Returns (y [B, D], h [B, Dm]).  Rows that are padding (a
+    slot outside the pools, or one that an earlier row names) have undefined y."""
     y, h, _ = _norm_in(p, x, residual)
     u, z = project_in(y)
     v = la_short_conv_step(u, p.conv_weight, conv_pool, p.conv_bias, slots=slots)

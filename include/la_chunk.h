@@ -471,7 +471,7 @@ int64_t la_ssm_workspace(const la_ssm_shape* shape, int32_t backward);
  *        delta_t = dt_t + dt_bias, through softplus if shape->softplus
  *        S_t[n,d] = exp(delta_t[d] A[d,n]) S_{t-1}[n,d] + delta_t[d] u_t[d] B_t[n]
  *        y_t[d]   = (sum_n C_t[n] S_t[n,d] + Dskip[d] u_t[d]) z_t[d] / (1 + exp(-z_t[d]))
- *   u, dt : [B,L,D] dtype         A : float[D,N] (negative for a decay; not checked)
+ *   u, dt : [B,L,D] dtype         A : float[D,N], finite (negative for a decay; not checked)
  *   Bm, Cm: [B,L,N] dtype         Dskip, dt_bias : float[D] or NULL (zero)
  *   z     : [B,L,D] dtype or NULL (no gate)        s_in : float[B,N,D] initial state or NULL (zero)
  *   y     : [B,L,D] dtype, written                  s_out: float[B,N,D] final state or NULL; may be

@@ -371,6 +371,28 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(y0, y1) and torch.equal(pool[S - 1], st[1]) and torch.equal(pool[0], st[0])
 
 
+def test_scan_backward_of_the_most_channels():
+    """The widest batch there is, at a state size that takes the sums past 2^32 threads: channels from the start, the
+    middle and the end against the oracle on those channels alone (what is summed over channels is left out)."""
+    note("scan backward, 2^25 channels")
+    D, N = 1 << 25, 33
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    rnd = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    u, dt, dy = rnd(1, 1, D), rnd(1, 1, D), rnd(1, 1, D)
+    Bm, C = rnd(1, 1, N), rnd(1, 1, N)
+    A = torch.rand(D, N, generator=g, device="cuda").neg_()
+    s_in = torch.rand(1, N, D, generator=g, device="cuda")
+    du, ddt, dA, _, _, _, _, _, ds_in = la.la_ssm_scan_bwd(u, dt, A, Bm, C, dy, s_in=s_in)
+    at = torch.cat([torch.arange(k, k + 70) for k in (0, (1 << 24) - 3, D - 70)]).cuda()
+    pick = lambda t: R.f64(t[..., at])  # noqa: E731
+    args = (pick(u), pick(dt), R.f64(A[at]), R.f64(Bm), R.f64(C), None, None, None, pick(s_in), None, True, pick(dy),
+            np.zeros((1, N, 210)))
+    r, m = R.scan_bwd(*args), R.scan_bwd(*args, mag=True)
+    for name, got, k in (("du", du[..., at], 0), ("ddt", ddt[..., at], 1), ("dA", dA[at], 2), ("ds_in", ds_in[..., at], 8)):
+        R.close(got, r[k], m[k], 8 + 64, F32, name)
+
+
 # ------------------------------------------------------------------------------------ norm
 
 NORM = [(1, 8, False), (3, 64, False), (5, 1000, False), (2, 7, False), (4, 130, True), (9, 2048, False), (2, 2056, True),
@@ -534,6 +556,24 @@ def test_layer_in_pieces_equals_one_prompt():
     assert ((got - ref).abs() <= 2.0 ** -7 * ref.abs() + 3 * (8 * L + 64) * R.U * float(ref.abs().max()) * 8).all()
     assert torch.equal(torch.cat([a[1], b[1]], 1), h) and torch.equal(b[2], cs)
     assert float((b[3] - so).abs().max()) <= 3 * (8 * L + 64) * R.U * float(so.abs().max()) * 8
+
+
+@pytest.mark.parametrize("B,L", [(0, 5), (2, 0)])
+def test_layer_of_no_tokens(B, L):
+    """An empty batch and prompts of no tokens: states pass through, gradients of the parameters are zero."""
+    note(f"layer: {B} prompts of {L}")
+    D, N, W = 64, 16, 4
+    p, pin, pdbc, _, _ = layer(D, N, W, 60)
+    g = Draw(61)
+    x, cs, s = g.normal(B, L, D), g.normal(B, W - 1, D), g.normal(B, N, D)
+    saved = {}
+    o, h, c1, s1 = pipeline.selective_prompt(p, x, x, pin, pdbc, conv_state=cs, s_in=s, saved=saved)
+    assert o.shape == (B, L, D) and h.shape == (B, L, D) and torch.equal(c1, cs) and torch.equal(s1, s)
+    gr = pipeline.selective_backward(p, saved, o, lambda ddt, dB, dC: ddt, lambda du, dz: du.reshape(B * L, D),
+                                     d_conv_state=cs, ds_out=s)
+    assert gr["dx"].shape == (B, L, D) and torch.equal(gr["conv_state"], cs) and torch.equal(gr["s_in"], s)
+    for k in ("norm_weight", "conv_weight", "conv_bias", "A", "skip", "dt_bias"):
+        assert (gr[k] == 0).all(), k
 
 
 def test_layer_gradients_against_differences():
