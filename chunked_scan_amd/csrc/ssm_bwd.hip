@@ -108,20 +108,23 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_states_kernel(BwdDev p) {
     // B and C of the tile's tokens, value j NC + n in lane (j NC + n) % 64, and the next tile's
     constexpr int BV = T * NC / 64;
     float br[BV], cr[BV], bn[BV], cn[BV];
+    const TileRow row_u(p.su, pl), row_dt(p.sdt, pl), row_dy(p.sdy, pl), row_z(p.sz, pl);
     Raw8<E> raw[4];
     auto fetch = [&](int t) {
         const BwdArgsPtr q = bwd_args();
-        const int tt = min(t + pl.token, t1 - 1);
-        raw[0] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
-        raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
-        raw[2] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
-        if (gate) raw[3] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
+        const int left = t1 - t;
+        raw[0] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + t * q->su.token + d0, row_u, q->su.token, left, pl);
+        raw[1] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + t * q->sdt.token + d0, row_dt, q->sdt.token, left, pl);
+        raw[2] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + t * q->sdy.token + d0, row_dy, q->sdy.token, left, pl);
+        if (gate)
+            raw[3] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + t * q->sz.token + d0, row_z, q->sz.token, left, pl);
+        const float* const rows = bcb + t * (2 * NP);
 #pragma unroll
         for (int v = 0; v < BV; v++) {
             const int e = v * 64 + lane;
-            const float* r = bcb + min(t + e / NC, t1 - 1) * (2 * NP) + e % NC;
-            bn[v] = r[0];
-            cn[v] = r[NP];
+            const int at = left >= T ? e / NC * (2 * NP) + e % NC : min(e / NC, left - 1) * (2 * NP) + e % NC;
+            bn[v] = rows[at];
+            cn[v] = rows[at + NP];
         }
     };
     float sum = 0.f;
@@ -329,10 +332,10 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
 #pragma unroll
         for (int k = 0; k < (ONE ? 4 : 2); k++) {
             const int i = w + k * nw;
-            if (i == 0) raw[k] = tile_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
-            if (i == 1) raw[k] = tile_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
-            if (i == 2) raw[k] = tile_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
-            if (i == 3 && gate) raw[k] = tile_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
+            if (i == 0) raw[k] = token_load<E, VEC>((const E*)q->u + b * q->su.batch + d0, q->su.token, tt, pl);
+            if (i == 1) raw[k] = token_load<E, VEC>((const E*)q->dt + b * q->sdt.batch + d0, q->sdt.token, tt, pl);
+            if (i == 2) raw[k] = token_load<E, VEC>((const E*)q->dy + b * q->sdy.batch + d0, q->sdy.token, tt, pl);
+            if (i == 3 && gate) raw[k] = token_load<E, VEC>((const E*)q->z + b * q->sz.batch + d0, q->sz.token, tt, pl);
         }
         const float* r = bcv + min(t + lane / NC, t1 - 1) * (2 * NP) + lane % NC;
         bn = r[0];
