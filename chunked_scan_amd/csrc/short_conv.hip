@@ -415,7 +415,7 @@ bool rows16(const void* p, la_rows r, size_t es) {
 
 // Tokens per thread: 16 in the forward and 32 in the backward (which writes W + 1 sums per channel and tile),
 // fewer where that leaves under 2048 waves, two per SIMD.  Each tile re-reads W - 1 rows and loads the taps:
-// 16384 x 2048 bf16, W = 4: 8 tokens 35 us, 16 30, 32 33, 64 33; backward of 8192 x 2048: 16 tokens 38 + 8 us
+// 16384 x 2048 bf16, W = 4, ordinary stores: 8 tokens 35 us, 16 30, 32 33, 64 33; backward of 8192 x 2048: 16 tokens 38 + 8 us
 // for the sums, 32 29 + 5, 64 32 + 4.
 int tile_tokens(int64_t B, int64_t L, int64_t nvec, int TL) {
     while (TL > 8 && B * ((L + TL - 1) / TL) * nvec < 2048 * 64) TL /= 2;
