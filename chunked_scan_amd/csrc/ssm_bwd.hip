@@ -575,8 +575,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
 int np_for(int N) { return (N + NW8 - 1) / NW8 * NW8; }
 
 // Segments: about 6144 waves in the main pass (NP / 8 to a channel block), two rounds of what fits the device
-// at once, none under 16 tokens.  2 x 4096 tokens x 2048 channels, N = 16, main and first pass: 3072 waves 302 +
-// 143 us, 6144 304 + 104, 9216 299 + 98 (and 4 us more in the sums over segments).
+// at once, none under 16 tokens.  2 x 4096 tokens x 2048 channels, N = 16, main and first pass: half as many
+// waves 302 + 143 us, 6144 304 + 104, half as many again 299 + 98 (and 4 us more in the sums over segments).
 SsmPlan bwd_plan(int64_t B, int64_t L, int64_t D, int NP) { return ssm_plan(B, L, D, 6144 / (NP / NW8), 16, T); }
 
 struct BwdWs {
