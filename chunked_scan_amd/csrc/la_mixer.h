@@ -38,7 +38,7 @@ struct ConvArgs {
     Tracer* tr;
 };
 hipError_t launch_short_conv(const ConvArgs& a);
-size_t short_conv_bwd_ws(int64_t B, int64_t L, int64_t D, int width, bool bf16);
+size_t short_conv_bwd_ws(int64_t B, int64_t L, int64_t D, int width);
 hipError_t launch_short_conv_bwd(const ConvArgs& a);
 hipError_t launch_short_conv_step(const ConvArgs& a);
 

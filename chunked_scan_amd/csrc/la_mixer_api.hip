@@ -244,7 +244,7 @@ la_status la_short_conv(const void* x, const float* weight, const float* bias, c
 int64_t la_short_conv_bwd_workspace(const la_conv_shape* s) {
     const la_status st = conv_shape(s, false);
     if (st != LA_OK) return st;
-    return (int64_t)la::short_conv_bwd_ws(s->B, s->L, s->D, s->width, s->dtype == LA_BF16);
+    return (int64_t)la::short_conv_bwd_ws(s->B, s->L, s->D, s->width);
 }
 
 la_status la_short_conv_bwd(const void* x, const float* weight, const float* bias, const void* state_in,
@@ -257,7 +257,7 @@ la_status la_short_conv_bwd(const void* x, const float* weight, const float* bia
     if (n > 0 && (!x || !dy || !dx)) return LA_ERR_NULL;
     if (s->D > 0 && (!weight || !d_weight)) return LA_ERR_NULL;
     if (!rows_ok(s, s->x, s->L) || !rows_ok(s, s->dy, s->L) || !rows_ok(s, s->dx, s->L)) return LA_ERR_SHAPE;
-    const size_t need = la::short_conv_bwd_ws(s->B, s->L, s->D, s->width, s->dtype == LA_BF16);
+    const size_t need = la::short_conv_bwd_ws(s->B, s->L, s->D, s->width);
     if (ws_bad(workspace, workspace_bytes, need)) return LA_ERR_WORKSPACE;
     la::ConvArgs a = conv_args(s, s->L);
     const size_t es = esize(s->dtype);

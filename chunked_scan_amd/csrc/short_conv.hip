@@ -496,7 +496,7 @@ hipError_t run(What what, const ConvArgs& a) { return a.bf16 ? run<__bf16>(what,
 
 // One row of W + 1 sums per token tile; the scalar form has the most threads and the longest tiles, so
 // the vector form's count bounds both.
-size_t short_conv_bwd_ws(int64_t B, int64_t L, int64_t D, int width, bool bf16) {
+size_t short_conv_bwd_ws(int64_t B, int64_t L, int64_t D, int width) {
     const int64_t nvec = std::max<int64_t>(1, D / 4);
     const int TL = bwd_tile(B, L, nvec);
     return (size_t)(B * std::max<int64_t>(1, (L + TL - 1) / TL) * (width + 1) * D) * sizeof(float);

@@ -24,8 +24,9 @@
 // halving: every exchange adds two registers into one (about 35 instructions against 170 of the recurrence).
 //
 // Bound by vector issue: the decays' exponentials (16 cycles a wave) are formed once in pass 1 and twice in pass
-// 3, which has no registers to keep them.  2 x 4096 tokens x 2048 channels, N = 16, bf16 with a gate: packing 5 us,
-// states 93, segments 13, main 290, sums 13; what it must read and write is 55 us at a copy's rate.
+// 3, which has no registers to keep them at three waves per SIMD (kept, at two waves, 330 us against 312 in the
+// same session).  2 x 4096 tokens x 2048 channels, N = 16, bf16 with a gate: packing 5 us, states 93, segments 13,
+// main 290 to 310, sums 13; what it must read and write is 55 us at a copy's rate.
 #include "la_mixer.h"
 #include "ssm_common.h"
 #include "ssm_tile.h"
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(64, 2) void ssm_bwd_states_kernel(BwdDev p) {
         wave_lds_fence();
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            if (i < 3 || gate) *lds_chunk(tile[i], pl) = raw[i];
+            if (i < 3 || gate) *lds_chunk(tile[i]) = raw[i];
         wave_lds_fence();
         float dl[T], du[T], ds[T];
 #pragma unroll
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
 #pragma unroll
         for (int k = 0; k < (ONE ? 4 : 2); k++) {
             const int i = w + k * nw;
-            if (i < 3 || (i == 3 && gate)) *lds_chunk(tile + i * SLOT, pl) = raw[k];
+            if (i < 3 || (i == 3 && gate)) *lds_chunk(tile + i * SLOT) = raw[k];
         }
         barrier();
         for (int j = w; j < T; j += nw) {
@@ -493,10 +494,10 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
         const int tt = t + pl.token;
         if (pl.in && tt < t1 && (ONE || pl.token % nw == w)) {  // the wave's own tokens
             const BwdArgsPtr q = bwd_args();
-            store8<VEC>((E*)q->du + b * q->sdu.batch + d0 + tt * q->sdu.token + pl.col, pl.n, *lds_chunk(tile + 2 * SLOT, pl));
-            store8<VEC>((E*)q->ddt + b * q->sddt.batch + d0 + tt * q->sddt.token + pl.col, pl.n, *lds_chunk(tile + SLOT, pl));
+            store8<VEC>((E*)q->du + b * q->sdu.batch + d0 + tt * q->sdu.token + pl.col, pl.n, *lds_chunk(tile + 2 * SLOT));
+            store8<VEC>((E*)q->ddt + b * q->sddt.batch + d0 + tt * q->sddt.token + pl.col, pl.n, *lds_chunk(tile + SLOT));
             if (gate)
-                store8<VEC>((E*)q->dz + b * q->sdz.batch + d0 + tt * q->sdz.token + pl.col, pl.n, *lds_chunk(tile + 3 * SLOT, pl));
+                store8<VEC>((E*)q->dz + b * q->sdz.batch + d0 + tt * q->sdz.token + pl.col, pl.n, *lds_chunk(tile + 3 * SLOT));
         }
         if (ONE) wave_lds_fence();
     }

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(64, 2) void ssm_fwd_kernel(FwdDev p) {
         wave_lds_fence();
 #pragma unroll
         for (int i = 0; i < NS; i++)
-            if (i < 2 || gate) *lds_chunk(tile[i], pl) = raw[i];
+            if (i < 2 || gate) *lds_chunk(tile[i]) = raw[i];
         if (STATE)
 #pragma unroll
             for (int v = 0; v < BV; v++) brow[v * 64 + lane] = bn[v];
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(64, 2) void ssm_fwd_kernel(FwdDev p) {
         if (pl.in && t + pl.token < t1) {
             const FwdArgsPtr q = fwd_args();
             store8<VEC>((E*)q->y + b * q->sy.batch + d0 + (t + pl.token) * q->sy.token + pl.col, pl.n,
-                        *lds_chunk(tile[3], pl));
+                        *lds_chunk(tile[3]));
         }
     }
     if (!live) return;

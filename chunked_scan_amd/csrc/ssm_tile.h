@@ -107,7 +107,7 @@ __device__ __forceinline__ Raw8<E> token_load(const E* p, int64_t stride, int t,
 }
 // The lane's 8 channels in an LDS tile [TT][64].
 template <typename E>
-__device__ __forceinline__ Raw8<E>* lds_chunk(E* tile, const TilePlace& pl) {
+__device__ __forceinline__ Raw8<E>* lds_chunk(E* tile) {
     return reinterpret_cast<Raw8<E>*>(tile + (threadIdx.x & 63) * 8);
 }
 
