@@ -687,3 +687,60 @@ def test_traced_kernels():
     torch.cuda.synchronize()
     names = [n for n, ms in timer.harvest()]
     assert names == ["short_conv_bwd", "short_conv_bwd_sums"]
+
+
+def test_token_step_in_two_graphs():
+    """Single tokens captured into two graphs of one memory pool, replayed in turn with other inputs and other slots (a
+    padding row and a slot named twice among them), eager steps on a second pool of states between: every replay gives
+    what the eager step gives."""
+    note("token: graphs")
+    D, N, W, S = 128, 16, 4, 6
+    p, pin, pdbc, _, _ = layer(D, N, W, 70)
+    g = Draw(71)
+    pools = [g.normal(S, W - 1, D), g.normal(S, N, D)]
+    mine = [t.clone() for t in pools]
+    shapes = [3, 5]
+    graphs, bufs, mem = [], [], None
+    for B in shapes:
+        b = dict(x=g.normal(B, D), res=g.normal(B, D), slots=torch.full((B,), -1, dtype=torch.int32, device="cuda"))
+        pipeline.selective_token(p, b["x"], b["res"], pin, pdbc, *mine, b["slots"])  # all padding: changes no state
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, pool=mem):
+            b["y"], b["h"] = pipeline.selective_token(p, b["x"], b["res"], pin, pdbc, *mine, b["slots"])
+        mem = mem or gr.pool()
+        graphs.append(gr)
+        bufs.append(b)
+    for t, m in zip(pools, mine):
+        assert torch.equal(t, m)
+    turns = [(0, [4, 0, 2]), (1, [5, 1, -1, 3, 1]), (0, [0, 0, 9]), (1, [0, 1, 2, 3, 4]), (0, [5, 4, 3])]
+    for k, slots in turns:
+        b = bufs[k]
+        x, res = g.normal(*b["x"].shape), g.normal(*b["x"].shape)
+        for name, v in (("x", x), ("res", res), ("slots", ints(slots))):
+            b[name].copy_(v)
+        graphs[k].replay()
+        y, h = pipeline.selective_token(p, x, res, pin, pdbc, *pools, ints(slots))
+        torch.cuda.synchronize()
+        live = [i for i, s in enumerate(slots) if 0 <= s < S and s not in slots[:i]]
+        assert torch.equal(b["y"][live], y[live]) and torch.equal(b["h"], h)
+        for t, m in zip(pools, mine):
+            assert torch.equal(t, m)
+
+
+def test_scan_on_a_given_stream():
+    """stream= for calls with workspaces: two at once on two streams, outputs and scratch of their own."""
+    note("scan: stream argument")
+    case = (2, 333, 72, 16, None, False, True, True, True, True, True)
+    sets = [scan_inputs(case, BF, 80 + i)[0] for i in range(2)]
+    args = lambda a: [a[k] for k in ("u", "dt", "A", "B", "C")]  # noqa: E731
+    kw = lambda a: {k: a[k] for k in ("D", "z", "dt_bias", "s_in")}  # noqa: E731
+    want = [(la.la_ssm_scan(*args(a), **kw(a)), la.la_ssm_scan_bwd(*args(a), a["dy"], **kw(a))) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [(la.la_ssm_scan(*args(a), **kw(a), stream=s), la.la_ssm_scan_bwd(*args(a), a["dy"], **kw(a), stream=s))
+           for a, s in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for w, v in zip(want, got):
+        for a, b in zip(w[0] + w[1], v[0] + v[1]):
+            assert torch.equal(a, b)
