@@ -6,7 +6,7 @@
 // Memory-bound: every input element is read once into registers and every output written once.  A row
 // belongs to TPR threads (one wave for short rows, whose reductions need no barrier; four or
 // sixteen for long ones), each holding VPT chunks of 8 adjacent elements in fp32.  16384 x 2048 bf16 with the sum
-// kept and 8-bit output: 236 MB in 53.4 us, 4.4 TB/s, where a large copy reaches 4.8.
+// kept and 8-bit output: 236 MB in 54.3 us, 4.3 TB/s, where a large copy reaches 4.8.
 #include <algorithm>
 
 #include "la_mixer.h"
@@ -16,7 +16,7 @@ namespace {
 
 // 8 adjacent elements, of which `n` exist; VEC: 16-byte words (the row is aligned and whole chunks exist).
 // ONCE: a streaming load.  The forward's rows are read once and its outputs are what comes next: 16384 x 2048 bf16 to
-// 8 bits, call after call, 62.6 -> 53.4 us, single launches 55.9 -> 54.6.  (With the outputs streamed as well 54.6; the
+// 8 bits, call after call, 62.6 -> 53.4 us (before the exact quotients), single launches 55.9 -> 54.6.  (With the outputs streamed as well 54.6; the
 // backward 35.2 -> 35.7.)
 template <typename V, bool ONCE>
 __device__ __forceinline__ V load_word(const V* p) {
@@ -132,6 +132,22 @@ __device__ __forceinline__ float inv_sqrt(float v) {
     return n == n ? n : r;  // v = 0 or infinite: the estimate is exact
 }
 
+// y / s, inv its reciprocal, cut to fp32 and marked in its last bit where it is inexact, so that a conversion to e4m3
+// rounds the quotient itself: rounded to nearest in fp32 first, one next to a tie of e4m3 could land on the tie or
+// across it.  y inv is off by at most 2 steps, the first residual brings it within one, the second is its side's sign.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+    float q = y * inv;
+    q = fmaf(fmaf(-q, s, y), inv, q);
+    const float rem = fmaf(-q, s, y);
+    uint32_t b = __float_as_uint(q);
+    b -= __uint_as_float(__float_as_uint(rem) ^ (b & 0x80000000u)) < 0.f;  // q is past y / s: the value before it
+    b |= rem != 0.f;
+    return __uint_as_float(b);
+}
+// Below TIE_NEAR where f is within 4 steps of a tie of e4m3's normal values (mantissa bits xxx1000...).
+constexpr uint32_t TIE_NEAR = 8u << 12;
+__device__ __forceinline__ uint32_t tie_distance(float f) { return (__float_as_uint(f) << 12) - (0x80000000u - (4u << 12)); }
+
 // Y8: 8-bit output.  Blocks of max(TPR, 256) threads hold 256 / TPR rows when TPR = 64, else one.
 template <typename E, int TPR, int VPT, bool VEC, bool Y8>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev p) {
@@ -200,14 +216,33 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev
         if (n <= 0) continue;
         const float s = amax > 0.f || amax != amax ? amax / 448.f : 1.f;
         if (p.group ? d % p.group == 0 : d == 0) p.scale[p.group ? m * (p.D / p.group) + d / p.group : m] = s;
-        // y / s through one reciprocal per group (2 ulp of fp32 against e4m3's half step of 2^-4); a scale
-        // so small that its reciprocal would overflow is first moved up, with y, by a power of two
-        const float up = s < 0x1p-100f ? 0x1p+64f : 1.f;
-        const float inv = 1.f / (s * up);
-        uint32_t c[2];
-        float f[8];
+        // y / s through one reciprocal per group, exact where that could miss a tie: next to one of the normal values, or
+        // in e4m3's subnormal range, below 2^-6 (2^-15 of the group's largest), where the ties lie otherwise.  16384 x 2048
+        // bf16 in groups of 128: 54.3 us, exact for all 56.3, for none 53.4.  A scale so small that its reciprocal would
+        // overflow, or the quotient's residual not be exact, is first moved up, with y, by a power of two; in a group
+        // with an infinite scale finite values give 0.
+        float su = s;
+        if (s < 0x1p-60f) {
+            su *= 0x1p+64f;
 #pragma unroll
-        for (int j = 0; j < 8; j++) f[j] = fminf(fmaxf(h[i][j] * up * inv, -448.f), 448.f);
+            for (int j = 0; j < 8; j++) h[i][j] *= 0x1p+64f;
+        }
+        const float inv = 1.f / su;
+        float f[8];
+        uint32_t near = ~0u;
+        float least = INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            f[j] = h[i][j] * inv;
+            near = min(near, tie_distance(f[j]));
+            least = fminf(least, fabsf(f[j]));
+        }
+        if ((near < TIE_NEAR || least < 0x1p-6f) && su < INFINITY)
+#pragma unroll
+            for (int j = 0; j < 8; j++) f[j] = quotient(h[i][j], su, inv);
+        uint32_t c[2];
+#pragma unroll
+        for (int j = 0; j < 8; j++) f[j] = __builtin_amdgcn_fmed3f(f[j], -448.f, 448.f);  // a NaN: -448
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k], f[4 * k + 1], 0, false);

@@ -1,0 +1,52 @@
+"""The short convolution, the selective scan and the residual norm where the ordinary cases of test_gpu_mixer.py do not
+look: values next to a tie of the 8-bit output, strong decays, values at the ends of fp32's range, padding that is
+not finite, and the sizes from which the kernels take their wide forms."""
+import numpy as np
+import pytest
+import torch
+
+import mixer_ref as R
+from chunked_scan_amd import binding as la
+from gpu_util import note
+from test_gpu_mixer import BF, F32, Draw
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------ norm
+
+
+def e4m3(v):
+    """The nearest e4m3 value, ties to even, of values given in fp64.  A quotient of two fp32 numbers that is not a
+    tie of e4m3 differs from it by 2^-29 of its size at least (24 bits against 24 + 5), so fp64's rounding of the
+    quotient never makes one."""
+    a = np.minimum(np.abs(v), 448.0)
+    step = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(a, 2.0 ** -6))), -6) - 3)
+    return np.round(a / step) * step * np.sign(v)
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_q8_rounds_the_quotient_itself(group):
+    """The codes are the nearest ones to y / scale, y being what la_add_norm gives in fp32 and scale the returned one:
+    values within a few fp32 steps of every tie of e4m3, normal and subnormal, at scales over many octaves, are
+    rounded to the right side of it."""
+    note(f"norm q8 at ties {group}")
+    ties = [(m + 0.5) * 2.0 ** -9 for m in range(8)]
+    ties += [(8 + m + 0.5) * 2.0 ** (e - 3) for e in range(-6, 9) for m in range(8) if (8 + m + 0.5) * 2.0 ** (e - 3) < 448]
+    base = np.array(ties, np.float32) / np.float32(448.0)
+    near = np.concatenate([(base.view(np.int32) + k).view(np.float32) for k in range(-4, 5)])
+    near = near[: len(near) // 127 * 127].reshape(-1, 127)  # every group of 128 leads with its largest, 1
+    w = torch.from_numpy(np.concatenate([np.ones((len(near), 1), np.float32), near], 1).reshape(-1)).cuda()
+    D, M = w.numel(), 96
+    g = Draw(5)
+    # rows of one value a: r = 1 / sqrt(a^2 + eps), so y / weight moves over many octaves as a falls below sqrt(eps)
+    a = torch.exp2(g.uniform(M, lo=-110.0, hi=3.0))
+    x = (a[:, None] * torch.where(g.uniform(M, D) < 0.5, -1.0, 1.0)).contiguous()
+    y, _, _ = la.la_add_norm(x, w)
+    q, s, _, _ = la.la_add_norm_q8(x, w, group=group)
+    y, s = y.cpu().numpy(), s.cpu().numpy()
+    same = s == np.abs(y).reshape(M, -1, group or D).max(2) / np.float32(448.0)
+    assert same.all(), (same.size, same.sum())
+    v = y.astype(np.float64) / np.repeat(s.astype(np.float64), group or D, 1)
+    same = q.to(F32).cpu().double().numpy() == e4m3(v)
+    assert same.all(), (same.size, same.sum())
