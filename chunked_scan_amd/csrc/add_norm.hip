@@ -214,7 +214,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev
             else amax = lanes_max<4>(amax);
         }
         if (n <= 0) continue;
-        const float s = amax > 0.f || amax != amax ? amax / 448.f : 1.f;
+        const float top = amax / 448.f;
+        const float s = top > 0.f || top != top ? top : 1.f;  // also where the quotient underflows
         if (p.group ? d % p.group == 0 : d == 0) p.scale[p.group ? m * (p.D / p.group) + d / p.group : m] = s;
         // y / s through one reciprocal per group, exact where that could miss a tie: next to one of the normal values, or
         // in e4m3's subnormal range, below 2^-6 (2^-15 of the group's largest), where the ties lie otherwise.  16384 x 2048

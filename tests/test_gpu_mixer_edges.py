@@ -50,3 +50,19 @@ def test_norm_q8_rounds_the_quotient_itself(group):
     v = y.astype(np.float64) / np.repeat(s.astype(np.float64), group or D, 1)
     same = q.to(F32).cpu().double().numpy() == e4m3(v)
     assert same.all(), (same.size, same.sum())
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_norm_q8_scale_that_underflows(group):
+    """Where the largest |y| / 448 is zero in fp32 the scale is 1 and the codes are zero, also for values that are not
+    zero themselves (subnormal ones); next to such a group an ordinary one."""
+    note(f"norm q8 underflow {group}")
+    w = torch.full((64,), 1e-44, device="cuda")
+    if group:
+        w[32:] = 1.0
+    x = Draw(9).normal(5, 64)
+    q, s, _, _ = la.la_add_norm_q8(x, w, group=group)
+    tiny = 32 if group else 64
+    assert (s[:, 0] == 1).all() and (q[:, :tiny].float() == 0).all()
+    if group:
+        assert (s[:, 1] < 1).all() and (q[:, 32:].float().abs().amax(1) == 448).all()
