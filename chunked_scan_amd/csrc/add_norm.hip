@@ -124,12 +124,16 @@ struct NormDev {
     int64_t sx, sres, sy, sh, sdy, sdh, sdx;
 };
 
-// 1 / sqrt(v), correctly rounded to about an ulp: the hardware estimate and one Newton step.
+// 1 / sqrt(v) to about an ulp: the hardware estimate and one Newton step.  The estimate takes a subnormal v for zero:
+// small ones are moved up by a power of two.
 __device__ __forceinline__ float inv_sqrt(float v) {
+    const bool small = v < 0x1p-100f;
+    v = small ? v * 0x1p+64f : v;
     const float r = __builtin_amdgcn_rsqf(v);
     const float e = fmaf(-v * r, r, 1.f);
     const float n = fmaf(r * 0.5f, e, r);
-    return n == n ? n : r;  // v = 0 or infinite: the estimate is exact
+    const float x = n == n ? n : r;  // v infinite: the estimate is exact
+    return small ? x * 0x1p+32f : x;
 }
 
 // y / s, inv its reciprocal, cut to fp32 and marked in its last bit where it is inexact, so that a conversion to e4m3

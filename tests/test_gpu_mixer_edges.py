@@ -66,3 +66,17 @@ def test_norm_q8_scale_that_underflows(group):
     assert (s[:, 0] == 1).all() and (q[:, :tiny].float() == 0).all()
     if group:
         assert (s[:, 1] < 1).all() and (q[:, 32:].float().abs().amax(1) == 448).all()
+
+
+def test_norm_with_a_subnormal_eps():
+    """Rows of zeros and a row of ones with an eps below fp32's normal range: 1 / sqrt(eps) is finite, and zeros stay
+    zeros.  K as in test_gpu_mixer.py."""
+    note("norm: subnormal eps")
+    eps = float(np.float32(1e-40))
+    x = torch.zeros(3, 64, device="cuda")
+    x[1] = 1.0
+    w = 1 + Draw(2).normal(64, std=0.1)
+    y, _, r = la.la_add_norm(x, w, eps=eps)
+    ry, _, rr = R.norm(R.f64(x), None, R.f64(w), eps)
+    R.close(y, ry, np.abs(ry), 64 / 8 + 32, F32, "y")
+    R.close(r, rr, np.abs(rr), 64 / 8 + 32, F32, "rstd")
