@@ -183,7 +183,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
     }
-    const float r = inv_sqrt(fmaf(row_sum<TPR>(ss, buf), p.inv_d, p.eps));
+    ss = row_sum<TPR>(ss, buf);
+    float r;
+    if (ss < INFINITY) {
+        r = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
+    } else {  // squares past fp32 (values of 1e19 and more): the sum of (h 2^-64)^2.  All threads of the row come here.
+        float s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; i++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float v = h[i][j] * 0x1p-64f;
+                s2 = fmaf(v, v, s2);
+            }
+        r = inv_sqrt(fmaf(row_sum<TPR>(s2, buf), p.inv_d, p.eps * 0x1p-64f * 0x1p-64f)) * 0x1p-64f;
+    }
     if (p.rstd && tid == 0) p.rstd[m] = r;
     float amax = 0.f;
 #pragma unroll

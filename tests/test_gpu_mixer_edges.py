@@ -80,3 +80,30 @@ def test_norm_with_a_subnormal_eps():
     ry, _, rr = R.norm(R.f64(x), None, R.f64(w), eps)
     R.close(y, ry, np.abs(ry), 64 / 8 + 32, F32, "y")
     R.close(r, rr, np.abs(rr), 64 / 8 + 32, F32, "rstd")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [7, 64, 4096, 16384])
+def test_norm_of_values_whose_squares_overflow(D, dtype):
+    """Rows of 1e19 to 1e37 between ordinary ones: the statistics hold, forward, 8 bits and backward.  K as in
+    test_gpu_mixer.py."""
+    note(f"norm: large values {D} {dtype}")
+    g = Draw(D)
+    M = 6
+    scale = torch.tensor([1.0, 1e25, 1.0, 1e36, 1e19, 1e30], device="cuda")[:, None]
+    x, w = (g.normal(M, D) * scale).to(dtype), 1 + g.normal(D, std=0.2)
+    y, h, r = la.la_add_norm(x, w)
+    ry, _, rr = R.norm(R.f64(x), None, R.f64(w), 1e-5)
+    K = D / 8 + 32
+    R.close(y, ry, np.abs(ry), K, dtype, "y")
+    assert (np.abs(R.f64(r) - rr) <= (K + 1) * R.U * rr).all()
+    q, s, _, r8 = la.la_add_norm_q8(x, w)
+    assert torch.equal(r8, r)
+    top = np.abs(ry).max(1, keepdims=True) / 448
+    assert (np.abs(R.f64(s) - top) <= (K + 3) * R.U * top).all()
+    dy = g.normal(M, D, dtype=dtype)
+    dx, dw = la.la_add_norm_bwd(dy, h, w, r)
+    args = (R.f64(dy), R.f64(h), R.f64(w), R.f64(r), None)
+    (rx, rw), (mx, mw) = R.norm_bwd(*args), R.norm_bwd(*args, mag=True)
+    R.close(dx, rx, mx, K, dtype, "dx")
+    R.close(dw, rw, mw, K + M, F32, "dw")
