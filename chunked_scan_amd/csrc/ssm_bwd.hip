@@ -1,6 +1,6 @@
 // ssm_bwd.hip -- the selective scan's backward pass.
 //
-// With ds_t = dy_t silu(z_t), W_t = a_t S_{t-1} = S_t - delta_t u_t B_t and the adjoint of the state
+// With ds_t = dy_t silu(z_t), W_t = a_t S_{t-1} and the adjoint of the state
 //   G_t = C_t ds_t + a_{t+1} G_{t+1}          (G after the last token: ds_out)
 // the derivatives are
 //   du = D ds + delta sum_n G B,   d delta = u sum_n G B + sum_n G W A,   dA = sum_t G W delta,
@@ -18,15 +18,16 @@
 //
 // A lane owns a channel as in the forward.  The main pass needs a token's states again on the way back,
 // which costs registers: a workgroup is NP / 8 waves on the same 64 channels, 8 key dims each, so that the
-// 8 x 8 states of a tile fit beside the rest at three waves per SIMD.  What concerns a token and not a key dim (step
+// 8 x 8 states of a tile fit beside the rest at three waves per SIMD (bf16 in aligned rows; the other instances
+// spill 10 registers (bf16, unaligned) to 26 (fp32, N <= 8, unaligned)).  What concerns a token and not a key dim (step
 // size, gate, the finished gradients) is computed by one of the waves per token and passed through LDS.
 // The sums over channels cross lanes: 16 values a token and wave (8 key dims of dB and of dC) over 64 lanes, by
 // halving: every exchange adds two registers into one (about 35 instructions against 170 of the recurrence).
 //
-// Bound by vector issue: the decays' exponentials (16 cycles a wave) are formed once in pass 1 and twice in pass
+// Bound by vector issue: the decays' exponentials are formed once in pass 1 and twice in pass
 // 3, which has no registers to keep them at three waves per SIMD (kept, at two waves, 330 us against 312 in the
-// same session).  2 x 4096 tokens x 2048 channels, N = 16, bf16 with a gate: packing 5 us, states 93, segments 13,
-// main 290 to 310, sums 13; what it must read and write is 55 us at a copy's rate.
+// same session).  2 x 4096 tokens x 2048 channels, N = 16, bf16 with a gate: packing 5 us, states 98, segments 13,
+// main 291 (317 before, in the same session), sums 13; what it must read and write is 55 us at a copy's rate.
 #include "la_mixer.h"
 #include "ssm_common.h"
 #include "ssm_tile.h"
@@ -364,6 +365,7 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
         if (ONE) wave_lds_fence();
         else lds_barrier();
     };
+    auto entry = [&](int n) -> float& { return sums[(w * 3 + n / (NC / 2)) * SLOT + n % (NC / 2) * 64 + lane]; };
     scalar_f32 bcb = as_scalar_uniform(bcv);
     // where lane 4 i of the wave adds the i-th of its 16 sums over channels
     float* const dbcb = p.dbc + (cbi * p.B + b) * p.L * (2 * NP) + nb;
@@ -403,6 +405,10 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
         f32x4 hs[T][NC / 4], h[NC / 4];
 #pragma unroll
         for (int n = 0; n < NC; n++) h[n / 4][n % 4] = fmaf(__builtin_amdgcn_exp2f(A2[n] * keptdt), hin[n], kept[n]);
+        // the way back needs it again at the tile's first token: kept where that way writes the sums of the first
+        // NC / 2 tokens, which it reaches last
+#pragma unroll
+        for (int n = 0; n < NC; n++) entry(n) = h[n / 4][n % 4];
         const float br[1] = {bn}, cr[1] = {cn};
         if (t > t0) {
             fetch(t - T);
@@ -447,21 +453,32 @@ __global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev 
             const float* rw = row[j & 1];
             const float dl = arrived(dl_[j & 1]), du = du_[j & 1], ds = ds_[j & 1];
             if (j > 0) load_token(j - 1, true);
+            if (j == NC / 2 - 1) {
+                // this token and the ones before it write where the entering state is; half of the states are done with
+                // and make room for the next tile's loads
+#pragma unroll
+                for (int n = 0; n < NC; n++) h[n / 4][n % 4] = entry(n);
+            }
             float s1 = 0.f, s2 = 0.f, v[2 * NC];
             static_for<NC / 4>([&](auto Q) {
                 constexpr int k = Q;
                 const f32x4 gn = outer4<j * NC + 4 * k>(cr, ds, adj[k]);
-                const f32x4 wv = outer4<j * NC + 4 * k>(br, -du, hs[j][k]);  // a S_{t-1}
+                const f32x4 before = j > 0 ? hs[j > 0 ? j - 1 : 0][k] : h[k];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int n = 4 * k + i;
-                    const float gw = gn[i] * wv[i];
+                    adj[k][i] = gn[i] * __builtin_amdgcn_exp2f(dl * A2[n]);
+                    // G W as a product: with W = S_t - delta u B it would keep the roundings of S_t, which are larger
+                    // than W itself where the decay is strong
+                    const float gw = adj[k][i] * before[i];
                     s1 = fmaf(gn[i], rw[n], s1);
                     s2 = fmaf(gw, A2[n], s2);
                     dA[n] = fmaf(gw, dl, dA[n]);
+                    // added here: left to itself the compiler adds behind the last token and holds the tile's 64
+                    // products until then (2 x 4096 x 2048, N = 16, bf16: 24 registers spilled, main 333 us for 291)
+                    asm volatile("" : "+v"(dA[n]));
                     v[n] = gn[i] * du;
                     v[NC + n] = ds * hs[j][k][i];
-                    adj[k][i] = gn[i] * __builtin_amdgcn_exp2f(dl * A2[n]);
                 }
             });
             sums[(w * 3) * SLOT + j * 64 + lane] = s1;

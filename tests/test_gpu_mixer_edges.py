@@ -107,3 +107,75 @@ def test_norm_of_values_whose_squares_overflow(D, dtype):
     (rx, rw), (mx, mw) = R.norm_bwd(*args), R.norm_bwd(*args, mag=True)
     R.close(dx, rx, mx, K, dtype, "dx")
     R.close(dw, rw, mw, K + M, F32, "dw")
+
+
+# ------------------------------------------------------------------------------------ scan
+
+
+def scan_bwd_bounds(a, s_in, ds_out):
+    """dA [D, N] and ddt [L, D] of one sequence in fp64, each with a bound on what fp32 arithmetic that forms them as the
+    formulas say may be off by.  Errors are carried through the recurrences to first order, u = 2^-24: a step size
+    is off by 8 u of itself; a decay exp(delta A) by 8 u plus the rounding of its exponent, (8 + L) u |delta A| with up to
+    L step sizes summed before the product, and by 2^-126 where it leaves fp32's normal range; every sum or product
+    by u of its result, a sum over N or L terms by as many."""
+    f = {k: R.f64(v) for k, v in a.items()}
+    u = R.U
+    L, D = f["u"].shape[1:]
+    N = f["A"].shape[1]
+    A = f["A"].T
+    S, E = R.f64(s_in)[0], np.zeros((N, D))
+    kept = []
+    for t in range(L):
+        x = f["dt"][0, t] + f["dt_bias"]
+        dl = R.softplus(x)
+        dec, b = np.exp(dl * A), f["B"][0, t][:, None] * (dl * f["u"][0, t])
+        rho = (8 + (8 + L) * np.abs(dl * A)) * u
+        kept.append((S, E, x, dl, dec, rho))
+        E = dec * E + np.abs(S) * (dec * rho + 2.0 ** -126) + 11 * u * np.abs(b)
+        S = dec * S + b
+        E = E + u * np.abs(S)
+    G, F = R.f64(ds_out)[0], np.zeros((N, D))
+    dA, dAe = np.zeros((N, D)), np.zeros((N, D))
+    ddt, ddte = np.zeros((L, D)), np.zeros((L, D))
+    for t in range(L - 1, -1, -1):
+        S, E, x, dl, dec, rho = kept[t]
+        B = f["B"][0, t][:, None]
+        z, dy = f["z"][0, t], f["dy"][0, t]
+        c = f["C"][0, t][:, None] * (dy * R.silu(z))
+        F = F + 16 * u * np.abs(c)
+        G = G + c
+        F = F + u * np.abs(G)
+        gw = G * dec * S
+        gwe = F * dec * np.abs(S) + np.abs(G) * (np.abs(S) * (dec * rho + 2.0 ** -126) + dec * E) + 4 * u * np.abs(gw)
+        dA += gw * dl
+        dAe += (gwe + (L + 10) * u * np.abs(gw)) * dl
+        ut = f["u"][0, t]
+        terms, termse = G * B * ut + gw * A, F * np.abs(B * ut) + gwe * np.abs(A)
+        termse = termse + (N + 8) * u * (np.abs(G * B * ut) + np.abs(gw * A))
+        sg = R.sig(x)
+        ddt[t], ddte[t] = terms.sum(0) * sg, termse.sum(0) * sg + 8 * u * np.abs(terms.sum(0) * sg)
+        G, F = G * dec, F * dec + np.abs(G) * (dec * rho + 2.0 ** -126) + u * np.abs(G * dec)
+    return dA.T, 1.01 * dAe.T, ddt, 1.01 * ddte
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("N,most", [(8, 12.0), (8, 32.0), (16, 32.0), (24, 60.0), (64, 64.0)])
+def test_scan_backward_under_strong_decay(N, most, dtype):
+    """Step sizes around 1.3 and rates to -most: a token leaves next to nothing of the state before it, and the
+    derivatives that go through that remainder keep their relative accuracy, element by element.  (mixer_ref.scan_bwd's
+    magnitudes are too wide to see that: they also hold for the remainder formed as S_t - delta u B.)"""
+    note(f"scan backward: strong decay {N} {most} {dtype}")
+    g = Draw(90 + N)
+    L, D = 40, 72
+    a = dict(u=g.normal(1, L, D, dtype=dtype), dt=g.normal(1, L, D, std=0.5, dtype=dtype),
+             A=-g.uniform(D, N, lo=0.5, hi=most), B=g.normal(1, L, N, dtype=dtype), C=g.normal(1, L, N, dtype=dtype),
+             D=g.normal(D), z=g.normal(1, L, D, dtype=dtype), dt_bias=g.uniform(D, lo=0.5, hi=1.5))
+    s_in, ds_out = g.normal(1, N, D), g.normal(1, N, D)
+    a["dy"] = g.normal(1, L, D, dtype=dtype)
+    _, ddt, dA, *_ = la.la_ssm_scan_bwd(a["u"], a["dt"], a["A"], a["B"], a["C"], a["dy"], D=a["D"], z=a["z"],
+                                        dt_bias=a["dt_bias"], s_in=s_in, ds_out=ds_out)
+    rA, eA, rdt, edt = scan_bwd_bounds(a, s_in, ds_out)
+    for name, got, ref, err, t in (("dA", dA, rA, eA, F32), ("ddt", ddt[0], rdt, edt, dtype)):
+        off = np.abs(R.f64(got) - ref)
+        bad = ~(off <= R.HALF[t] * np.abs(ref) + err * (1 + R.HALF[t]))
+        assert not bad.any(), (name, int(bad.sum()), bad.size, float((off / (np.abs(ref) + 1e-300))[bad].max()))
