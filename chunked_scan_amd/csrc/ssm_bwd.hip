@@ -18,8 +18,7 @@
 //
 // A lane owns a channel as in the forward.  The main pass needs a token's states again on the way back,
 // which costs registers: a workgroup is NP / 8 waves on the same 64 channels, 8 key dims each, so that the
-// 8 x 8 states of a tile fit beside the rest at three waves per SIMD (bf16 in aligned rows; the other instances
-// spill 10 registers (bf16, unaligned) to 26 (fp32, N <= 8, unaligned)).  What concerns a token and not a key dim (step
+// 8 x 8 states of a tile fit beside the rest at two (fp32) or three (bf16) waves per SIMD.  What concerns a token and not a key dim (step
 // size, gate, the finished gradients) is computed by one of the waves per token and passed through LDS.
 // The sums over channels cross lanes: 16 values a token and wave (8 key dims of dB and of dC) over 64 lanes, by
 // halving: every exchange adds two registers into one (about 35 instructions against 170 of the recurrence).
@@ -278,8 +277,13 @@ __device__ __forceinline__ float wave_sums16(float* v) {
 // Per tile, from the segment's last: the inputs to LDS | per token (shared out over the waves): step size
 // and gate | every wave: forwards to its states, backwards through them, its share of the sums over key dims
 // to LDS | per token: the finished gradients.  The bars are workgroup barriers.
+// Waves per SIMD: what an instance needs without spilling allows two (fp32, and single waves in unaligned rows, 175 to
+// 195 registers) or three (bf16, 165 and 168).  Held to three, fp32 spills up to 26: at 2 x 2048 x 2048 N = 8
+// 164 -> 142 us with two, N = 16 189 -> 173, in unaligned rows (2046 channels) 225 -> 169 and 242 -> 204; 2048 x 1024,
+// N = 64, the same 152.  bf16 of more than 8 key dims in unaligned rows is faster with three and 10 registers spilled
+// (2 x 2048 x 2044, N = 16: 181 us, with two 202); N = 8 there 135 -> 125 with two.
 template <typename E, bool VEC, bool ONE>
-__global__ __launch_bounds__(ONE ? 64 : 512, 3) void ssm_bwd_main_kernel(BwdDev p) {
+__global__ __launch_bounds__(ONE ? 64 : 512, sizeof(E) == 2 && !ONE ? 3 : 2) void ssm_bwd_main_kernel(BwdDev p) {
     extern __shared__ __align__(16) char lds[];
     constexpr int NC = NW8, SLOT = T * 64;
     E* const rawt = reinterpret_cast<E*>(lds);  // [2][4][SLOT], alternating: u; dt, then d dt; dy, then du; z, then dz
