@@ -242,12 +242,24 @@ class SelectiveParams:
     q8_group: Optional[int] = None
 
 
-def _norm_in(p: SelectiveParams, x, residual):
-    """(what the input projection takes, h, rstd): the normed rows, or (q, scale) in 8 bits."""
+def _norm_in(p: SelectiveParams, x, residual, pad=None):
+    """(what the input projection takes, h, rstd): the normed rows, or (q, scale) in 8 bits; those of ``pad``, a mask
+    [rows, 1], are zero."""
     if p.q8_group is None:
-        return la_add_norm(x, p.norm_weight, residual, eps=p.eps)
+        y, h, rstd = la_add_norm(x, p.norm_weight, residual, eps=p.eps)
+        return (y if pad is None else y.masked_fill_(pad, 0)), h, rstd
     q, scale, h, rstd = la_add_norm_q8(x, p.norm_weight, residual, eps=p.eps, group=p.q8_group)
+    if pad is not None:
+        q.view(torch.uint8).masked_fill_(pad, 0)
+        scale.masked_fill_(pad, 1)
     return (q, scale), h, rstd
+
+
+def _padding(lengths, B, L, device):
+    """Which of B L rows lie behind their sequence's length: [B L, 1], or None."""
+    if lengths is None:
+        return None
+    return (torch.arange(L, device=device)[None] >= lengths[:, None]).view(B * L, 1)
 
 
 def selective_prompt(p: SelectiveParams, x: torch.Tensor, residual: Optional[torch.Tensor],
@@ -257,15 +269,16 @@ def selective_prompt(p: SelectiveParams, x: torch.Tensor, residual: Optional[tor
     """One layer over x [B, L, Dm] (residual the same or None).  project_in maps the normed rows [B L, Dm] (or
     (q, scale)) to (u, z): two [B L, D] tensors, the gate z possibly None, usually the halves of one
     product.  project_dbc maps the convolved [B, L, D] to (dt, B, C): [B, L, D], [B, L, N], [B, L, N].
+    Rows of x and residual behind a sequence's length may hold anything: what project_in takes is zero there.
     conv_state [B, W-1, D] and s_in [B, N, D]: states of the tokens before, or None.  Returns (y [B, L, D],
     zero behind a sequence's length, h [B, L, Dm] the residual stream, conv_state, s_out).  `saved`, a dict, receives what
     selective_backward takes."""
     B, L, Dm = x.shape
     rows = lambda t: None if t is None else t.reshape(B * L, Dm)  # noqa: E731
-    y, h, rstd = _norm_in(p, rows(x), rows(residual))
+    y, h, rstd = _norm_in(p, rows(x), rows(residual), _padding(lengths, B, L, x.device))
     u, z = (None if t is None else t.unflatten(0, (B, L)) for t in project_in(y))
-    # rows behind a sequence's length are not written: they are zero here, so that a product over all rows
-    # (the projections' weight derivatives) stays finite
+    # rows behind a sequence's length are not written: they are zero here (as the normed ones are), so that a product
+    # over all rows (the projections' weight derivatives) stays finite whatever the padding holds
     blank = lambda: None if lengths is None else torch.zeros(u.shape, dtype=u.dtype, device=u.device)  # noqa: E731
     v, conv_out = la_short_conv(u, p.conv_weight, p.conv_bias, conv_state, lengths=lengths, y=blank(), want_state=True)
     dt, Bm, C = project_dbc(v)
@@ -280,8 +293,8 @@ def selective_backward(p: SelectiveParams, saved: dict, dy: torch.Tensor, dbc_ba
                        d_conv_state: Optional[torch.Tensor] = None, ds_out: Optional[torch.Tensor] = None) -> dict:
     """Backward of selective_prompt from dy [B, L, D], dh [B, L, Dm] (the residual stream's derivative) and those of
     the returned states.  dbc_backward maps (ddt, dB, dC) to the convolved tensor's part of the derivative
-    [B, L, D]; in_backward maps (du, dz) to the normed rows' [B L, Dm].  Returns dx (of x and residual
-    alike) and the parameters' and incoming states' derivatives by name."""
+    [B, L, D]; in_backward maps (du, dz), zero behind a sequence's length, to the normed rows' [B L, Dm].  Returns
+    dx (of x and residual alike; behind a length dh) and the parameters' and incoming states' derivatives by name."""
     s = saved
     B, L, _ = s["u"].shape
     dv, ddt, dA, dB, dC, dskip, dz, d_dt_bias, ds_in = la_ssm_scan_bwd(
@@ -291,7 +304,10 @@ def selective_backward(p: SelectiveParams, saved: dict, dy: torch.Tensor, dbc_ba
     du, dcw, dcb, d_conv = la_short_conv_bwd(s["u"], p.conv_weight, dv, p.conv_bias, s["conv_state"], d_conv_state,
                                              lengths=s["lengths"])
     dn = in_backward(du, dz)
-    dx, dnw = la_add_norm_bwd(dn, s["h"], p.norm_weight, s["rstd"], None if dh is None else dh.reshape(dn.shape))
+    h, rstd, pad = s["h"], s["rstd"], _padding(s["lengths"], B, L, dy.device)
+    if pad is not None:  # the normed padding rows were zero: dn is zero there and what they hold may not meet it
+        h, rstd = h.masked_fill(pad, 0), rstd.masked_fill(pad[:, 0], 1)
+    dx, dnw = la_add_norm_bwd(dn, h, p.norm_weight, rstd, None if dh is None else dh.reshape(dn.shape))
     return dict(dx=dx.view(B, L, dn.shape[1]), norm_weight=dnw, conv_weight=dcw, conv_bias=dcb, A=dA, skip=dskip,
                 dt_bias=d_dt_bias, conv_state=d_conv, s_in=ds_in)
 

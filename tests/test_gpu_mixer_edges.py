@@ -7,8 +7,9 @@ import torch
 
 import mixer_ref as R
 from chunked_scan_amd import binding as la
+from chunked_scan_amd import pipeline
 from gpu_util import note
-from test_gpu_mixer import BF, F32, Draw
+from test_gpu_mixer import BF, F32, Draw, ints, layer
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +180,45 @@ def test_scan_backward_under_strong_decay(N, most, dtype):
         off = np.abs(R.f64(got) - ref)
         bad = ~(off <= R.HALF[t] * np.abs(ref) + err * (1 + R.HALF[t]))
         assert not bad.any(), (name, int(bad.sum()), bad.size, float((off / (np.abs(ref) + 1e-300))[bad].max()))
+
+
+# ------------------------------------------------------------------------------------ together
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("q8", [None, 0, 32])
+def test_layer_with_padding_that_is_not_finite(q8, value):
+    """Rows behind a sequence's length hold NaN or infinities, as in a batch of uninitialised memory: outputs, states
+    and every derivative, the projections' own (products over all rows) among them, are what they are with zeros
+    there."""
+    note(f"layer: padding of {value}, q8 {q8}")
+    B, L, D, N, W = 3, 40, 64, 16, 4
+    p, pin, pdbc, wx, wp = layer(D, N, W, 47, q8=q8)
+    g = Draw(48)
+    lens = [40, -1, 17]
+    live = (torch.arange(L)[None] < torch.tensor(lens)[:, None])[..., None].cuda()
+    x, res, dy, dh = (g.normal(B, L, D) for _ in range(4))
+    taken = []
+
+    def project_in(y):
+        taken.append(y if q8 is None else (y[0].float().view(B * L, y[1].shape[1], -1) * y[1][:, :, None]).view(B * L, D))
+        return pin(y)
+
+    def run(fill):
+        put = lambda t: torch.where(live, t, torch.full_like(t, fill))  # noqa: E731
+        e = torch.float32 if q8 is None else torch.bfloat16
+        saved = {}
+        o, h, c, s = pipeline.selective_prompt(p, put(x).to(e), put(res).to(e), project_in, pdbc, lengths=ints(lens), saved=saved)
+        d_in = []
+
+        def in_backward(du, dz):
+            d_in.append(torch.cat([du, dz], -1).view(B * L, -1).float())
+            return (d_in[0] @ wx.t()).to(e)
+
+        gr = pipeline.selective_backward(p, saved, put(dy).to(e), lambda ddt, dB, dC: (torch.cat([ddt, dB, dC], -1).float() @ wp.t()).to(e),
+                                         in_backward, dh=dh.to(e))
+        return [torch.where(live, h, torch.zeros_like(h)), o, c, s, taken[-1].float().t() @ d_in[0]] + [gr[k] for k in sorted(gr) if gr[k] is not None]
+
+    want, got = run(0.0), run(value)
+    for k, (a, b) in enumerate(zip(want, got)):
+        assert torch.isfinite(b).all() and torch.equal(a, b), k
