@@ -9,7 +9,7 @@ import mixer_ref as R
 from chunked_scan_amd import binding as la
 from chunked_scan_amd import pipeline
 from gpu_util import note
-from test_gpu_mixer import BF, F32, Draw, ints, layer
+from test_gpu_mixer import BF, F32, Draw, cut, ints, layer
 
 pytestmark = pytest.mark.gpu
 
@@ -222,3 +222,141 @@ def test_layer_with_padding_that_is_not_finite(q8, value):
     want, got = run(0.0), run(value)
     for k, (a, b) in enumerate(zip(want, got)):
         assert torch.isfinite(b).all() and torch.equal(a, b), k
+
+
+# ------------------------------------------------------------------------------------ the wide forms
+
+
+def chosen(D, n=24, seed=3):
+    """n channels: the ends, and some between (channels do not meet in the convolution or the scan's states)."""
+    rng = np.random.default_rng(seed)
+    return torch.from_numpy(np.unique(np.concatenate([[0, 1, D - 2, D - 1], rng.integers(0, D, n - 4)]))).cuda()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D,W,lengths", [
+    (1, 1100, 16384, 4, None),            # vectors: tiles of 16 tokens forward, 32 back, a remainder of 12
+    (2, 1077, 4095, 3, [1077, 530]),      # one channel a thread
+    (2, 1077, 8192, 2, [-5, 1061]),
+    (40, 33, 16384, 4, None),             # a tile and a token
+])
+def test_conv_in_long_tiles(B, L, D, W, lengths, dtype):
+    """Sizes from which a thread walks 16 tokens forward and 32 back, on some of the channels."""
+    note(f"conv in long tiles {B} {L} {D} {W} {lengths} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(L + D)
+    rnd = lambda *s, e=F32: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    x, dy = rnd(B, L, D, e=dtype), rnd(B, L, D, e=dtype)
+    w, b, st, dso = rnd(D, W) * 0.6, rnd(D), rnd(B, W - 1, D, e=dtype), rnd(B, W - 1, D, e=dtype)
+    n = cut(lengths, L)
+    y, so = la.la_short_conv(x, w, b, st, lengths=ints(lengths), y=torch.zeros_like(x), want_state=True)
+    got = la.la_short_conv_bwd(x, w, dy, b, st, dso, lengths=ints(lengths))
+    at = chosen(D)
+    p = lambda t: R.f64(t[..., at])  # noqa: E731
+    args = (p(x), R.f64(w[at]), R.f64(b[at]), p(st), n, True)
+    K = W + 28
+    ref, ref_so = R.conv(*args)
+    mag, _ = R.conv(*[np.abs(v) if i < 4 else v for i, v in enumerate(args[:5])], False)
+    R.close(y[..., at], ref, mag, K, dtype, "y")
+    assert np.array_equal(p(so), ref_so)
+    r, m = R.conv_bwd(*args, p(dy), p(dso)), R.conv_bwd(*args, p(dy), p(dso), mag=True)
+    R.close(got[0][..., at], r[0], m[0], 2 * K, dtype, "dx")
+    R.close(got[1][at], r[1], m[1], 2 * K + B * L, F32, "dw")
+    R.close(got[2][at], r[2], m[2], 2 * K + B * L, F32, "db")
+    R.close(got[3][..., at], r[3], m[3], 2 * K, dtype, "d_state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,D,N,gate", [(258, 4096, 16, True), (300, 2100, 17, False), (515, 2048, 8, True), (1100, 700, 24, True)])
+def test_scan_step_of_many_rows(B, D, N, gate, dtype):
+    """Several rows a wave: slots outside the pool, repeated ones next to each other and in other waves, a last wave
+    with fewer rows, on some of the channels."""
+    note(f"scan step of many rows {B} {D} {N} {dtype}")
+    rng = np.random.default_rng(B)
+    S = B + 7
+    slots = rng.permutation(S)[:B].astype(np.int64)
+    slots[1], slots[2], slots[5] = slots[0], -1, S  # neighbours of one wave
+    slots[B - 1], slots[B - 2], slots[77] = slots[3], slots[B - 3], -(1 << 31)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    rnd = lambda *s, e=F32: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    u, dt, z = rnd(B, D, e=dtype), rnd(B, D, e=dtype), rnd(B, 2 * D, e=dtype)[:, D:] if gate else None
+    Bm, C = rnd(B, N, e=dtype), rnd(B, N, e=dtype)
+    A = -8 * torch.rand(D, N, generator=g, device="cuda") - 0.5
+    skip, bias, state = rnd(D), rnd(D) - 3, rnd(S, N, D)
+    before = state.clone()
+    y = torch.full((B, D), 7.0, dtype=dtype, device="cuda")
+    la.la_ssm_step(u, dt, A, Bm, C, state, D=skip, z=z, dt_bias=bias, slots=ints(slots.tolist()), y=y)
+    first = {}
+    for i, s in enumerate(slots):
+        if 0 <= s < S:
+            first.setdefault(int(s), i)
+    rows = torch.tensor(sorted(first.values()), device="cuda")
+    rest = torch.tensor(sorted(set(range(B)) - set(first.values())), device="cuda")
+    assert len(rest) == 6 and (y[rest] == 7.0).all()
+    untouched = torch.tensor(sorted(set(range(S)) - set(first)), device="cuda")
+    assert torch.equal(state[untouched], before[untouched])
+    at = chosen(D)
+    sl = torch.from_numpy(slots).cuda()[rows]
+    p = lambda t: None if t is None else R.f64(t[rows][:, at])[:, None]  # noqa: E731
+    args = (p(u), p(dt), R.f64(A[at]), R.f64(Bm[rows])[:, None], R.f64(C[rows])[:, None], R.f64(skip[at]), p(z),
+            R.f64(bias[at]), R.f64(before[sl][..., at]), None, True)
+    ref, so, _ = R.scan(*args)
+    mag, mso, _ = R.scan(*args, mag=True)
+    R.close(y[rows][:, at], ref[:, 0], mag[:, 0], 72, dtype, "y")
+    R.close(state[sl][..., at], so, mso, 72, F32, "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D,N,lengths", [
+    (1, 1296, 600, 16, None),         # more than 8192 states, 81 segments of 16 tokens: 4 shares of 20
+    (2, 1152, 300, 16, [1151, 1000]), # 72 segments: 4 shares of 18
+    (1, 4800, 64, 16, None),          # few states, 300 segments: 16 shares of 19
+    (3, 60, 700, 8, [60, 0, 33]),     # more than 8192 states, 3 segments
+])
+def test_scan_over_many_segments(B, L, D, N, lengths, dtype):
+    """The scan over segments with shares of more than 16, which are loaded twice, forward and backward."""
+    note(f"scan over many segments {B} {L} {D} {N} {lengths} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(L)
+    rnd = lambda *s, e=F32: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    u, dt, dy = rnd(B, L, D, e=dtype), 0.5 * rnd(B, L, D), rnd(B, L, D, e=dtype)
+    dt = dt.to(dtype)
+    Bm, C = rnd(B, L, N, e=dtype), rnd(B, L, N, e=dtype)
+    A = -4 * torch.rand(D, N, generator=g, device="cuda") - 0.05
+    skip, bias, s_in, ds_out = rnd(D), rnd(D) - 4, rnd(B, N, D), rnd(B, N, D)
+    n = cut(lengths, L)
+    kw = dict(D=skip, dt_bias=bias, s_in=s_in, lengths=ints(lengths))
+    y, so = la.la_ssm_scan(u, dt, A, Bm, C, y=torch.zeros_like(u), **kw)
+    got = la.la_ssm_scan_bwd(u, dt, A, Bm, C, dy, ds_out=ds_out, **kw)
+    args = (R.f64(u), R.f64(dt), R.f64(A), R.f64(Bm), R.f64(C), R.f64(skip), None, R.f64(bias), R.f64(s_in), n, True)
+    K = 8 * L + 64
+    ref, ref_so, _ = R.scan(*args)
+    mag, mag_so, _ = R.scan(*args, mag=True)
+    R.close(y, ref, mag, K, dtype, "y")
+    R.close(so, ref_so, mag_so, K, F32, "s_out")
+    r, m = R.scan_bwd(*args, R.f64(dy), R.f64(ds_out)), R.scan_bwd(*args, R.f64(dy), R.f64(ds_out), mag=True)
+    extra = dict(dA=B * L, dB=D, dC=D, dD=B * L, d_dt_bias=B * L)
+    for k, name in enumerate(("du", "ddt", "dA", "dB", "dC", "dD", "dz", "d_dt_bias", "ds_in")):
+        if name != "dz":
+            t = F32 if name in ("dA", "dD", "d_dt_bias", "ds_in") else dtype
+            R.close(got[k], r[k], m[k], 2 * K + extra.get(name, 0), t, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(2051, 512), (4500, 63), (2500, 1024), (700, 4096), (1030, 2056), (530, 16384)])
+def test_norm_backward_of_many_rows(M, D, dtype):
+    """More rows than one turn of the workgroups takes."""
+    note(f"norm backward of many rows {M} {D} {dtype}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    rnd = lambda *s, e=F32: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    h, dy, dh = 2 * rnd(M, D), rnd(M, D, e=dtype), rnd(M, D, e=dtype)
+    h, w = h.to(dtype), 1 + 0.2 * rnd(D)
+    _, _, r = la.la_add_norm(h, w)
+    dx, dw = la.la_add_norm_bwd(dy, h, w, r, dh)
+    args = (R.f64(dy), R.f64(h), R.f64(w), R.f64(r), R.f64(dh))
+    (rx, rw), (mx, mw) = R.norm_bwd(*args), R.norm_bwd(*args, mag=True)
+    K = D / 8 + 32
+    R.close(dx, rx, mx, K, dtype, "dx")
+    R.close(dw, rw, mw, K + M, F32, "dw")
