@@ -803,7 +803,7 @@ def _row_stride(t: Optional[torch.Tensor], name: str) -> int:
     return t.stride(0)
 
 
-def _norm_args(on, x, residual, weight, h, M, D):
+def _norm_args(on, x, residual, weight, M, D):
     on.check(x, "x", x.dtype, (M, D), dense=False)
     on.check(residual, "residual", x.dtype, (M, D), dense=False)
     on.check(weight, "weight", torch.float32, (D,))
@@ -817,7 +817,7 @@ def la_add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     M, D = _dims(x, "x", 2)
     code = _dtype_code(x)
     with _On(x, "x", stream) as on:
-        _norm_args(on, x, residual, weight, h, M, D)
+        _norm_args(on, x, residual, weight, M, D)
         want = residual is not None or h is not None
         h = on.out(h, "h", x.dtype, (M, D), dense=False) if want else None
         y = on.out(y, "y", x.dtype, (M, D), dense=False)
@@ -840,7 +840,7 @@ def la_add_norm_q8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if group not in (0, 32, 64, 128) or (group and D % group):
         raise ValueError(f"group must be 0, 32, 64 or 128 and divide D = {D}, not {group}")
     with _On(x, "x", stream) as on:
-        _norm_args(on, x, residual, weight, h, M, D)
+        _norm_args(on, x, residual, weight, M, D)
         want = residual is not None or h is not None
         h = on.out(h, "h", x.dtype, (M, D), dense=False) if want else None
         q = on.out(q, "q", torch.float8_e4m3fn, (M, D))

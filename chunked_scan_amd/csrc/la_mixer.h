@@ -114,6 +114,11 @@ hipError_t launch_add_norm(const NormArgs& a);
 size_t add_norm_bwd_ws(int64_t M, int64_t D);
 hipError_t launch_add_norm_bwd(const NormArgs& a);
 
+// Whether every row of a view starts on 16 bytes.
+inline bool rows16(const void* p, const la_rows& r, size_t es) {
+    return !p || ((uintptr_t)p % 16 == 0 && (r.batch * es) % 16 == 0 && (r.token * es) % 16 == 0);
+}
+
 // A workspace cut into 256-byte aligned regions.
 struct WsCut {
     char* base;

@@ -409,9 +409,6 @@ __global__ __launch_bounds__(64) void conv_step_kernel(const E* __restrict__ x, 
 }
 
 bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
-bool rows16(const void* p, la_rows r, size_t es) {
-    return !p || (aligned16(p) && (r.batch * es) % 16 == 0 && (r.token * es) % 16 == 0);
-}
 
 // Tokens per thread: 16 in the forward and 32 in the backward (which writes W + 1 sums per channel and tile),
 // fewer where that leaves under 2048 waves, two per SIMD.  Each tile re-reads W - 1 rows and loads the taps:

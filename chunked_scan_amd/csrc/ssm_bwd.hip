@@ -594,7 +594,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const float* __restri
         dbias[d] = s;
 }
 
-int np_for(int N) { return (N + NW8 - 1) / NW8 * NW8; }
+int bwd_np(int N) { return (N + NW8 - 1) / NW8 * NW8; }
 
 // Segments: about 6144 waves in the main pass (NP / 8 to a channel block), two rounds of what fits the device
 // at once, none under 16 tokens.  2 x 4096 tokens x 2048 channels, N = 16, main and first pass: half as many
@@ -609,7 +609,7 @@ struct BwdWs {
 BwdWs bwd_cut(void* base, int64_t B, int64_t L, int64_t D, int N, int G) {
     WsCut c{(char*)base};
     BwdWs w;
-    const int NP = np_for(N);
+    const int NP = bwd_np(N);
     const size_t seg = (size_t)(B * G) * D, tok = (size_t)(B * L);
     w.nk = (L + T - 1) / T;
     w.bc = c.take(tok * 2 * NP);
@@ -628,7 +628,7 @@ BwdWs bwd_cut(void* base, int64_t B, int64_t L, int64_t D, int N, int G) {
 
 template <typename E>
 hipError_t launch_e(const SsmArgs& a) {
-    const SsmPlan pl = bwd_plan(a.B, a.L, a.D, np_for(a.N));
+    const SsmPlan pl = bwd_plan(a.B, a.L, a.D, bwd_np(a.N));
     const BwdWs w = bwd_cut(a.ws, a.B, a.L, a.D, a.N, pl.G);
     BwdDev p;
     p.u = a.u; p.dt = a.dt; p.z = a.z; p.dy = a.dy; p.a2 = w.a2; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
@@ -637,7 +637,7 @@ hipError_t launch_e(const SsmArgs& a) {
     p.dbc = w.dbc; p.dap = w.dap; p.ddp = w.ddp;
     p.ds_in = a.ds_in; p.du = a.du; p.ddt = a.ddt; p.dz = a.dz;
     p.B = a.B; p.L = a.L; p.D = a.D; p.seglen = pl.seglen; p.nk = w.nk;
-    p.N = a.N; p.NP = np_for(a.N); p.G = pl.G;
+    p.N = a.N; p.NP = bwd_np(a.N); p.G = pl.G;
     p.cb = (unsigned)((a.D + 63) / 64);
     p.softplus = a.softplus;
     p.su = a.su; p.sdt = a.sdt; p.sz = a.sz; p.sdy = a.sdy; p.sdu = a.sdu; p.sddt = a.sddt; p.sdz = a.sdz;
@@ -693,7 +693,7 @@ hipError_t launch_e(const SsmArgs& a) {
 }  // namespace
 
 size_t ssm_bwd_ws(int64_t B, int64_t L, int64_t D, int N) {
-    return bwd_cut(nullptr, B, L, D, N, bwd_plan(B, L, D, np_for(N)).G).bytes;
+    return bwd_cut(nullptr, B, L, D, N, bwd_plan(B, L, D, bwd_np(N)).G).bytes;
 }
 
 hipError_t launch_ssm_scan_bwd(const SsmArgs& a) { return a.bf16 ? launch_e<__bf16>(a) : launch_e<float>(a); }

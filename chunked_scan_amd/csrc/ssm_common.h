@@ -20,11 +20,6 @@ inline SsmPlan ssm_plan(int64_t B, int64_t L, int64_t D, int64_t waves, int64_t 
     return {(int)((L + seglen - 1) / seglen), seglen};
 }
 
-// Whether every row of a view starts on 16 bytes.
-inline bool rows16(const void* p, const la_rows& r, size_t es) {
-    return !p || ((uintptr_t)p % 16 == 0 && (r.batch * es) % 16 == 0 && (r.token * es) % 16 == 0);
-}
-
 // Packs B and C as fp32 [B, L, 2 NP] and A log2(e) as [NP, D], zeros behind N (ssm_scan.hip).
 void launch_pack(const SsmArgs& a, float* bc, float* a2, int NP);
 

@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * PARTS) void ssm_segments_kernel(const float* _
         [&](int k, float, float next) { pp[(k + 1) * ps] = next; });
 }
 
-int np_for(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 24 ? 24 : N <= 32 ? 32 : N <= 48 ? 48 : 64; }
+int fwd_np(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 24 ? 24 : N <= 32 ? 32 : N <= 48 ? 48 : 64; }
 
 // Segments: about 4096 waves, none under 16 tokens.
 SsmPlan fwd_plan(int64_t B, int64_t L, int64_t D) { return ssm_plan(B, L, D, 4096, 16, TT); }
@@ -268,8 +268,8 @@ struct FwdWs {
 FwdWs fwd_cut(void* base, int64_t B, int64_t L, int64_t D, int N, int G) {
     WsCut c{(char*)base};
     FwdWs w;
-    w.bc = c.take((size_t)(B * L) * 2 * np_for(N));
-    w.a2 = c.take((size_t)np_for(N) * D);
+    w.bc = c.take((size_t)(B * L) * 2 * fwd_np(N));
+    w.a2 = c.take((size_t)fwd_np(N) * D);
     w.part = G > 1 ? c.take((size_t)(B * G) * N * D) : nullptr;
     w.sumdt = G > 1 ? c.take((size_t)(B * G) * D) : nullptr;
     w.bytes = c.used;
@@ -298,7 +298,7 @@ template <typename T>
 hipError_t launch_t(const SsmArgs& a) {
     const SsmPlan pl = fwd_plan(a.B, a.L, a.D);
     const FwdWs w = fwd_cut(a.ws, a.B, a.L, a.D, a.N, pl.G);
-    const int NP = np_for(a.N);
+    const int NP = fwd_np(a.N);
     FwdDev p;
     p.u = a.u; p.dt = a.dt; p.z = a.z; p.Dskip = a.Dskip; p.dt_bias = a.dt_bias;
     p.bc = w.bc;
@@ -445,7 +445,7 @@ void step_np(const SsmArgs& a) {
 }
 template <typename T>
 hipError_t step_t(const SsmArgs& a) {
-    switch (np_for(a.N)) {
+    switch (fwd_np(a.N)) {
         case 8: step_np<T, 8>(a); break;
         case 16: step_np<T, 16>(a); break;
         case 24: step_np<T, 24>(a); break;
