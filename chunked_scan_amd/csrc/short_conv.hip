@@ -9,8 +9,10 @@
 // tile from the neighbour's (which the cache holds).  Loads of TB tokens are in flight together.
 //
 // What is written once and not read here leaves the forward by a streaming store (st_once): 16384 x 2048 bf16,
-// W = 4, in 28.0 us (134 MB, 4.8 TB/s, what a copy of this size reaches), 33.0 with ordinary stores; streaming
-// loads, which lose the neighbours' W - 1 rows, 28.8.  The backward keeps ordinary stores (28.1 and 27.9 us).
+// W = 4, in 26.8 us (134 MB, 5.0 TB/s; a copy of as many bytes takes 25.7), 33.0 with ordinary stores; streaming
+// loads, which lose the neighbours' W - 1 rows, 28.8.  That is call after call; in a layer, whose projection and scan read
+// the output next, both kinds of store take the same time (766 to 773 us for the whole prompt).  The backward keeps
+// ordinary stores (28.1 and 27.9 us).
 #include <algorithm>
 
 #include "la_mixer.h"

@@ -182,6 +182,36 @@ def test_scan_backward_under_strong_decay(N, most, dtype):
         assert not bad.any(), (name, int(bad.sum()), bad.size, float((off / (np.abs(ref) + 1e-300))[bad].max()))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_scan_with_step_sizes_of_zero(dtype):
+    """dt of minus infinity and of the type's lowest value through softplus: a step size of zero, which leaves the state
+    alone and whose derivatives are zero; forward, backward and one token.  K as in test_gpu_mixer.py."""
+    note(f"scan: step sizes of zero {dtype}")
+    B, L, D, N = 2, 70, 72, 16
+    g = Draw(33)
+    u, dy, z = (g.normal(B, L, D, dtype=dtype) for _ in range(3))
+    dt, Bm, C = g.normal(B, L, D, std=0.5, dtype=dtype), g.normal(B, L, N, dtype=dtype), g.normal(B, L, N, dtype=dtype)
+    dt[0, 5:9], dt[:, 30, ::2], dt[1, 40:] = -float("inf"), torch.finfo(dtype).min, -float("inf")
+    A, bias, skip, s_in, ds_out = -g.uniform(D, N, lo=0.5, hi=8.0), g.uniform(D, lo=-4.0, hi=0.0), g.normal(D), g.normal(B, N, D), g.normal(B, N, D)
+    kw = dict(D=skip, z=z, dt_bias=bias, s_in=s_in)
+    y, so = la.la_ssm_scan(u, dt, A, Bm, C, **kw)
+    got = la.la_ssm_scan_bwd(u, dt, A, Bm, C, dy, ds_out=ds_out, **kw)
+    args = (R.f64(u), R.f64(dt), R.f64(A), R.f64(Bm), R.f64(C), R.f64(skip), R.f64(z), R.f64(bias), R.f64(s_in), None, True)
+    K = 8 * L + 64
+    (ry, rs, _), (my, ms, _) = R.scan(*args), R.scan(*args, mag=True)
+    R.close(y, ry, my, K, dtype, "y")
+    R.close(so, rs, ms, K, F32, "s_out")
+    r, m = R.scan_bwd(*args, R.f64(dy), R.f64(ds_out)), R.scan_bwd(*args, R.f64(dy), R.f64(ds_out), mag=True)
+    extra = dict(dA=B * L, dB=D, dC=D, dD=B * L, d_dt_bias=B * L)
+    for k, name in enumerate(("du", "ddt", "dA", "dB", "dC", "dD", "dz", "d_dt_bias", "ds_in")):
+        t = F32 if name in ("dA", "dD", "d_dt_bias", "ds_in") else dtype
+        R.close(got[k], r[k], m[k], 2 * K + extra.get(name, 0), t, name)
+    assert (got[1][0, 5:9] == 0).all() and (got[1][1, 40:] == 0).all()
+    st = s_in.clone()
+    la.la_ssm_step(u[:, 5], dt[:, 50], A, Bm[:, 5], C[:, 5], st, D=skip, z=z[:, 5], dt_bias=bias)
+    assert torch.equal(st[1], s_in[1])
+
+
 # ------------------------------------------------------------------------------------ together
 
 
