@@ -26,7 +26,7 @@
 // Bound by vector issue: the decays' exponentials are formed once in pass 1 and twice in pass
 // 3, which has no registers to keep them at three waves per SIMD (kept, at two waves, 330 us against 312 in the
 // same session).  2 x 4096 tokens x 2048 channels, N = 16, bf16 with a gate: packing 5 us, states 98, segments 13,
-// main 275 to 291 (its vector units busy 80 % of the time), sums 13.  What it must read and write is 55 us at a copy's
+// main 275 to 291 (the vector units busy 78 % of the time), sums 13.  What it must read and write is 55 us at a copy's
 // rate; the kept states (0.5 N bytes per token and channel, written by pass 1 and read by pass 3, 134 MB each way) and the
 // partial sums of dB and dC (N / 8 bytes, 34 MB each way) are as much again and half, under the arithmetic.
 #include "la_mixer.h"

@@ -6,7 +6,7 @@
 // matrix product; the work is, per (t, n, d): a product and an exponential for the decay, a product
 // and a fused multiply-add for the state, one more for the output, and per (t, d) a softplus and a gate.  That
 // bounds the operator by vector issue, not by memory: a wave's exponential takes 8 cycles, its product or
-// multiply-add 4, and both passes below keep the vector units busy 79 % of the time.
+// multiply-add 4, and both passes below keep the vector units busy 78 % of the time.
 //
 // Layout.  A lane owns one channel and keeps its N states and its N rates A log2(e) in registers.  Activations
 // come and go through LDS (ssm_tile.h).  B_t and C_t are the same for every channel; a first launch packs them
