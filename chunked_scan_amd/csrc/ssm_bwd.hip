@@ -18,8 +18,9 @@
 //
 // A lane owns a channel as in the forward.  The main pass needs a token's states again on the way back,
 // which costs registers: a workgroup is NP / 8 waves on the same 64 channels, 8 key dims each, so that the
-// 8 x 8 states of a tile fit beside the rest at two (fp32) or three (bf16) waves per SIMD.  What concerns a token and not a key dim (step
-// size, gate, the finished gradients) is computed by one of the waves per token and passed through LDS.
+// 8 x 8 states of a tile fit beside the rest at two (fp32) or three (bf16) waves per SIMD.  What concerns a
+// token and not a key dim (step size, gate, the finished gradients) is computed by one of the waves per token and
+// passed through LDS.
 // The sums over channels cross lanes: 16 values a token and wave (8 key dims of dB and of dC) over 64 lanes, by
 // halving: every exchange adds two registers into one (about 35 instructions against 170 of the recurrence).
 //

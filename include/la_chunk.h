@@ -539,6 +539,7 @@ typedef struct la_norm_shape {
  *   h           : [M,D] dtype or NULL, the sum, rounded (the norm takes the unrounded sum); may be
  *                 the same pointer, with the same stride, as residual or x
  *   rstd        : float[M] or NULL, r of every row.
+ * Holds for any finite h, also where its squares overflow fp32.
  * No output may otherwise overlap another argument.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
  */

@@ -192,7 +192,8 @@ def test_scan_with_step_sizes_of_zero(dtype):
     u, dy, z = (g.normal(B, L, D, dtype=dtype) for _ in range(3))
     dt, Bm, C = g.normal(B, L, D, std=0.5, dtype=dtype), g.normal(B, L, N, dtype=dtype), g.normal(B, L, N, dtype=dtype)
     dt[0, 5:9], dt[:, 30, ::2], dt[1, 40:] = -float("inf"), torch.finfo(dtype).min, -float("inf")
-    A, bias, skip, s_in, ds_out = -g.uniform(D, N, lo=0.5, hi=8.0), g.uniform(D, lo=-4.0, hi=0.0), g.normal(D), g.normal(B, N, D), g.normal(B, N, D)
+    A, bias, skip = -g.uniform(D, N, lo=0.5, hi=8.0), g.uniform(D, lo=-4.0, hi=0.0), g.normal(D)
+    s_in, ds_out = g.normal(B, N, D), g.normal(B, N, D)
     kw = dict(D=skip, z=z, dt_bias=bias, s_in=s_in)
     y, so = la.la_ssm_scan(u, dt, A, Bm, C, **kw)
     got = la.la_ssm_scan_bwd(u, dt, A, Bm, C, dy, ds_out=ds_out, **kw)
@@ -245,9 +246,10 @@ def test_layer_with_padding_that_is_not_finite(q8, value):
             d_in.append(torch.cat([du, dz], -1).view(B * L, -1).float())
             return (d_in[0] @ wx.t()).to(e)
 
-        gr = pipeline.selective_backward(p, saved, put(dy).to(e), lambda ddt, dB, dC: (torch.cat([ddt, dB, dC], -1).float() @ wp.t()).to(e),
-                                         in_backward, dh=dh.to(e))
-        return [torch.where(live, h, torch.zeros_like(h)), o, c, s, taken[-1].float().t() @ d_in[0]] + [gr[k] for k in sorted(gr) if gr[k] is not None]
+        dbc_backward = lambda ddt, dB, dC: (torch.cat([ddt, dB, dC], -1).float() @ wp.t()).to(e)  # noqa: E731
+        gr = pipeline.selective_backward(p, saved, put(dy).to(e), dbc_backward, in_backward, dh=dh.to(e))
+        out = [torch.where(live, h, torch.zeros_like(h)), o, c, s, taken[-1].float().t() @ d_in[0]]
+        return out + [gr[k] for k in sorted(gr) if gr[k] is not None]
 
     want, got = run(0.0), run(value)
     for k, (a, b) in enumerate(zip(want, got)):
@@ -390,3 +392,43 @@ def test_norm_backward_of_many_rows(M, D, dtype):
     K = D / 8 + 32
     R.close(dx, rx, mx, K, dtype, "dx")
     R.close(dw, rw, mw, K + M, F32, "dw")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_longest_sequences(dtype):
+    """2^24 tokens, the most there may be, at the largest state size: the last ones against the oracle.  Step sizes of
+    at least softplus(-0.1 - 0.5) = 0.43 and rates of at most -2 leave e^-0.86 a token, so that of what lies
+    more than 200 tokens back nothing is left in fp64 next to the tolerance."""
+    note(f"longest sequences {dtype}")
+    L, D, N, W, T, back = 1 << 24, 3, 64, 4, 300, 200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    rnd = lambda *s, e=F32: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    uni = lambda *s: torch.rand(s, generator=g, device="cuda")  # noqa: E731
+    u, dy = rnd(1, L, D, e=dtype), rnd(1, L, D, e=dtype)
+    dt = (uni(1, L, D) - 0.5).to(dtype)
+    w, b = rnd(D, W), rnd(D)
+    y, so = la.la_short_conv(u, w, b, want_state=True)
+    dx = la.la_short_conv_bwd(u, w, dy, b)[0]
+    p = lambda t: R.f64(t[:, L - T :])  # noqa: E731
+    args = (p(u), R.f64(w), R.f64(b), None, None, True)
+    ref, ref_so = R.conv(*args)
+    mag, _ = R.conv(*[None if v is None else np.abs(v) for v in args[:4]], None, False)
+    R.close(y[:, L - T + W :], ref[:, W:], mag[:, W:], W + 28, dtype, "conv")
+    assert np.array_equal(R.f64(so), ref_so)
+    r, m = R.conv_bwd(*args, p(dy), None), R.conv_bwd(*args, p(dy), None, mag=True)
+    R.close(dx[:, L - T + W :], r[0][:, W:], m[0][:, W:], 2 * (W + 28), dtype, "conv dx")
+    del y, dx
+    Bm, C = rnd(1, L, N, e=dtype), rnd(1, L, N, e=dtype)
+    A, bias, skip, ds_out = -2 - 2 * uni(D, N), uni(D) * 0.1 - 0.1, rnd(D), rnd(1, N, D)
+    kw = dict(D=skip, dt_bias=bias)
+    y, so = la.la_ssm_scan(u, dt, A, Bm, C, **kw)
+    got = la.la_ssm_scan_bwd(u, dt, A, Bm, C, dy, ds_out=ds_out, **kw)
+    args = (p(u), p(dt), R.f64(A), p(Bm), p(C), R.f64(skip), None, R.f64(bias), None, None, True)
+    (ry, rs, _), (my, ms, _) = R.scan(*args), R.scan(*args, mag=True)
+    K = 8 * T + 64
+    R.close(y[:, L - T + back :], ry[:, back:], my[:, back:], K, dtype, "y")
+    R.close(so, rs, ms, K, F32, "s_out")
+    r, m = R.scan_bwd(*args, p(dy), R.f64(ds_out)), R.scan_bwd(*args, p(dy), R.f64(ds_out), mag=True)
+    for k, name, extra in ((0, "du", 0), (1, "ddt", 0), (3, "dB", D), (4, "dC", D)):
+        R.close(got[k][:, L - T + back :], r[k][:, back:], m[k][:, back:], 2 * K + extra, dtype, name)
