@@ -432,3 +432,72 @@ def test_longest_sequences(dtype):
     r, m = R.scan_bwd(*args, p(dy), R.f64(ds_out)), R.scan_bwd(*args, p(dy), R.f64(ds_out), mag=True)
     for k, name, extra in ((0, "du", 0), (1, "ddt", 0), (3, "dB", D), (4, "dC", D)):
         R.close(got[k][:, L - T + back :], r[k][:, back:], m[k][:, back:], 2 * K + extra, dtype, name)
+
+
+def test_most_sequences():
+    """2^20 sequences, the most there may be: rows from the start, the middle and the end give what they give alone (one
+    segment either way, so bit for bit), forward, backward and one token; so does the convolution."""
+    note("most sequences")
+    B, L, D, N, W = 1 << 20, 2, 32, 16, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(20)
+    rnd = lambda *s, e=BF: torch.randn(s, generator=g, device="cuda").to(e)  # noqa: E731
+    at = torch.cat([torch.arange(k, k + 40) for k in (0, (1 << 19) - 7, B - 40)]).cuda()
+    u, dt, z, dy, Bm, C = (rnd(B, L, n) for n in (D, D, D, D, N, N))
+    A, skip, bias = -torch.rand(D, N, generator=g, device="cuda") - 0.1, rnd(D, e=F32), rnd(D, e=F32) - 3
+    s_in, lens = rnd(B, N, D, e=F32), torch.randint(0, L + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+
+    def scan(pick, back):
+        a = [pick(t) for t in (u, dt)] + [A, pick(Bm), pick(C)]
+        kw = dict(D=skip, z=pick(z), dt_bias=bias, s_in=pick(s_in), lengths=pick(lens))
+        if back:
+            r = la.la_ssm_scan_bwd(*a, pick(dy), ds_out=pick(s_in), **kw)
+            return [r[k] for k in (0, 1, 3, 4, 6, 8)]  # what is not summed over sequences
+        return la.la_ssm_scan(*a, y=torch.zeros_like(a[0]), **kw)
+
+    for back in (False, True):
+        for k, (one, all_) in enumerate(zip(scan(lambda t: t[at], back), scan(lambda t: t, back))):
+            assert torch.equal(one, all_[at]), (back, k)
+    w, b, st = rnd(D, W, e=F32), rnd(D, e=F32), rnd(B, W - 1, D)
+    conv = lambda pick: la.la_short_conv(pick(u), w, b, pick(st), lengths=pick(lens), y=torch.zeros_like(pick(u)), want_state=True)  # noqa: E731
+    for one, all_ in zip(conv(lambda t: t[at]), conv(lambda t: t)):
+        assert torch.equal(one, all_[at])
+    one, all_ = (la.la_short_conv_bwd(p(u), w, p(dy), b, p(st), p(st), lengths=p(lens)) for p in (lambda t: t[at], lambda t: t))
+    assert torch.equal(one[0], all_[0][at]) and torch.equal(one[3], all_[3][at])
+    pools = [s_in[at].clone(), s_in], [st[at].clone(), st]
+    y = [la.la_ssm_step(p(u)[:, 0], p(dt)[:, 0], A, p(Bm)[:, 0], p(C)[:, 0], s, D=skip, z=p(z)[:, 0], dt_bias=bias)
+         for p, s in zip((lambda t: t[at], lambda t: t), pools[0])]
+    assert torch.equal(y[0], y[1][at]) and torch.equal(pools[0][0], s_in[at])
+    y = [la.la_short_conv_step(p(u)[:, 1], w, s, b) for p, s in zip((lambda t: t[at], lambda t: t), pools[1])]
+    assert torch.equal(y[0], y[1][at]) and torch.equal(pools[1][0], st[at])
+
+
+@pytest.mark.parametrize("M,D", [(1 << 25, 8), (1 << 25, 3), ((1 << 22) + 5, 2048), ((1 << 19) + 3, 16384)])
+def test_norm_of_the_most_rows(M, D):
+    """2^25 rows, and rows past 2^33 elements: rows from the start, the middle and the end give what they give alone; the
+    backward's dx likewise, and d_weight of repeated rows is the repeated rows' sum.  Each of 512 workgroups adds at most
+    M / 512 + 1 rows one after the other, then come at most 4 + 32 + 16 partial sums: K = M / 512 + 64 on top of a
+    term's own roundings, 8."""
+    note(f"norm of the most rows {M} {D}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    R_ = 4096
+    few = torch.randn(R_, D, generator=g, device="cuda").to(BF)
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    reps = -(-M // R_)
+    x = few.repeat(reps, 1)[:M]
+    y1, _, r1 = la.la_add_norm(few, w)
+    y, _, r = la.la_add_norm(x, w)
+    at = torch.cat([torch.arange(k, k + 40) for k in (0, M // 2 - 7, M - 40)]).cuda()
+    assert torch.equal(y[at], y1[at % R_]) and torch.equal(r, r1.repeat(reps)[:M])
+    del y
+    q1, s1, _, _ = la.la_add_norm_q8(few, w)
+    q, s, _, _ = la.la_add_norm_q8(x, w)
+    assert torch.equal(q[at].view(torch.uint8), q1[at % R_].view(torch.uint8)) and torch.equal(s, s1.repeat(reps, 1)[:M])
+    del q
+    dx, dw = la.la_add_norm_bwd(x, x, w, r)
+    dx2, _ = la.la_add_norm_bwd(few, few, w, r1)
+    assert torch.equal(dx[at], dx2[at % R_])
+    xh = R.f64(few) * R.f64(r1)[:, None]
+    times = np.full((R_, 1), M // R_) + (np.arange(R_)[:, None] < M % R_)
+    R.close(dw, (R.f64(few) * xh * times).sum(0), (np.abs(R.f64(few) * xh) * times).sum(0), M / 512 + 72, F32, "dw")
