@@ -501,3 +501,44 @@ def test_norm_of_the_most_rows(M, D):
     xh = R.f64(few) * R.f64(r1)[:, None]
     times = np.full((R_, 1), M // R_) + (np.arange(R_)[:, None] < M % R_)
     R.close(dw, (R.f64(few) * xh * times).sum(0), (np.abs(R.f64(few) * xh) * times).sum(0), M / 512 + 72, F32, "dw")
+
+
+def test_padded_layer_in_a_graph():
+    """A padded batch, forward and backward, captured once and replayed with other inputs and other lengths, NaN in the
+    padding, eager work between the replays: every replay gives what the eager call gives."""
+    note("padded layer in a graph")
+    B, L, D, N, W = 3, 150, 64, 16, 4
+    p, pin, pdbc, wx, wp = layer(D, N, W, 57)
+    g = Draw(58)
+
+    def inputs(lens):
+        live = (torch.arange(L)[None] < torch.tensor(lens)[:, None])[..., None].cuda()
+        t = [torch.where(live, g.normal(B, L, D), torch.full((), float("nan"), device="cuda")) for _ in range(3)]
+        return t + [g.normal(B, L, D), ints(lens)]
+
+    def both(x, res, dy, dh, lens):
+        saved = {}
+        out = pipeline.selective_prompt(p, x, res, pin, pdbc, lengths=lens, saved=saved)
+        gr = pipeline.selective_backward(p, saved, dy, lambda ddt, dB, dC: torch.cat([ddt, dB, dC], -1) @ wp.t(),
+                                         lambda du, dz: torch.cat([du, dz], -1).view(B * L, -1) @ wx.t(), dh=dh)
+        return [out[0], out[2], out[3]] + [t for t in gr.values() if t is not None]
+
+    sets = [inputs(n) for n in ([150, 3, 97], [0, 150, 40], [1, 2, 149], [150, 150, 150])]
+    eager = [both(*s) for s in sets]
+    bufs = [t.clone() for t in sets[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(*bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both(*bufs)
+    for k in (1, 2, 3, 0, 2):
+        for t, v in zip(bufs, sets[k]):
+            t.copy_(v)
+        graph.replay()
+        other = both(*sets[(k + 1) % 4])
+        torch.cuda.synchronize()
+        for i, (a, b, c, d) in enumerate(zip(outs, eager[k], other, eager[(k + 1) % 4])):
+            assert torch.isfinite(b).all() and torch.equal(a, b) and torch.equal(c, d), (k, i)
