@@ -175,10 +175,11 @@ def _own(s):
     if op == "step":
         return la.la_gated_step(*a, s["state"], slots=s["slots"], **kw), s["state"]
     kw.update(h_in=get("h_in"), lengths=get("lengths"))
-    out = la.la_gated_scan(*a, y=s["y"], **kw)
-    if op == "scan_train":
-        out = tuple(out) + tuple(la.la_gated_scan_bwd(*a, s["dy"], dh_out=s["dh_out"], **kw))
-    return out
+    if op == "scan":
+        return la.la_gated_scan(*a, y=s["y"], **kw)[:2]
+    # the states that enter every 64 tokens, kept for the backward
+    y, h_out, blocks = la.la_gated_scan(*a, y=s["y"], want_blocks=True, **kw)
+    return (y, h_out) + tuple(la.la_gated_scan_bwd(*a, s["dy"], dh_out=s["dh_out"], h_blocks=blocks, **kw))
 
 
 # ------------------------------------------------------------------------------- the plain form
