@@ -6,7 +6,8 @@ binding to it and the seeded synthetic input generators.  Importing the package 
 the library; the first call of a binding function does, and fails loudly if it is missing.
 """
 _MIXER = ("la_short_conv", "la_short_conv_bwd", "la_short_conv_step", "la_ssm_scan", "la_ssm_scan_bwd", "la_ssm_step",
-          "la_add_norm", "la_add_norm_q8", "la_add_norm_bwd")
+          "la_add_norm", "la_add_norm_q8", "la_add_norm_bwd", "la_gated_scan", "la_gated_scan_bwd", "la_gated_step",
+          "la_block_norm", "la_block_norm_bwd", "la_dropout")
 
 __all__ = ["la_chunk_fwd", "la_state_scan", "la_state_correct", "la_cumdecay", "inputs", *_MIXER]
 

@@ -32,7 +32,11 @@ EXPORTS = ("la_chunk_fwd", "la_chunk_fwd_noalloc", "la_chunk_fwd_decayed", "la_c
            "la_cumdecay", "la_trim_workspace", "la_chain_status", "la_set_chain_spin_limit", "la_status_str", "la_supported",
            "la_version", "la_short_conv", "la_short_conv_bwd_workspace", "la_short_conv_bwd", "la_short_conv_step",
            "la_ssm_workspace", "la_ssm_scan", "la_ssm_scan_bwd", "la_ssm_step", "la_add_norm", "la_add_norm_q8",
-           "la_add_norm_bwd_workspace", "la_add_norm_bwd")
+           "la_add_norm_bwd_workspace", "la_add_norm_bwd", "la_gated_scan_workspace", "la_gated_scan",
+           "la_gated_scan_bwd", "la_gated_step", "la_block_norm", "la_block_norm_bwd_workspace", "la_block_norm_bwd",
+           "la_dropout")
+GATED_BLOCK = 64  # LA_GATED_BLOCK of la_chunk.h
+GATE_ACTS = {"linear": 0, "sigmoid": 1, "silu": 2}
 
 
 TRACE_MAX = 16
@@ -86,6 +90,27 @@ class NormShape(ctypes.Structure):
         ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("x_stride", ctypes.c_int64),
         ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64),
         ("dy_stride", ctypes.c_int64), ("dh_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
+    ]
+
+
+class GatedShape(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("c", ctypes.c_float), ("nslots", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("x", Rows), ("r", Rows), ("i", Rows), ("z", Rows), ("y", Rows),
+        ("dy", Rows), ("dx", Rows), ("dr", Rows), ("di", Rows), ("dz", Rows),
+        ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
+    ]
+
+
+class BlockShape(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("p", ctypes.c_float), ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64), ("dh_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64),
+        ("dgate_stride", ctypes.c_int64), ("dresidual_stride", ctypes.c_int64),
         ("stream", ctypes.c_void_p), ("trace", ctypes.POINTER(Trace)),
     ]
 
@@ -163,10 +188,21 @@ def lib() -> ctypes.CDLL:
         L.la_add_norm_q8.argtypes = [P] * 7 + [NS]
         L.la_add_norm_bwd_workspace.argtypes = [NS]
         L.la_add_norm_bwd.argtypes = [P] * 8 + [U64, NS]
+        GS, BS = ctypes.POINTER(GatedShape), ctypes.POINTER(BlockShape)
+        L.la_gated_scan_workspace.argtypes = [GS, ctypes.c_int32]
+        L.la_gated_scan.argtypes = [P] * 13 + [U64, GS]
+        L.la_gated_scan_bwd.argtypes = [P] * 21 + [U64, GS]
+        L.la_gated_step.argtypes = [P] * 10 + [GS]
+        L.la_block_norm.argtypes = [P] * 11 + [BS]
+        L.la_block_norm_bwd_workspace.argtypes = [BS]
+        L.la_block_norm_bwd.argtypes = [P] * 18 + [U64, BS]
+        L.la_dropout.argtypes = [P] * 4 + [BS]
         for f in (L.la_short_conv, L.la_short_conv_bwd, L.la_short_conv_step, L.la_ssm_scan, L.la_ssm_scan_bwd,
-                  L.la_ssm_step, L.la_add_norm, L.la_add_norm_q8, L.la_add_norm_bwd):
+                  L.la_ssm_step, L.la_add_norm, L.la_add_norm_q8, L.la_add_norm_bwd, L.la_gated_scan, L.la_gated_scan_bwd,
+                  L.la_gated_step, L.la_block_norm, L.la_block_norm_bwd, L.la_dropout):
             f.restype = ctypes.c_int
-        for f in (L.la_short_conv_bwd_workspace, L.la_ssm_workspace, L.la_add_norm_bwd_workspace):
+        for f in (L.la_short_conv_bwd_workspace, L.la_ssm_workspace, L.la_add_norm_bwd_workspace,
+                  L.la_gated_scan_workspace, L.la_block_norm_bwd_workspace):
             f.restype = ctypes.c_int64
         _lib = L
     return _lib
@@ -876,3 +912,231 @@ def la_add_norm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rst
         _check("la_add_norm_bwd", lib().la_add_norm_bwd(_at(dy), _at(h), _at(weight), _at(rstd), _at(dh), _at(dx),
                                                         _at(dw), _at(ws), n, ctypes.byref(shp)))
     return dx, dw
+
+
+# ------------------------------------------------------------------------------------------------
+# Gated recurrent layer: the gated recurrence, the norms around a block, dropout.  Views, devices and streams as above.
+
+
+def _gated_common(on, x, r, i, lam, r_bias, i_bias, z, wide):
+    e, f32, check = x.dtype, torch.float32, on.check
+    per_channel = wide[-1:]
+    check(x, "x", e, wide, False)
+    check(r, "r", e, wide, False)
+    check(i, "i", e, wide, False)
+    check(lam, "lam", f32, per_channel)
+    check(r_bias, "r_bias", f32, per_channel)
+    check(i_bias, "i_bias", f32, per_channel)
+    check(z, "z", e, wide, False)
+
+
+def la_gated_scan(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor, *,
+                  r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                  z: Optional[torch.Tensor] = None, h_in: Optional[torch.Tensor] = None,
+                  lengths: Optional[torch.Tensor] = None, c: float = 8.0, y: Optional[torch.Tensor] = None,
+                  h_out: Optional[torch.Tensor] = None, want_state: bool = True,
+                  h_blocks: Optional[torch.Tensor] = None, want_blocks: bool = False, stream=None, timer=None):
+    """Gated linear recurrence: h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(i_t + i_bias) x_t with
+    a_t = exp(-c softplus(lam) sigma(r_t + r_bias)), y_t = h_t silu(z_t).  x, r, i, z [B,L,D] (f32 or bf16, strided rows
+    allowed), lam, r_bias and i_bias f32 [D], h_in f32 [B,D], lengths int32 [B].  Returns (y [B,L,D], h_out f32 [B,D] or
+    None, h_blocks f32 [B, ceil(L / 64), D] or None): the last, the states that enter every 64 tokens, spare
+    la_gated_scan_bwd a pass over the inputs.  h_out may be h_in.  Rows of y (and blocks) behind a sequence's length are
+    left as they were."""
+    B, L, D = _dims(x, "x", 3)
+    code = _dtype_code(x)
+    f32 = torch.float32
+    with _On(x, "x", stream) as on:
+        _gated_common(on, x, r, i, lam, r_bias, i_bias, z, x.shape)
+        on.check(h_in, "h_in", f32, (B, D))
+        on.check(lengths, "lengths", torch.int32, (B,))
+        y = on.out(y, "y", x.dtype, (B, L, D), dense=False)
+        if h_out is not None or want_state:
+            h_out = on.out(h_out, "h_out", f32, (B, D))
+        if h_blocks is not None or want_blocks:
+            h_blocks = on.out(h_blocks, "h_blocks", f32, (B, -(-L // GATED_BLOCK), D))
+        shp = _finish(GatedShape(B, L, D, code, c), on, timer)
+        _strided(shp, x=x, r=r, i=i, z=z, y=y)
+        n = lib().la_gated_scan_workspace(ctypes.byref(shp), 0)
+        ws = on.workspace("la_gated_scan_workspace", n)
+        _check("la_gated_scan", lib().la_gated_scan(_at(x), _at(r), _at(i), _at(lam), _at(r_bias), _at(i_bias), _at(z),
+                                                    _at(h_in), _at(lengths), _at(y), _at(h_out), _at(h_blocks), _at(ws),
+                                                    n, ctypes.byref(shp)))
+    return y, h_out, h_blocks
+
+
+def la_gated_scan_bwd(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor, dy: torch.Tensor, *,
+                      r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                      z: Optional[torch.Tensor] = None, h_in: Optional[torch.Tensor] = None,
+                      lengths: Optional[torch.Tensor] = None, h_blocks: Optional[torch.Tensor] = None,
+                      dh_out: Optional[torch.Tensor] = None, c: float = 8.0, dx: Optional[torch.Tensor] = None,
+                      dr: Optional[torch.Tensor] = None, di: Optional[torch.Tensor] = None,
+                      dz: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """Backward of la_gated_scan from dy [B,L,D] and dh_out f32 [B,D] (None: zero); h_blocks: the forward's, or None.
+    Returns (dx, dr, di, dlam, dr_bias, di_bias, dz, dh_in); those of arguments that are None are None.  dx, dr, di and
+    dz may be given as strided views (slices of a projection's gradient); they are zero behind a sequence's length."""
+    B, L, D = _dims(x, "x", 3)
+    code = _dtype_code(x)
+    f32 = torch.float32
+    with _On(x, "x", stream) as on:
+        _gated_common(on, x, r, i, lam, r_bias, i_bias, z, x.shape)
+        on.check(dy, "dy", x.dtype, (B, L, D), dense=False)
+        on.check(h_in, "h_in", f32, (B, D))
+        on.check(dh_out, "dh_out", f32, (B, D))
+        on.check(lengths, "lengths", torch.int32, (B,))
+        on.check(h_blocks, "h_blocks", f32, (B, -(-L // GATED_BLOCK), D))
+        if z is None and dz is not None:
+            raise ValueError("dz without z")
+        dx = on.out(dx, "dx", x.dtype, (B, L, D), dense=False)
+        dr = on.out(dr, "dr", x.dtype, (B, L, D), dense=False)
+        di = on.out(di, "di", x.dtype, (B, L, D), dense=False)
+        dz = on.out(dz, "dz", x.dtype, (B, L, D), dense=False) if z is not None else None
+        dlam = on.out(None, "dlam", f32, (D,))
+        drb = on.out(None, "dr_bias", f32, (D,)) if r_bias is not None else None
+        dib = on.out(None, "di_bias", f32, (D,)) if i_bias is not None else None
+        dh_in = on.out(None, "dh_in", f32, (B, D)) if h_in is not None else None
+        shp = _finish(GatedShape(B, L, D, code, c), on, timer)
+        _strided(shp, x=x, r=r, i=i, z=z, dy=dy, dx=dx, dr=dr, di=di, dz=dz)
+        n = lib().la_gated_scan_workspace(ctypes.byref(shp), 2 if _at(h_blocks) else 1)
+        ws = on.workspace("la_gated_scan_workspace", n)
+        _check("la_gated_scan_bwd", lib().la_gated_scan_bwd(
+            _at(x), _at(r), _at(i), _at(lam), _at(r_bias), _at(i_bias), _at(z), _at(h_in), _at(lengths), _at(h_blocks),
+            _at(dy), _at(dh_out), _at(dx), _at(dr), _at(di), _at(dlam), _at(drb), _at(dib), _at(dz), _at(dh_in), _at(ws), n,
+            ctypes.byref(shp)))
+    return dx, dr, di, dlam, drb, dib, dz, dh_in
+
+
+def la_gated_step(x: torch.Tensor, r: torch.Tensor, i: torch.Tensor, lam: torch.Tensor, state: torch.Tensor, *,
+                  r_bias: Optional[torch.Tensor] = None, i_bias: Optional[torch.Tensor] = None,
+                  z: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, c: float = 8.0,
+                  y: Optional[torch.Tensor] = None, stream=None, timer=None) -> torch.Tensor:
+    """One token of each of B sequences of la_gated_scan.  x, r, i, z [B,D]; state f32 [S,D], updated in place; slots
+    as in la_short_conv_step.  Returns y [B,D]."""
+    B, D = _dims(x, "x", 2)
+    S = _dims(state, "state", 2)[0]
+    code = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        _gated_common(on, x, r, i, lam, r_bias, i_bias, z, x.shape)
+        on.check(state, "state", torch.float32, (S, D))
+        on.check(slots, "slots", torch.int32, (B,))
+        y = on.out(y, "y", x.dtype, (B, D), dense=False)
+        shp = _finish(GatedShape(B, 1, D, code, c, S), on, timer)
+        _strided(shp, x=x, r=r, i=i, z=z, y=y)
+        _check("la_gated_step", lib().la_gated_step(_at(x), _at(r), _at(i), _at(lam), _at(r_bias), _at(i_bias), _at(z),
+                                                    _at(state), _at(slots), _at(y), ctypes.byref(shp)))
+    return y
+
+
+def _act_code(act: str) -> int:
+    if act not in GATE_ACTS:
+        raise ValueError(f"act must be one of {', '.join(GATE_ACTS)}, not {act!r}")
+    return GATE_ACTS[act]
+
+
+def _rng(on, rng, p):
+    if p > 0 and rng is None:
+        raise ValueError("p > 0 needs rng, an int64 [2] device tensor of seed and offset")
+    return on.check(rng, "rng", torch.int64, (2,))
+
+
+def _block_common(on, x, gate, w_post, scale, w_pre):
+    M, D = x.shape
+    on.check(x, "x", x.dtype, (M, D), dense=False)
+    on.check(gate, "gate", x.dtype, (M, D), dense=False)
+    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
+        on.check(t, name, torch.float32, (D,))
+
+
+def la_block_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
+                  w_pre: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, act: str = "silu",
+                  scale: Optional[torch.Tensor] = None, p: float = 0.0, rng: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None,
+                  timer=None):
+    """From a block's output x [M,D] to the next one's input: u = norm(x) w_post act(gate) scale, h = residual + drop(u),
+    y = norm(h) w_pre, norms by root mean square.  gate and residual [M,D] (strided rows allowed), w_post, scale and
+    w_pre f32 [D]; what is None is left out.  act: linear, sigmoid or silu.  p: the share dropped, from the generator
+    whose seed and offset stand in rng (int64 [2] on the device, read when the kernels run).  Returns (y or None, h
+    [M,D], rstd_post f32 [M] or None, rstd_pre f32 [M] or None); h may be given as residual or x (updated in place)."""
+    M, D = _dims(x, "x", 2)
+    code, kind = _dtype_code(x), _act_code(act)
+    with _On(x, "x", stream) as on:
+        _block_common(on, x, gate, w_post, scale, w_pre)
+        on.check(residual, "residual", x.dtype, (M, D), dense=False)
+        _rng(on, rng, p)
+        h = on.out(h, "h", x.dtype, (M, D), dense=False)
+        if w_pre is not None:
+            y = on.out(y, "y", x.dtype, (M, D), dense=False)
+        elif y is not None:
+            raise ValueError("y without w_pre")
+        rp = on.out(None, "rstd_post", torch.float32, (M,)) if w_post is not None else None
+        rq = on.out(None, "rstd_pre", torch.float32, (M,)) if w_pre is not None else None
+        shp = _finish(BlockShape(M, D, code, kind, eps, p, x_stride=_row_stride(x, "x"),
+                                 gate_stride=_row_stride(gate, "gate"), residual_stride=_row_stride(residual, "residual"),
+                                 y_stride=_row_stride(y, "y"), h_stride=_row_stride(h, "h")), on, timer)
+        _check("la_block_norm", lib().la_block_norm(_at(x), _at(gate), _at(residual), _at(w_post), _at(scale), _at(w_pre),
+                                                    _at(rng), _at(y), _at(h), _at(rp), _at(rq), ctypes.byref(shp)))
+    return y, h, rp, rq
+
+
+def la_block_norm_bwd(x: torch.Tensor, h: Optional[torch.Tensor], dy: Optional[torch.Tensor],
+                      dh: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
+                      w_pre: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, act: str = "silu",
+                      scale: Optional[torch.Tensor] = None, p: float = 0.0, rng: Optional[torch.Tensor] = None,
+                      rstd_post: Optional[torch.Tensor] = None, rstd_pre: Optional[torch.Tensor] = None,
+                      dx: Optional[torch.Tensor] = None, dresidual: Optional[torch.Tensor] = None,
+                      dgate: Optional[torch.Tensor] = None, stream=None, timer=None):
+    """Backward of la_block_norm from dy [M,D] (with w_pre, else None) and dh [M,D] (the derivative that reaches h along
+    the residual stream; None: zero), with the forward's h, rstd_post and rstd_pre, its p and what rng held then.
+    Returns (dx, dresidual, dgate, dw_post, dw_pre, dscale), None for what has no argument; dresidual may be given as
+    dh or dy."""
+    M, D = _dims(x, "x", 2)
+    code, kind, f32 = _dtype_code(x), _act_code(act), torch.float32
+    with _On(x, "x", stream) as on:
+        _block_common(on, x, gate, w_post, scale, w_pre)
+        for t, name in ((h, "h"), (dy, "dy"), (dh, "dh")):
+            on.check(t, name, x.dtype, (M, D), dense=False)
+        on.check(rstd_post, "rstd_post", f32, (M,))
+        on.check(rstd_pre, "rstd_pre", f32, (M,))
+        if w_pre is not None and (h is None or dy is None or rstd_pre is None):
+            raise ValueError("w_pre needs h, dy and rstd_pre")
+        if w_pre is None and dy is not None:
+            raise ValueError("dy without w_pre")
+        if w_post is not None and rstd_post is None:
+            raise ValueError("w_post needs rstd_post")
+        if gate is None and dgate is not None:
+            raise ValueError("dgate without gate")
+        _rng(on, rng, p)
+        dx = on.out(dx, "dx", x.dtype, (M, D), dense=False)
+        dresidual = on.out(dresidual, "dresidual", x.dtype, (M, D), dense=False)
+        dgate = on.out(dgate, "dgate", x.dtype, (M, D), dense=False) if gate is not None else None
+        dwp = on.out(None, "dw_post", f32, (D,)) if w_post is not None else None
+        dwq = on.out(None, "dw_pre", f32, (D,)) if w_pre is not None else None
+        dsc = on.out(None, "dscale", f32, (D,)) if scale is not None else None
+        shp = _finish(BlockShape(M, D, code, kind, 1.0, p, x_stride=_row_stride(x, "x"),
+                                 gate_stride=_row_stride(gate, "gate"), h_stride=_row_stride(h, "h"),
+                                 dy_stride=_row_stride(dy, "dy"), dh_stride=_row_stride(dh, "dh"),
+                                 dx_stride=_row_stride(dx, "dx"), dgate_stride=_row_stride(dgate, "dgate"),
+                                 dresidual_stride=_row_stride(dresidual, "dresidual")), on, timer)
+        n = lib().la_block_norm_bwd_workspace(ctypes.byref(shp))
+        ws = on.workspace("la_block_norm_bwd_workspace", n)
+        _check("la_block_norm_bwd", lib().la_block_norm_bwd(
+            _at(x), _at(gate), _at(h), _at(w_post), _at(scale), _at(w_pre), _at(rng), _at(rstd_post), _at(rstd_pre), _at(dy),
+            _at(dh), _at(dx), _at(dgate), _at(dresidual), _at(dwp), _at(dsc), _at(dwq), _at(ws), n, ctypes.byref(shp)))
+    return dx, dresidual, dgate, dwp, dwq, dsc
+
+
+def la_dropout(x: torch.Tensor, rng: Optional[torch.Tensor], p: float, residual: Optional[torch.Tensor] = None, *,
+               y: Optional[torch.Tensor] = None, stream=None, timer=None) -> torch.Tensor:
+    """residual + drop(x) (residual None: drop(x)), rows [M,D] (f32 or bf16, strided rows allowed): a share p of the
+    elements is zero, the others are divided by the share kept.  rng: int64 [2] on the device, the generator's seed and
+    offset.  The same call on dy, without residual, is the backward pass.  y may be given as x or residual."""
+    M, D = _dims(x, "x", 2)
+    code = _dtype_code(x)
+    with _On(x, "x", stream) as on:
+        on.check(x, "x", x.dtype, (M, D), dense=False)
+        on.check(residual, "residual", x.dtype, (M, D), dense=False)
+        _rng(on, rng, p)
+        y = on.out(y, "y", x.dtype, (M, D), dense=False)
+        shp = _finish(BlockShape(M, D, code, 0, 1.0, p, x_stride=_row_stride(x, "x"),
+                                 residual_stride=_row_stride(residual, "residual"), y_stride=_row_stride(y, "y")), on, timer)
+        _check("la_dropout", lib().la_dropout(_at(x), _at(residual), _at(rng), _at(y), ctypes.byref(shp)))
+    return y

@@ -331,15 +331,6 @@ hipError_t launch_t(const SsmArgs& a) {
 // per wave and key dim; with many rows a wave takes R of them one after the other, the next row's loads in
 // flight, so that its rates (A's rows, N floats apart from lane to lane) are loaded once for all of them.
 // B and C are loaded once per wave and row, lane n holding B[n] and C[n], and broadcast by lane reads.
-// Rows that name a slot an earlier row names are padding, so that no two rows write one state.  Every wave looks
-// through the earlier rows' slots, which is quadratic in the rows: nothing at a few thousand; 65536 rows of 64 channels
-// take 1.15 ms, 0.09 without slots.
-__device__ __forceinline__ bool earlier_row_has(const int32_t* slots, int64_t b, int32_t s) {
-    bool dup = false;
-    for (int64_t i = threadIdx.x & 63; i < b; i += 64) dup |= slots[i] == s;
-    return __any(dup);
-}
-
 struct StepDev {
     const void* u;
     const void* dt;

@@ -43,6 +43,14 @@ around the caller's two projections (which are not part of the library):
 ``selective_token``  -- the same for one token of each of several running sequences, whose convolution and scan
                      states live in pools.
 ``selective_backward`` -- the prompt's operators in reverse, the projections' own backward left to the caller.
+
+The gated recurrent layer, whose state is one value per channel, likewise, from one pre-norm's output to the next one's:
+
+``gated_prompt``   -- projection to the recurrence's input and output gate, short convolution, projection to the
+                     recurrence's gates, gated recurrence, projection back, then the norm after the block, its gate, residual
+                     scale, dropout, the residual sum and the norm before the next block.
+``gated_token``    -- the same for one token of each of several running sequences, states in pools.
+``gated_backward`` -- the prompt's operators in reverse.
 """
 from __future__ import annotations
 
@@ -51,9 +59,10 @@ from typing import Callable, Optional, Tuple
 
 import torch
 
-from .binding import (la_add_norm, la_add_norm_bwd, la_add_norm_q8, la_chunk_fwd, la_chunk_fwd_decayed, la_cumdecay,
-                      la_short_conv, la_short_conv_bwd, la_short_conv_step, la_ssm_scan, la_ssm_scan_bwd, la_ssm_step,
-                      la_state_correct, la_state_scan)
+from .binding import (la_add_norm, la_add_norm_bwd, la_add_norm_q8, la_block_norm, la_block_norm_bwd, la_chunk_fwd,
+                      la_chunk_fwd_decayed, la_cumdecay, la_gated_scan, la_gated_scan_bwd, la_gated_step, la_short_conv,
+                      la_short_conv_bwd, la_short_conv_step, la_ssm_scan, la_ssm_scan_bwd, la_ssm_step, la_state_correct,
+                      la_state_scan)
 
 
 def _tile_flags(B, H, L, nseg, dev):
@@ -323,3 +332,106 @@ def selective_token(p: SelectiveParams, x: torch.Tensor, residual: Optional[torc
     v = la_short_conv_step(u, p.conv_weight, conv_pool, p.conv_bias, slots=slots)
     dt, Bm, C = project_dbc(v)
     return la_ssm_step(v, dt, p.A, Bm, C, state_pool, D=p.skip, z=z, dt_bias=p.dt_bias, slots=slots), h
+
+
+@dataclass
+class GatedParams:
+    """A gated recurrent layer's own parameters, all float32: conv_weight [D, W], conv_bias [D] or None; lam [D], r_bias
+    and i_bias [D] or None, c the log-decay's scale; w_post and scale [Dm] or None (the norm after the block and the
+    residual scale), w_pre [Dm] or None (the norm before the next block); act the output gate's activation, dropout the
+    share of the branch that is dropped."""
+    conv_weight: torch.Tensor
+    conv_bias: Optional[torch.Tensor]
+    lam: torch.Tensor
+    r_bias: Optional[torch.Tensor] = None
+    i_bias: Optional[torch.Tensor] = None
+    c: float = 8.0
+    w_post: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+    w_pre: Optional[torch.Tensor] = None
+    act: str = "silu"
+    dropout: float = 0.0
+    eps: float = 1e-5
+
+    def scan(self):
+        return dict(r_bias=self.r_bias, i_bias=self.i_bias, c=self.c)
+
+    def norms(self):
+        return dict(w_post=self.w_post, w_pre=self.w_pre, scale=self.scale, act=self.act)
+
+
+def _blank_rows(t: Optional[torch.Tensor], pad):
+    """``t`` [rows, n] with the rows of ``pad``, a mask [rows, 1], zero; ``t`` itself without a mask."""
+    return t if t is None or pad is None else t.masked_fill(pad, 0)
+
+
+def gated_prompt(p: GatedParams, n: torch.Tensor, residual: Optional[torch.Tensor], project_in: Callable,
+                 project_gates: Callable, project_out: Callable, *, conv_state: Optional[torch.Tensor] = None,
+                 h_in: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                 rng: Optional[torch.Tensor] = None, saved: Optional[dict] = None) -> Tuple[torch.Tensor, ...]:
+    """One layer over n [B, L, Dm], the normed rows (a layer's y or the first norm's), and the residual stream (the same
+    shape, or None).  project_in maps n's rows [B L, Dm] to (u, z): two [B L, D] tensors, z possibly None; project_gates
+    the convolved [B, L, D] to (r, i): two [B, L, D]; project_out the recurrence's rows [B L, D] to (x, gate): two
+    [B L, Dm], gate possibly None.  Rows of n and residual behind a sequence's length may hold anything and count as
+    zero.  conv_state [B, W-1, D] and h_in [B, D]: states of the tokens before, or None; rng: dropout's seed and
+    offset.  Returns (y [B, L, Dm] the next layer's n or None without w_pre, h [B, L, Dm] the residual stream, conv_state,
+    h_out).  `saved`, a dict, receives what gated_backward takes."""
+    B, L, Dm = n.shape
+    pad = _padding(lengths, B, L, n.device)
+    rows = lambda t: None if t is None else t.reshape(B * L, Dm)  # noqa: E731
+    u, z = (None if t is None else t.unflatten(0, (B, L)) for t in project_in(_blank_rows(rows(n), pad)))
+    # rows behind a sequence's length are not written: they are zero here, so that a product over all rows stays finite
+    blank = lambda: None if lengths is None else torch.zeros(u.shape, dtype=u.dtype, device=u.device)  # noqa: E731
+    v, conv_out = la_short_conv(u, p.conv_weight, p.conv_bias, conv_state, lengths=lengths, silu=False, y=blank(),
+                                want_state=True)
+    r, i = project_gates(v)
+    o, h_out, blocks = la_gated_scan(v, r, i, p.lam, z=z, h_in=h_in, lengths=lengths, y=blank(),
+                                     want_blocks=saved is not None, **p.scan())
+    x, gate = project_out(o.view(B * L, -1))
+    y, h, rstd_post, rstd_pre = la_block_norm(x, _blank_rows(rows(residual), pad), gate=gate, p=p.dropout, rng=rng,
+                                              eps=p.eps, **p.norms())
+    if saved is not None:
+        saved.update(u=u, z=z, v=v, r=r, i=i, conv_state=conv_state, h_in=h_in, lengths=lengths, blocks=blocks, x=x,
+                     gate=gate, h=h, rstd_post=rstd_post, rstd_pre=rstd_pre, rng=rng)
+    return None if y is None else y.view(B, L, Dm), h.view(B, L, Dm), conv_out, h_out
+
+
+def gated_backward(p: GatedParams, saved: dict, dy: Optional[torch.Tensor], dh: Optional[torch.Tensor],
+                   out_backward: Callable, gates_backward: Callable, in_backward: Callable, *,
+                   d_conv_state: Optional[torch.Tensor] = None, dh_out: Optional[torch.Tensor] = None) -> dict:
+    """Backward of gated_prompt from dy [B, L, Dm] (None without w_pre), dh [B, L, Dm] (the residual stream's derivative,
+    or None) and those of the returned states; rows behind a sequence's length count as zero.  out_backward maps
+    (dx, dgate) [B L, Dm] to the recurrence's rows' derivative [B L, D]; gates_backward (dr, di) to the convolved tensor's
+    part [B, L, D]; in_backward (du, dz), zero behind a sequence's length, to n's rows' [B L, Dm].  Returns dn and
+    dresidual and the parameters' and incoming states' derivatives by name."""
+    s = saved
+    B, L, D = s["u"].shape
+    Dm = s["x"].shape[1]
+    pad = _padding(s["lengths"], B, L, s["x"].device)
+    rows = lambda t: _blank_rows(None if t is None else t.reshape(B * L, Dm), pad)  # noqa: E731
+    dx, dres, dgate, dw_post, dw_pre, dscale = la_block_norm_bwd(
+        s["x"], s["h"] if p.w_pre is not None else None, rows(dy), rows(dh), gate=s["gate"], p=p.dropout, rng=s["rng"],
+        rstd_post=s["rstd_post"], rstd_pre=s["rstd_pre"], **p.norms())
+    do = out_backward(dx, dgate).view(B, L, D)
+    dv, dr, di, dlam, dr_bias, di_bias, dz, dh_in = la_gated_scan_bwd(
+        s["v"], s["r"], s["i"], p.lam, do, z=s["z"], h_in=s["h_in"], lengths=s["lengths"], h_blocks=s["blocks"],
+        dh_out=dh_out, **p.scan())
+    dv += gates_backward(dr, di)
+    du, dcw, dcb, d_conv = la_short_conv_bwd(s["u"], p.conv_weight, dv, p.conv_bias, s["conv_state"], d_conv_state,
+                                             lengths=s["lengths"], silu=False)
+    dn = in_backward(du, dz)
+    return dict(dn=dn.view(B, L, Dm), dresidual=dres.view(B, L, Dm), conv_weight=dcw, conv_bias=dcb, lam=dlam,
+                r_bias=dr_bias, i_bias=di_bias, w_post=dw_post, w_pre=dw_pre, scale=dscale, conv_state=d_conv, h_in=dh_in)
+
+
+def gated_token(p: GatedParams, n: torch.Tensor, residual: Optional[torch.Tensor], project_in: Callable,
+                project_gates: Callable, project_out: Callable, conv_pool: torch.Tensor, state_pool: torch.Tensor,
+                slots: Optional[torch.Tensor] = None) -> Tuple[Optional[torch.Tensor], torch.Tensor]:
+    """One layer over one token of each of B sequences, n [B, Dm], without dropout; conv_pool [S, W-1, D] and state_pool
+    [S, D] are updated in place at the rows' slots.  Returns (y [B, Dm] or None, h [B, Dm]).  Rows that are padding (a
+    slot outside the pools, or one that an earlier row names) have undefined y and h."""
+    u, z = project_in(n)
+    v = la_short_conv_step(u, p.conv_weight, conv_pool, p.conv_bias, slots=slots, silu=False)
+    r, i = project_gates(v)
+    x, gate = project_out(la_gated_step(v, r, i, p.lam, state_pool, z=z, slots=slots, **p.scan()))
+    return la_block_norm(x, residual, gate=gate, eps=p.eps, **p.norms())[:2]

@@ -570,6 +570,158 @@ la_status la_add_norm_bwd(const void* dy, const void* h, const float* weight, co
                           const void* dh, void* dx, float* d_weight, void* workspace,
                           uint64_t workspace_bytes, const la_norm_shape* shape);
 
+/* ------------------------------------------------------------------------------------------------
+ * Gated recurrent layer: a linear recurrence of one state per channel whose decay and input are gated
+ * by the token, what stands between two blocks (the norms after the one and before the other, a
+ * gate, a residual scale, dropout and the residual sum), and dropout by itself.  Layouts, padded batches, memory, limits
+ * and numerics are those of the selective layer above, with what is said here.
+ *
+ * Workspaces: la_gated_scan and la_gated_scan_bwd 12 bytes per channel and 64 tokens (nothing for sequences of up to
+ * 64 tokens), the backward 12 more for its parameters' derivatives and, without h_blocks, 4 more;
+ * la_block_norm_bwd 12 D bytes per row, of 512 rows at most.
+ *
+ * Random numbers.  Dropout's are Philox4x32-10 (Salmon et al., 2011), so that a mask is made again wherever it is
+ * needed and never stored.  rng points to two uint64 on the device, read when the kernels run: {seed, offset} (a
+ * captured graph that is replayed takes what stands there then).  Row m, channels 8 j .. 8 j + 7 take one call with
+ * key seed and counter (low 64 bits m ceil(D / 8) + j, high 64 bits offset); channel 8 j + i takes bits 16 (i % 2) to
+ * 16 (i % 2) + 15 of its output word i / 2 and is dropped where they are below T = round(65536 p).  What is kept is
+ * multiplied by 65536 / (65536 - T).  The mask depends on seed, offset, T, m and D alone: not on the strides or
+ * the type.  Calls that shall draw apart from each other use different offsets (or seeds).
+ * ---------------------------------------------------------------------------------------------- */
+
+/* Tokens per block of la_gated_scan's h_blocks. */
+#define LA_GATED_BLOCK 64
+
+typedef struct la_gated_shape {
+    int64_t B;         /* sequences, >= 0 */
+    int64_t L;         /* tokens per sequence, >= 0 (la_gated_step: not used) */
+    int64_t D;         /* channels, >= 0 */
+    int32_t dtype;     /* la_dtype of x, r, i, z, y and their gradients */
+    float c;           /* scale of the log-decay, > 0, finite */
+    int32_t nslots;    /* la_gated_step: states in the pool, >= 0 */
+    int32_t reserved;  /* 0 */
+    la_rows x, r, i, z, y;        /* la_gated_step: the batch strides alone */
+    la_rows dy, dx, dr, di, dz;   /* la_gated_scan_bwd */
+    void* stream;
+    la_trace* trace;
+} la_gated_shape;
+
+/* Bytes of workspace of la_gated_scan (backward = 0), of la_gated_scan_bwd without h_blocks (1) or with them (2), or a
+ * negative la_status. */
+int64_t la_gated_scan_workspace(const la_gated_shape* shape, int32_t backward);
+
+/*
+ * Gated linear recurrence over every sequence, with sigma(v) = 1 / (1 + exp(-v)):
+ *        a_t[d] = exp(-c softplus(lam[d]) sigma(r_t[d] + r_bias[d])),
+ *        h_t[d] = a_t[d] h_{t-1}[d] + sqrt(1 - a_t[d]^2) sigma(i_t[d] + i_bias[d]) x_t[d],
+ *        y_t[d] = h_t[d] z_t[d] sigma(z_t[d])                                  (without z: h_t[d]).
+ *   x, r, i : [B,L,D] dtype       lam : float[D], finite        r_bias, i_bias : float[D] or NULL (zero)
+ *   z       : [B,L,D] dtype or NULL (no gate)                   h_in : float[B,D] initial state or NULL (zero)
+ *   y       : [B,L,D] dtype, written                             h_out: float[B,D] final state or NULL; may be the
+ *             same pointer as h_in
+ *   h_blocks: float[B, ceil(L / 64), D] or NULL: the state that enters every 64 tokens, for the backward pass; blocks
+ *             behind a sequence's last token are left as they were.
+ * No output may otherwise overlap another argument.  r = -infinity holds the state (a = 1, no input).  A channel with
+ * a NaN in x, r or i gives NaN from that token on.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED,
+ * LA_ERR_WORKSPACE or LA_ERR_LAUNCH.
+ */
+la_status la_gated_scan(const void* x, const void* r, const void* i, const float* lam, const float* r_bias,
+                        const float* i_bias, const void* z, const float* h_in, const int32_t* lengths, void* y,
+                        float* h_out, float* h_blocks, void* workspace, uint64_t workspace_bytes,
+                        const la_gated_shape* shape);
+
+/*
+ * Backward of la_gated_scan from dy [B,L,D] and dh_out float[B,D] (NULL: zero).  Writes dx, dr, di [B,L,D] dtype,
+ * dlam float[D], dr_bias, di_bias float[D] or NULL, dz [B,L,D] dtype (exactly when z is given), dh_in float[B,D] or
+ * NULL.  h_blocks: what the forward wrote for the same inputs, or NULL (made again: the inputs are read once more).
+ * No output may overlap another argument.
+ * Returns the codes of la_gated_scan.
+ */
+la_status la_gated_scan_bwd(const void* x, const void* r, const void* i, const float* lam, const float* r_bias,
+                            const float* i_bias, const void* z, const float* h_in, const int32_t* lengths,
+                            const float* h_blocks, const void* dy, const float* dh_out, void* dx, void* dr, void* di,
+                            float* dlam, float* dr_bias, float* di_bias, void* dz, float* dh_in, void* workspace,
+                            uint64_t workspace_bytes, const la_gated_shape* shape);
+
+/*
+ * One token of each of B sequences: x, r, i, z, y [B,D]; state float[nslots,D] is a pool that is updated in place;
+ * slots as in la_short_conv_step.
+ * Returns the codes of la_gated_scan but LA_ERR_WORKSPACE.
+ */
+la_status la_gated_step(const void* x, const void* r, const void* i, const float* lam, const float* r_bias,
+                        const float* i_bias, const void* z, float* state, const int32_t* slots, void* y,
+                        const la_gated_shape* shape);
+
+/* The gate's factor act(g) in la_block_norm. */
+typedef enum la_gate_act { LA_GATE_LINEAR = 0, LA_GATE_SIGMOID = 1, LA_GATE_SILU = 2 } la_gate_act;
+
+typedef struct la_block_shape {
+    int64_t M;      /* rows, >= 0 */
+    int64_t D;      /* row length, 1..16384 */
+    int32_t dtype;  /* la_dtype of x, gate, residual, y, h and their gradients */
+    int32_t act;    /* la_gate_act */
+    float eps;      /* > 0, finite */
+    float p;        /* share dropped, 0 <= p <= 1 - 2^-16; taken to the nearest multiple of 2^-16 */
+    int64_t x_stride, gate_stride, residual_stride, y_stride, h_stride;        /* elements between rows; 0 = D */
+    int64_t dy_stride, dh_stride, dx_stride, dgate_stride, dresidual_stride;
+    void* stream;
+    la_trace* trace;
+} la_block_shape;
+
+/*
+ * From one block's output x to the next one's input y, along the residual stream:
+ *        n = x rp w_post,  rp = 1 / sqrt(mean_d x[d]^2 + eps)       (without w_post: n = x)
+ *        u = n act(gate) scale                                      (without gate or scale: those factors are 1)
+ *        h = residual + drop(u)                                     (without residual: drop(u); p = 0: u)
+ *        y = h rq w_pre,   rq = 1 / sqrt(mean_d h[d]^2 + eps)
+ *   x, gate, residual : [M,D] dtype, gate and residual or NULL      w_post, w_pre, scale : float[D] or NULL
+ *   rng               : uint64[2] on the device, 8-byte aligned; not read where T = round(65536 p) = 0
+ *   y                 : [M,D] dtype, required with w_pre and not written without it
+ *   h                 : [M,D] dtype, the stream, rounded (the norm takes the unrounded sum); may be the same pointer,
+ *                       with the same stride, as residual or x
+ *   rstd_post, rstd_pre : float[M] or NULL, rp and rq of every row (only written where there is such a norm).
+ * Both norms hold for any finite row, also where its squares overflow fp32.
+ * No output may otherwise overlap another argument.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
+ */
+la_status la_block_norm(const void* x, const void* gate, const void* residual, const float* w_post, const float* scale,
+                        const float* w_pre, const uint64_t* rng, void* y, void* h, float* rstd_post, float* rstd_pre,
+                        const la_block_shape* shape);
+
+/* Bytes of workspace of la_block_norm_bwd, or a negative la_status. */
+int64_t la_block_norm_bwd_workspace(const la_block_shape* shape);
+
+/*
+ * Backward of la_block_norm from dy [M,D], dh [M,D] (the derivative that reaches h along the residual stream; NULL:
+ * zero), the forward's h, rstd_post and rstd_pre, the same p and the same values behind rng.  dy, h and rstd_pre are
+ * required with w_pre and not read without it; rstd_post goes with w_post likewise.  With hh = h rq and xh = x rp (without w_post: x):
+ *        dresidual = rq (dy w_pre - hh mean_d(dy w_pre hh)) + dh
+ *        du        = dresidual, dropped as u was
+ *        dgate     = du n scale act'(gate),      dn = du act(gate) scale
+ *        dx        = rp (dn w_post - xh mean_d(dn w_post xh))       (without w_post: dn)
+ *        dw_post   = sum_rows dn xh,   dscale = sum_rows du n act(gate),   dw_pre = sum_rows dy hh.
+ * A dropped element adds exactly zero to dgate, dn and the sums.  Writes dx [M,D] dtype; dresidual [M,D] dtype or NULL
+ * (may be the same pointer, with the same stride, as dh or dy); dgate [M,D] dtype, dw_post, dscale and dw_pre float[D],
+ * each required where what it belongs to is given and not written otherwise.  No output may otherwise overlap another
+ * argument.
+ * Returns the codes of la_block_norm, or LA_ERR_WORKSPACE.
+ */
+la_status la_block_norm_bwd(const void* x, const void* gate, const void* h, const float* w_post, const float* scale,
+                            const float* w_pre, const uint64_t* rng, const float* rstd_post, const float* rstd_pre,
+                            const void* dy, const void* dh, void* dx, void* dgate, void* dresidual, float* dw_post,
+                            float* dscale, float* dw_pre, void* workspace, uint64_t workspace_bytes,
+                            const la_block_shape* shape);
+
+/*
+ * y = residual + drop(x), rows of [M,D] (residual NULL: drop(x); the backward pass of drop is la_dropout of dy with the
+ * same p and values behind rng).  y may be the same pointer, with the same stride, as x or residual; it may not
+ * otherwise overlap them.  Takes shape's M, D, dtype, p, x_stride, residual_stride, y_stride, stream and trace; the
+ * row length D may be up to 2^34 here and M up to 2^25, M D up to 2^34.  Where T = 0, y = residual + x.
+ * Returns the codes of la_block_norm.
+ */
+la_status la_dropout(const void* x, const void* residual, const uint64_t* rng, void* y, const la_block_shape* shape);
+
 /* Releases the current device's workspace: when the device holds buffers kept between calls, it
  * waits for the device to be idle and frees them; then it returns the pool's memory that no
  * enqueued call still uses to the device (later calls obtain it again).  Not to be called while
