@@ -8,6 +8,7 @@
 
 #include "la_chunk.h"
 #include "la_internal.h"
+#include "la_mixer.h"
 
 namespace {
 
@@ -193,8 +194,10 @@ const char* la_status_str(int32_t status) {
 int32_t la_supported(const la_shape* s, int32_t chunk) { return check_fwd_shape(s, chunk) == LA_OK ? 1 : 0; }
 
 la_status la_chain_status(int32_t clear, int64_t* give_ups) {
-    unsigned int n = 0;
-    if (la::chain_status(&n, clear != 0) != hipSuccess) return LA_ERR_LAUNCH;
+    unsigned int chained = 0, gated = 0;
+    if (la::chain_status(&chained, clear != 0) != hipSuccess || la::gated_status(&gated, clear != 0) != hipSuccess)
+        return LA_ERR_LAUNCH;
+    const int64_t n = (int64_t)chained + gated;
     if (give_ups) *give_ups = n;
     return n ? LA_ERR_TIMEOUT : LA_OK;
 }

@@ -157,6 +157,8 @@ hipError_t launch_gated_scan(const GatedArgs& a);
 size_t gated_bwd_ws(int64_t B, int64_t L, int64_t D, bool have_blocks);
 hipError_t launch_gated_scan_bwd(const GatedArgs& a);
 hipError_t launch_gated_step(const GatedArgs& a);
+// as chain_status, of the gated recurrence's waits
+hipError_t gated_status(unsigned int* give_ups, bool clear);
 
 struct BlockArgs {
     const void* x;

@@ -729,7 +729,8 @@ la_status la_dropout(const void* x, const void* residual, const uint64_t* rng, v
  * Returns LA_OK or LA_ERR_LAUNCH. */
 la_status la_trim_workspace(void);
 
-/* Give-up counter of the chained forward (fwd_schedule = 2).  Its workgroups wait for each other's
+/* Give-up counter of the chained forward (fwd_schedule = 2) and of the gated recurrence, forward and backward, whose
+ * workgroups take the state that enters their tokens from those before.  They wait for each other's
  * flags; every wait is bounded, and a compute wave that polls a flag la_set_chain_spin_limit's
  * number of times without seeing it set stops waiting, computes on a NaN state (so its outputs are
  * NaN rather than the GPU hanging) and adds one to a per-device counter.  This call synchronises
