@@ -13,6 +13,7 @@
 // is below 1.1e-8 of it for v <= 1/2), and k = a / (2 S).
 #include <algorithm>
 #include <initializer_list>
+#include <type_traits>
 #include <utility>
 
 #include "la_mixer.h"
@@ -47,49 +48,56 @@ struct GatedDev {
     unsigned* ticket;
     uint64_t* map;         // [B, tiles, D]
     uint32_t* state_word;  // [B, tiles, D]
-    int64_t L, D, tiles;   // tiles of a sequence
+    uint32_t* hint;        // [B, cb, tiles]: not all ones when the tile's states are published
+    int64_t L, D, tiles;   // tiles of a sequence, at least 1
+    int64_t blocks_per_seq;
     unsigned cb, per_tile, total;  // channel blocks; tiles at one position; tiles in all
     int nslots, limit;
     float c;
     la_rows sx, sr, si, sz, sy, sdy, sdx, sdr, sdi, sdz;
 };
 
-constexpr int TILE = LA_GATED_BLOCK;
-
-// A channel's parameters: the biases times -log2 e, the largest v.
+// A channel's parameters: the biases times -log2 e, the largest v in base 2 (v log2 e).
 struct Channel {
     float nr, ni, rate;
 };
-__device__ __forceinline__ Channel channel(const GatedDev& p, int64_t d) {
-    return {p.r_bias ? -LOG2E * p.r_bias[d] : 0.f, p.i_bias ? -LOG2E * p.i_bias[d] : 0.f, p.c * softplus(p.lam[d])};
+__device__ __forceinline__ Channel channel(const float* lam, const float* r_bias, const float* i_bias, float c, int64_t d) {
+    return {r_bias ? -LOG2E * r_bias[d] : 0.f, i_bias ? -LOG2E * i_bias[d] : 0.f, c * LOG2E * softplus(lam[d])};
 }
 
-struct Gates {
-    float rho, iota, v, a, mi;  // mi = m iota
-    float s;                    // S, or 1 - a^2 where v > 1/2
-};
-__device__ __forceinline__ float one_minus_a2(float v, float a) {
-    const float v2 = v * v;
-    const float sh = fmaf(v2, fmaf(v2, fmaf(v2, 1.f / 5040.f, 1.f / 120.f), 1.f / 6.f), 1.f);
-    return v <= 0.5f ? sh : fmaf(-a, a, 1.f);
+// With w = v log2 e, a = 2^-w.  1 - a^2 = a w p for w up to SMALL_W (v <= 1/2), where p = 2 ln2 S is a polynomial in w^2;
+// above it 1 - a^2 itself has its digits.  SMALL: every w is small (a channel's rate bounds its w, so a whole wave knows).
+constexpr float SMALL_W = 0.5f * LOG2E;
+constexpr float P0 = 2.f * LN2, P1 = P0 * LN2 * LN2 / 6.f, P2 = P1 * LN2 * LN2 / 20.f, P3 = P2 * LN2 * LN2 / 42.f;
+__device__ __forceinline__ float poly_p(float w) {
+    const float w2 = w * w;
+    return fmaf(w2, fmaf(w2, fmaf(w2, P3, P2), P1), P0);
 }
+struct Gates {
+    float rho, iota, w, a, mi;  // mi = m iota
+};
+template <bool SMALL>
 __device__ __forceinline__ Gates gates(float r, float i, const Channel& c) {
     Gates g;
     g.rho = rcp(1.f + __builtin_amdgcn_exp2f(fmaf(r, -LOG2E, c.nr)));
     g.iota = rcp(1.f + __builtin_amdgcn_exp2f(fmaf(i, -LOG2E, c.ni)));
-    g.v = c.rate * g.rho;
-    g.a = __builtin_amdgcn_exp2f(g.v * -LOG2E);
-    g.s = one_minus_a2(g.v, g.a);
-    g.mi = __builtin_amdgcn_sqrtf(g.v <= 0.5f ? 2.f * g.a * g.v * g.s : g.s) * g.iota;
+    g.w = c.rate * g.rho;
+    g.a = __builtin_amdgcn_exp2f(-g.w);
+    float m2 = g.a * g.w * poly_p(g.w);
+    if (!SMALL) m2 = g.w <= SMALL_W ? m2 : fmaf(-g.a, g.a, 1.f);
+    g.mi = __builtin_amdgcn_sqrtf(m2) * g.iota;
     return g;
 }
-// k = a^2 v / (1 - a^2)
-__device__ __forceinline__ float input_slope(const Gates& g) {
-    return g.v <= 0.5f ? g.a * rcp(2.f * g.s) : g.a * g.a * g.v * rcp(g.s);
+// k / (a ln2) = a v / (m^2 ln2): 1 / p, or a w / (1 - a^2)
+template <bool SMALL>
+__device__ __forceinline__ float input_slope(float w, float a) {
+    const float k = rcp(poly_p(w));
+    if (SMALL) return k;
+    return w <= SMALL_W ? k : a * w * rcp(fmaf(-a, a, 1.f));
 }
 
 // ---------------------------------------------------------------------------------------------
-// The scan over a sequence.  A tile is 64 tokens x 64 VEC channels, a workgroup of 8 waves with 8 tokens each.  A tile's
+// The scan over a sequence.  A tile is 128 tokens x 64 channels (backward 64 x 64), a workgroup's.  A tile's
 // tokens map the state that enters it to the one that leaves it, h -> A h + B; its workgroup publishes (A, B) for the
 // tiles behind it as soon as it has read its inputs, then looks back for the state that enters it (look_back), publishes the
 // one that leaves it, and walks its tokens, whose a and b have stayed in registers.  So every input is read once, a
@@ -107,9 +115,14 @@ __device__ __forceinline__ float input_slope(const Gates& g) {
 // Results do not depend on scheduling: a state is always the left fold h_k+1 = A_k h_k + B_k from the sequence's start,
 // wherever a workgroup finds it done.
 
-constexpr int WAVES = 8, TPT = 8;  // waves a workgroup, tokens a thread
-static_assert(WAVES * TPT == TILE, "a tile is a block");
 constexpr uint32_t EMPTY = ~0u;
+
+// Access size, tokens a lane, waves a workgroup, and the least waves a SIMD of the 2-byte vector form, whose registers fit.
+template <bool BWD> struct Cfg;
+template <> struct Cfg<false> { static constexpr int VEC = 2, TPT = 8, WAVES = 8, OCC = 6; };
+template <> struct Cfg<true> { static constexpr int VEC = 2, TPT = 8, WAVES = 4, OCC = 3; };
+template <bool BWD> constexpr int tokens_of() { return Cfg<BWD>::VEC * Cfg<BWD>::TPT * Cfg<BWD>::WAVES; }
+constexpr int FWD_TOKENS = tokens_of<false>(), BWD_TOKENS = tokens_of<true>();  // tokens of a tile
 
 // VEC adjacent elements of a row in one access.
 template <typename E, int VEC> struct Row;
@@ -140,14 +153,15 @@ template <typename E> struct Row<E, 1> {
     static __device__ __forceinline__ void get(raw r, float* f) { f[0] = (float)r; }
     static __device__ __forceinline__ raw put(const float* f) { return (E)f[0]; }
 };
-// A token's row (uniform address) at a lane's channels: `at` bytes, which fit 32 bits.
+// A token's row (uniform address) at a lane's channels: `at` bytes, which fit 32 bits.  What is written is not read here
+// and leaves by a streaming store: 2 x 4096 x 2048 bf16 forward and backward 168 -> 159 us.
 template <typename E, int VEC>
 __device__ __forceinline__ typename Row<E, VEC>::raw ld(const E* row, uint32_t at) {
     return *(const typename Row<E, VEC>::raw*)((const char*)row + at);
 }
 template <typename E, int VEC>
 __device__ __forceinline__ void st(E* row, uint32_t at, const float* f) {
-    *(typename Row<E, VEC>::raw*)((char*)row + at) = Row<E, VEC>::put(f);
+    __builtin_nontemporal_store(Row<E, VEC>::put(f), (typename Row<E, VEC>::raw*)((char*)row + at));
 }
 
 // Waits that gave up, per device (read and cleared by gated_status).
@@ -155,438 +169,528 @@ __device__ unsigned int gated_give_ups;
 
 // A result as a published word: any NaN as the quiet one, so that none is EMPTY.
 __device__ __forceinline__ uint32_t word(float f) { return f == f ? __float_as_uint(f) : 0x7fc00000u; }
-__device__ __forceinline__ void publish_map(uint64_t* p, float a, float b) {
-    __hip_atomic_store(p, (uint64_t)word(b) << 32 | word(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void publish_state(uint32_t* p, float h) {
-    __hip_atomic_store(p, word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
 template <typename T>
 __device__ __forceinline__ T peek(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// The state that enters tile k > 0 of a lane's channel: back to the nearest tile whose outgoing state is known for all
-// lanes, then forward through the maps of those between.  map, state: tile 0's entries, `pitch` apart.
-constexpr int WINDOW = 8;  // entries loaded together
-__device__ __forceinline__ float look_back(const uint64_t* map, const uint32_t* state, int64_t pitch, int k, int limit) {
+// Where the words of one chain (a sequence's 64 channels) stand: tile 0's, `pitch` words a tile; one hint a tile.
+struct Chain {
+    uint64_t* map;
+    uint32_t* state;
+    uint32_t* hint;
+    int64_t pitch;
+};
+__device__ __forceinline__ void publish_map(const Chain& c, int k, float a, float b, bool on) {
+    if (on) __hip_atomic_store(c.map + k * c.pitch, (uint64_t)word(b) << 32 | word(a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish_state(const Chain& c, int k, float h, bool on) {
+    if (on) __hip_atomic_store(c.state + k * c.pitch, word(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if ((threadIdx.x & 63) == 0) __hip_atomic_store(c.hint + k, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The state that enters tile k > 0 of a lane's channel: the hints of the 64 tiles before (of those before them, if need be)
+// in one access say which is the nearest whose state is on its way; from there forward through the maps of the tiles
+// between.  A word that has not arrived yet, whatever its tile's hint says, is polled for.
+constexpr int WINDOW = 8;  // maps loaded together
+__device__ __forceinline__ float look_back(const Chain& c, int k, int limit) {
+    const int lane = threadIdx.x & 63;
     int polls = 0, from = -1;
-    uint32_t h = 0;
     for (;;) {
-        for (int j = k - 1; j >= 0 && from < 0; j -= WINDOW) {
-            uint32_t v[WINDOW];
-#pragma unroll
-            for (int w = 0; w < WINDOW; w++) v[w] = j >= w ? peek(state + (j - w) * pitch) : EMPTY;
-#pragma unroll
-            for (int w = 0; w < WINDOW; w++)
-                if (from < 0 && __all(v[w] != EMPTY)) {
-                    from = j - w;
-                    h = v[w];
-                }
+        for (int j = k - 1; j >= 0 && from < 0; j -= 64) {
+            const uint64_t known = __ballot(j >= lane && peek(c.hint + max(j - lane, 0)) != EMPTY);
+            if (known) from = j - __builtin_ctzll(known);
         }
-        if (from >= 0) break;
-        if (++polls > limit) break;
+        if (from >= 0 || ++polls > limit) break;
         __builtin_amdgcn_s_sleep(1);
     }
-    float s = __uint_as_float(h);
-    for (int j = from + 1; from >= 0 && j < k; j += WINDOW) {
-        uint64_t m[WINDOW];
+    float s = 0.f;
+    if (from >= 0) {
+        uint32_t h = peek(c.state + from * c.pitch);
+        for (int j = from + 1; j < k; j += WINDOW) {
+            uint64_t m[WINDOW];
 #pragma unroll
-        for (int w = 0; w < WINDOW; w++) m[w] = j + w < k ? peek(map + (j + w) * pitch) : 0;
-#pragma unroll
-        for (int w = 0; w < WINDOW; w++)
-            if (j + w < k) {
-                while (!__all((uint32_t)m[w] != EMPTY) && polls <= limit) {
-                    polls++;
-                    __builtin_amdgcn_s_sleep(1);
-                    m[w] = peek(map + (j + w) * pitch);
-                }
-                s = fmaf(__uint_as_float((uint32_t)m[w]), s, __uint_as_float((uint32_t)(m[w] >> 32)));
+            for (int w = 0; w < WINDOW; w++) m[w] = peek(c.map + min(j + w, k - 1) * c.pitch);
+            if (j == from + 1) {
+                while (!__all(h != EMPTY) && polls++ < limit) h = peek(c.state + from * c.pitch);
+                s = __uint_as_float(h);
             }
+#pragma unroll
+            for (int w = 0; w < WINDOW; w++)
+                if (j + w < k) {
+                    while (!__all((uint32_t)m[w] != EMPTY) && polls++ < limit) {
+                        __builtin_amdgcn_s_sleep(1);
+                        m[w] = peek(c.map + (j + w) * c.pitch);
+                    }
+                    s = fmaf(__uint_as_float((uint32_t)m[w]), s, __uint_as_float((uint32_t)(m[w] >> 32)));
+                }
+        }
+        if (from == k - 1) {
+            while (!__all(h != EMPTY) && polls++ < limit) h = peek(c.state + from * c.pitch);
+            s = __uint_as_float(h);
+        }
     }
     if (polls > limit) {
-        if ((threadIdx.x & 63) == 0) atomicAdd(&gated_give_ups, 1u);
+        if (lane == 0) atomicAdd(&gated_give_ups, 1u);
         return __uint_as_float(0x7fc00000u);
     }
     return s;
 }
 
-// The tile that a workgroup takes next; false when there is none.  A barrier on either side of the shared word's use.
-__device__ __forceinline__ bool take(const GatedDev& p, unsigned turn, unsigned* shared, unsigned* idx) {
-    if (p.tiles > 1) {
-        if (threadIdx.x == 0) *shared = atomicAdd(p.ticket, 1u) + 1u;  // from all ones
-        __syncthreads();
-        *idx = (unsigned)uniform((int)*shared);
-        __syncthreads();
+// The kernel's arguments, read again from memory where they are used: held over the whole tile they would push each other
+// out of the scalar registers.
+typedef const __attribute__((address_space(4))) GatedDev* GatedArgsPtr;
+__device__ __forceinline__ GatedArgsPtr gated_args() {
+    GatedArgsPtr q = (GatedArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(q));
+    return q;
+}
+// Keeps what is computed from these registers behind this place: else both sides of a branch's unpacking of all rows moves
+// up in front of it, and its floats fill the registers.
+template <typename... R>
+__device__ __forceinline__ void here(R&... r) {
+    (([](R& x) { asm volatile("" : "+v"(x)); }(r)), ...);
+}
+// Where a tile lies and what of it exists.  Its width is 64 channels whatever the access size: VEC adjacent channels a
+// lane, so 64 / VEC lanes span a row and a wave holds VEC runs of TPT tokens, one behind the other.  Long narrow tiles
+// keep few of them in flight on one chain, which is what a look-back has to fold.
+struct Place {
+    int64_t b, d0, len;
+    int64_t t0;    // the wave's first token
+    int k, tile, live;
+    int run;       // the lane's run
+    int n;         // tokens of it that exist
+    bool on;       // the lane's channels exist (else it does the tile's first ones' work)
+    bool full;     // all tokens of the wave exist
+    bool any;      // at least one does
+    int64_t d;
+};
+template <int VEC, int WAVES, int TPT>
+__device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool backward) {
+    constexpr int TT = WAVES * VEC * TPT, LANES = 64 / VEC;
+    const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
+    Place q;
+    q.k = (int)(idx / p->per_tile);
+    const unsigned rest = idx - q.k * p->per_tile;
+    q.b = rest / p->cb;
+    q.d0 = (int64_t)(rest % p->cb) * 64;
+    q.len = seq_len(p->lengths, q.b, p->L);
+    q.live = (int)((q.len + TT - 1) / TT);
+    q.tile = backward && q.k < q.live ? q.live - 1 - q.k : q.k;
+    q.t0 = (int64_t)q.tile * TT + wv * (VEC * TPT);
+    q.run = lane / LANES;
+    q.n = (int)max((int64_t)0, min((int64_t)TPT, q.len - (q.t0 + q.run * TPT)));
+    q.full = q.t0 + VEC * TPT <= q.len;
+    q.any = q.t0 < q.len;
+    q.d = q.d0 + lane % LANES * VEC;
+    q.on = q.d < p->D;
+    if (!q.on) q.d = q.d0;
+    return q;
+}
+// The rows of one operand: a uniform address and the lane's 32-bit offset (rows_on sees to the range where VEC > 1).
+// Tokens that do not exist are read as the sequence's last.
+template <typename E, int VEC, int TPT>
+__device__ __forceinline__ void load_rows(const void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q,
+                                          typename Row<E, VEC>::raw (&r)[TPT]) {
+    const int64_t step = s.token;
+    const E* row = (const E*)base + q.b * s.batch + q.t0 * step;
+    const uint32_t at = (uint32_t)q.d * (uint32_t)sizeof(E), pitch = (uint32_t)step * (uint32_t)sizeof(E);
+    if (VEC == 1 || q.full) {
+        const uint32_t own = VEC == 1 ? at : at + (uint32_t)(q.run * TPT) * pitch;
+#pragma unroll
+        for (int j = 0; j < TPT; j++) {
+            r[j] = ld<E, VEC>(row, own);
+            if (q.t0 + j + 1 < q.len) row += step;
+        }
     } else {
-        *idx = blockIdx.x + turn * gridDim.x;
-        __syncthreads();
+        const int last = (int)(q.len - 1 - q.t0);
+#pragma unroll
+        for (int j = 0; j < TPT; j++) r[j] = ld<E, VEC>(row, at + (uint32_t)min(q.run * TPT + j, last) * pitch);
     }
-    return *idx < p.total;
+}
+// An output's rows: the lane's VEC values of its j-th token.
+template <typename E, int VEC, int TPT>
+struct OutRows {
+    E* row;
+    int64_t step;
+    uint32_t own;
+    __device__ __forceinline__ OutRows(void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q) {
+        step = s.token;
+        row = (E*)base + q.b * s.batch + q.t0 * step;
+        own = (uint32_t)q.d * (uint32_t)sizeof(E);
+        if (VEC > 1) own += (uint32_t)(q.run * TPT) * ((uint32_t)step * (uint32_t)sizeof(E));
+    }
+    __device__ __forceinline__ void put(int j, const float* f) const { st<E, VEC>(row + j * step, own, f); }
+};
+
+__device__ __forceinline__ Chain chain_of(GatedArgsPtr p, const Place& q, int64_t d) {
+    const int64_t first = q.b * p->tiles * p->D + d;
+    return {p->map + first, p->state_word + first, p->hint + (q.b * p->cb + q.d0 / 64) * p->tiles, p->D};
 }
 
-template <typename E, int VEC>
-__global__ __launch_bounds__(512) void gated_fwd_kernel(GatedDev p) {
-    constexpr int CW = 64 * VEC;
+// The tile of this workgroup: by ticket, or where sequences have one tile (nobody waits) by its number.
+__device__ __forceinline__ unsigned take(GatedArgsPtr p, unsigned* shared) {
+    if (p->tiles == 1) return blockIdx.y * gridDim.x + blockIdx.x;
+    if (threadIdx.x == 0) *shared = atomicAdd(p->ticket, 1u) + 1u;  // from all ones
+    __syncthreads();
+    return (unsigned)uniform((int)*shared);
+}
+
+template <typename E, int VEC, int WAVES, int TPT>
+__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>::OCC : 4) void gated_fwd_kernel(GatedDev) {
+    constexpr int TT = WAVES * VEC * TPT, RUNS = WAVES * VEC, LANES = 64 / VEC;
+    static_assert(LA_GATED_BLOCK % TPT == 0, "a run lies in one block");
     typedef typename Row<E, VEC>::raw raw;
-    __shared__ float map_a[WAVES][CW], map_b[WAVES][CW];  // map_b: then the states that enter the waves' tokens
+    __shared__ __align__(16) float map_a[RUNS][64], map_b[RUNS][64];  // map_b: then the states that enter the runs
     __shared__ unsigned shared;
-    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-    unsigned idx;
-    for (unsigned turn = 0; take(p, turn, &shared, &idx); turn++) {
-        const int tile = (int)(idx / p.per_tile);
-        const unsigned rest = idx - tile * p.per_tile;
-        const int64_t b = rest / p.cb, d0 = (int64_t)(rest % p.cb) * CW;
-        const int64_t len = seq_len(p.lengths, b, p.L);
-        const int live = (int)((len + TILE - 1) / TILE);  // tiles with tokens
-        if (tile > 0 && tile >= live) continue;
-        const bool on = d0 + lane * VEC < p.D;
-        const int64_t d = on ? d0 + lane * VEC : d0;
-        const uint32_t at = (uint32_t)d * (uint32_t)sizeof(E);  // lanes behind the last channel do the block's first one's work
-        const int64_t t0 = (int64_t)tile * TILE + w * TPT;
-        const int n = (int)max((int64_t)0, min((int64_t)TPT, len - t0));
-        float a[TPT][VEC], bb[TPT][VEC];
-        if (n > 0) {
-            const E* xp = (const E*)p.x + b * p.sx.batch + t0 * p.sx.token;
-            const E* rp = (const E*)p.r + b * p.sr.batch + t0 * p.sr.token;
-            const E* ip = (const E*)p.i + b * p.si.batch + t0 * p.si.token;
-            raw xr[TPT], rr[TPT], ir[TPT];
+    const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
+    GatedArgsPtr p = gated_args();
+    const unsigned idx = take(p, &shared);
+    if (idx >= p->total) return;
+    const Place q = place_of<VEC, WAVES, TPT>(p, idx, false);
+    if (q.k > 0 && q.k >= q.live) return;
+    const bool gated = p->z && p->y;
+    float a[TPT][VEC], bb[TPT][VEC];
+    raw zr[TPT];
+    if (q.any) {
+        raw xr[TPT], rr[TPT], ir[TPT];
+        load_rows<E, VEC, TPT>(p->r, p->sr, q, rr);
+        load_rows<E, VEC, TPT>(p->i, p->si, q, ir);
+        load_rows<E, VEC, TPT>(p->x, p->sx, q, xr);
+        if (gated) load_rows<E, VEC, TPT>(p->z, p->sz, q, zr);
+        Channel c[VEC];
+        bool small = true;
 #pragma unroll
-            for (int j = 0; j < TPT; j++) {
-                const int t = min(j, n - 1);  // behind the end: the last token's, not used
-                rr[j] = ld<E, VEC>(rp + t * p.sr.token, at);
-                ir[j] = ld<E, VEC>(ip + t * p.si.token, at);
-                xr[j] = ld<E, VEC>(xp + t * p.sx.token, at);
-            }
-            Channel c[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; v++) c[v] = channel(p, d + v);
+        for (int v = 0; v < VEC; v++) {
+            c[v] = channel(p->lam, p->r_bias, p->i_bias, p->c, q.d + v);
+            small = small && c[v].rate <= SMALL_W;
+        }
+        auto maps = [&](auto known) {
 #pragma unroll
             for (int j = 0; j < TPT; j++) {
                 float fx[VEC], fr[VEC], fi[VEC];
+                here(xr[j], rr[j], ir[j]);
                 Row<E, VEC>::get(xr[j], fx);
                 Row<E, VEC>::get(rr[j], fr);
                 Row<E, VEC>::get(ir[j], fi);
 #pragma unroll
                 for (int v = 0; v < VEC; v++) {
-                    const Gates g = gates(fr[v], fi[v], c[v]);
-                    a[j][v] = j < n ? g.a : 1.f;
-                    bb[j][v] = j < n ? g.mi * fx[v] : 0.f;
+                    const Gates g = gates<decltype(known)::value>(fr[v], fi[v], c[v]);
+                    a[j][v] = g.a;
+                    bb[j][v] = g.mi * fx[v];
                 }
             }
-        } else {
+        };
+        if (__all(small)) maps(std::true_type());
+        else maps(std::false_type());
+    }
+    if (!q.full) {  // tokens that are not there: a = 1, no input
 #pragma unroll
-            for (int j = 0; j < TPT; j++)
+        for (int j = 0; j < TPT; j++)
 #pragma unroll
-                for (int v = 0; v < VEC; v++) {
-                    a[j][v] = 1.f;
-                    bb[j][v] = 0.f;
-                }
+            for (int v = 0; v < VEC; v++) {
+                a[j][v] = j < q.n ? a[j][v] : 1.f;
+                bb[j][v] = j < q.n ? bb[j][v] : 0.f;
+            }
+    }
+    const int run = wv * VEC + q.run, col = lane % LANES * VEC;
+#pragma unroll
+    for (int v = 0; v < VEC; v++) {
+        float A = a[0][v], B = bb[0][v];
+#pragma unroll
+        for (int j = 1; j < TPT; j++) {
+            A *= a[j][v];
+            B = fmaf(a[j][v], B, bb[j][v]);
         }
-#pragma unroll
-        for (int v = 0; v < VEC; v++) {
-            float A = 1.f, B = 0.f;
-#pragma unroll
-            for (int j = 0; j < TPT; j++) {
-                A *= a[j][v];
-                B = fmaf(a[j][v], B, bb[j][v]);
-            }
-            map_a[w][lane * VEC + v] = A;
-            map_b[w][lane * VEC + v] = B;
-        }
-        __syncthreads();
-        if (threadIdx.x < CW) {  // whole waves: a lane per channel
-            const int ch = threadIdx.x;
-            const bool in = d0 + ch < p.D;
-            const int64_t dc = in ? d0 + ch : d0, first = b * p.tiles * p.D + dc, own = first + tile * p.D;
-            const bool more = tile + 1 < live;
-            float h = 0.f;
-            if (tile > 0) {
-                float A = 1.f, B = 0.f;
-#pragma unroll
-                for (int k = 0; k < WAVES; k++) {
-                    A *= map_a[k][ch];
-                    B = fmaf(map_a[k][ch], B, map_b[k][ch]);
-                }
-                if (more && in) publish_map(p.map + own, A, B);
-                h = look_back(p.map + first, p.state_word + first, p.D, tile, p.limit);
-                if (more && in) publish_state(p.state_word + own, fmaf(A, h, B));
-            } else {
-                if (p.h_in) h = p.h_in[b * p.D + dc];
-                if (more && in) {
-                    float A = 1.f, B = 0.f;
-#pragma unroll
-                    for (int k = 0; k < WAVES; k++) {
-                        A *= map_a[k][ch];
-                        B = fmaf(map_a[k][ch], B, map_b[k][ch]);
-                    }
-                    publish_state(p.state_word + own, fmaf(A, h, B));
-                }
-            }
-            if (p.blocks && in && tile < live) p.blocks[own] = h;
-#pragma unroll
-            for (int k = 0; k < WAVES; k++) {
-                const float next = fmaf(map_a[k][ch], h, map_b[k][ch]);
-                map_b[k][ch] = h;
-                h = next;
-            }
-            if (p.h_out && in && !more) p.h_out[b * p.D + dc] = h;
-        }
-        __syncthreads();
-        if (p.y && n > 0) {
-            float h[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; v++) h[v] = map_b[w][lane * VEC + v];
-            raw zr[TPT];
-            if (p.z) {
-                const E* zp = (const E*)p.z + b * p.sz.batch + t0 * p.sz.token;
-#pragma unroll
-                for (int j = 0; j < TPT; j++) zr[j] = ld<E, VEC>(zp + min(j, n - 1) * p.sz.token, at);
-            }
-            E* yp = (E*)p.y + b * p.sy.batch + t0 * p.sy.token;
-#pragma unroll
-            for (int j = 0; j < TPT; j++) {
-                float o[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; v++) o[v] = h[v] = fmaf(a[j][v], h[v], bb[j][v]);
-                if (p.z) {
-                    float z[VEC];
-                    Row<E, VEC>::get(zr[j], z);
-#pragma unroll
-                    for (int v = 0; v < VEC; v++) o[v] *= z[v] * sigmoid(z[v]);
-                }
-                if (on && j < n) st<E, VEC>(yp + j * p.sy.token, at, o);
+        map_a[run][col + v] = A;
+        map_b[run][col + v] = B;
+    }
+    __syncthreads();
+    p = gated_args();
+    if (wv == 0) {  // a lane per channel
+        const int64_t D = p->D;
+        const bool in = q.d0 + lane < D;
+        const int64_t d = in ? q.d0 + lane : q.d0;
+        const Chain chain = chain_of(p, q, d);
+        const bool more = q.k + 1 < q.live;
+        float h = 0.f, A = 1.f, B = 0.f;
+        if (more) {
+#pragma unroll 4
+            for (int k = 0; k < RUNS; k++) {
+                A *= map_a[k][lane];
+                B = fmaf(map_a[k][lane], B, map_b[k][lane]);
             }
         }
+        if (q.k > 0) {
+            if (more) publish_map(chain, q.k, A, B, in);
+            h = look_back(chain, q.k, p->limit);
+        } else if (p->h_in) {
+            h = p->h_in[q.b * D + d];
+        }
+        if (more) publish_state(chain, q.k, fmaf(A, h, B), in);
+        float* blocks = p->blocks && in ? p->blocks + q.b * p->blocks_per_seq * D + d : nullptr;
+#pragma unroll 4
+        for (int k = 0; k < RUNS; k++) {
+            const int64_t t = (int64_t)q.tile * TT + k * TPT;
+            if (blocks && t % LA_GATED_BLOCK == 0 && t < q.len) blocks[t / LA_GATED_BLOCK * D] = h;
+            const float after = fmaf(map_a[k][lane], h, map_b[k][lane]);
+            map_b[k][lane] = h;
+            h = after;
+        }
+        if (p->h_out && in && !more) p->h_out[q.b * D + d] = h;
+    }
+    if (!p->y) return;
+    __syncthreads();
+    if (!q.any) return;
+    float h[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) h[v] = map_b[run][col + v];
+    p = gated_args();
+    const OutRows<E, VEC, TPT> y(p->y, p->sy, q);
+#pragma unroll
+    for (int j = 0; j < TPT; j++) {
+        float o[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) o[v] = h[v] = fmaf(a[j][v], h[v], bb[j][v]);
+        if (gated) {
+            float z[VEC];
+            Row<E, VEC>::get(zr[j], z);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) o[v] *= z[v] * sigmoid(z[v]);
+        }
+        if (q.on && (q.full || j < q.n)) y.put(j, o);
     }
 }
 
 // Backward.  The same from the sequence's end: the carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the
 // carry that enters it from behind to A c + R.  The states h_{t-1} come from the forward's states at the tiles'
 // starts.  Tiles behind a sequence's end write zeros.
-template <typename E, int VEC>
-__global__ __launch_bounds__(512) void gated_bwd_kernel(GatedDev p) {
-    constexpr int CW = 64 * VEC;
+template <typename E, int VEC, int WAVES, int TPT>
+__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::OCC : 2) void gated_bwd_kernel(GatedDev) {
+    constexpr int TT = WAVES * VEC * TPT, RUNS = WAVES * VEC, LANES = 64 / VEC;
+    static_assert(TT % LA_GATED_BLOCK == 0 && WAVES >= 2, "a tile starts with a block; a wave for each chain");
     typedef typename Row<E, VEC>::raw raw;
-    // the waves' maps of state and carry, then what enters their tokens; then their shares of the parameters' sums
-    __shared__ float map_a[WAVES][CW], map_h[WAVES][CW], map_c[WAVES][CW];
+    // the runs' maps of state and carry, then what enters them; then their shares of the parameters' sums
+    __shared__ __align__(16) float map_a[RUNS][64], map_h[RUNS][64], map_c[RUNS][64];
     __shared__ unsigned shared;
-    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-    unsigned idx;
-    for (unsigned turn = 0; take(p, turn, &shared, &idx); turn++) {
-        const int k = (int)(idx / p.per_tile);  // position from the sequence's end
-        const unsigned rest = idx - k * p.per_tile;
-        const int64_t b = rest / p.cb, d0 = (int64_t)(rest % p.cb) * CW;
-        const int64_t len = seq_len(p.lengths, b, p.L);
-        const int live = (int)((len + TILE - 1) / TILE);
-        const int tile = k < live ? live - 1 - k : k;
-        const bool on = d0 + lane * VEC < p.D;
-        const int64_t d = on ? d0 + lane * VEC : d0;
-        const uint32_t at = (uint32_t)d * (uint32_t)sizeof(E);
-        const int64_t t0 = (int64_t)tile * TILE + w * TPT;
-        const int n = (int)max((int64_t)0, min((int64_t)TPT, len - t0));
-        const int out = (int)max((int64_t)0, min((int64_t)TPT, p.L - t0));  // rows to write
-        float a[TPT][VEC], rho[TPT][VEC], iota[TPT][VEC], mi[TPT][VEC], s[TPT][VEC];
-        raw xr[TPT], zr[TPT], yr[TPT];
+    const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
+    GatedArgsPtr p = gated_args();
+    const unsigned idx = take(p, &shared);
+    if (idx >= p->total) return;
+    const Place q = place_of<VEC, WAVES, TPT>(p, idx, true);
+    const bool gated = p->z != nullptr;
+    float a[TPT][VEC], rho[TPT][VEC], iota[TPT][VEC], mi[TPT][VEC];
+    raw xr[TPT], zr[TPT], yr[TPT];
+    float rate[VEC];
+    bool small = true;
+    const int run = wv * VEC + q.run, col = lane % LANES * VEC;
+    if (q.any) {
+        raw rr[TPT], ir[TPT];
+        load_rows<E, VEC, TPT>(p->r, p->sr, q, rr);
+        load_rows<E, VEC, TPT>(p->i, p->si, q, ir);
+        load_rows<E, VEC, TPT>(p->x, p->sx, q, xr);
+        load_rows<E, VEC, TPT>(p->dy, p->sdy, q, yr);
+        if (gated) load_rows<E, VEC, TPT>(p->z, p->sz, q, zr);
         Channel c[VEC];
-        if (n > 0) {
-            const E* xp = (const E*)p.x + b * p.sx.batch + t0 * p.sx.token;
-            const E* rp = (const E*)p.r + b * p.sr.batch + t0 * p.sr.token;
-            const E* ip = (const E*)p.i + b * p.si.batch + t0 * p.si.token;
-            const E* yp = (const E*)p.dy + b * p.sdy.batch + t0 * p.sdy.token;
-            raw rr[TPT], ir[TPT];
 #pragma unroll
-            for (int j = 0; j < TPT; j++) {
-                const int t = min(j, n - 1);
-                rr[j] = ld<E, VEC>(rp + t * p.sr.token, at);
-                ir[j] = ld<E, VEC>(ip + t * p.si.token, at);
-                xr[j] = ld<E, VEC>(xp + t * p.sx.token, at);
-                yr[j] = ld<E, VEC>(yp + t * p.sdy.token, at);
-            }
-            if (p.z) {
-                const E* zp = (const E*)p.z + b * p.sz.batch + t0 * p.sz.token;
-#pragma unroll
-                for (int j = 0; j < TPT; j++) zr[j] = ld<E, VEC>(zp + min(j, n - 1) * p.sz.token, at);
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; v++) c[v] = channel(p, d + v);
+        for (int v = 0; v < VEC; v++) {
+            c[v] = channel(p->lam, p->r_bias, p->i_bias, p->c, q.d + v);
+            rate[v] = c[v].rate;
+            small = small && c[v].rate <= SMALL_W;
+        }
+        small = __all(small);
+        auto maps = [&](auto known) {
 #pragma unroll
             for (int j = 0; j < TPT; j++) {
                 float fr[VEC], fi[VEC];
+                here(rr[j], ir[j]);
                 Row<E, VEC>::get(rr[j], fr);
                 Row<E, VEC>::get(ir[j], fi);
-                Row<E, VEC>::get(yr[j], s[j]);
-                if (p.z) {
+#pragma unroll
+                for (int v = 0; v < VEC; v++) {
+                    const Gates g = gates<decltype(known)::value>(fr[v], fi[v], c[v]);
+                    a[j][v] = g.a;
+                    rho[j][v] = g.rho;
+                    iota[j][v] = g.iota;
+                    mi[j][v] = g.mi;
+                }
+            }
+        };
+        if (small) maps(std::true_type());
+        else maps(std::false_type());
+    }
+    // s_t: the derivative that reaches h_t from y_t
+    auto reach = [&](int j, float* s) {
+        Row<E, VEC>::get(yr[j], s);
+        if (gated) {
+            float z[VEC];
+            Row<E, VEC>::get(zr[j], z);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) s[v] *= z[v] * sigmoid(z[v]);
+        }
+    };
+    {
+        float A[VEC], B[VEC], R[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            A[v] = 1.f;
+            B[v] = R[v] = 0.f;
+        }
+        if (q.any) {
+#pragma unroll
+            for (int j = 0; j < TPT; j++) {
+                float fx[VEC], s[VEC];
+                here(xr[j], yr[j]);
+                Row<E, VEC>::get(xr[j], fx);
+                reach(j, s);
+#pragma unroll
+                for (int v = 0; v < VEC; v++) {
+                    const bool there = q.full || j < q.n;
+                    a[j][v] = there ? a[j][v] : 1.f;
+                    A[v] *= a[j][v];
+                    R[v] = there ? fmaf(A[v], s[v], R[v]) : R[v];  // sum over t of the decays up to t times s_t
+                    B[v] = there ? fmaf(a[j][v], B[v], mi[j][v] * fx[v]) : B[v];
+                }
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            map_a[run][col + v] = A[v];
+            map_h[run][col + v] = B[v];
+            map_c[run][col + v] = R[v];
+        }
+    }
+    __syncthreads();
+    p = gated_args();
+    if (wv < 2) {  // a lane per channel: the first wave the carry, the second the states
+        const int64_t D = p->D;
+        const bool in = q.d0 + lane < D;
+        const int64_t d = in ? q.d0 + lane : q.d0;
+        if (q.k >= q.live) {
+            if (wv == 0 && q.k == 0 && p->dh_in && in) p->dh_in[q.b * D + d] = p->dh_out ? p->dh_out[q.b * D + d] : 0.f;
+        } else if (wv == 0) {
+            const Chain chain = chain_of(p, q, d);
+            const bool more = q.k + 1 < q.live;
+            float cy = 0.f, A = 1.f, R = 0.f;
+#pragma unroll 4
+            for (int k = RUNS - 1; k >= 0; k--) {
+                A *= map_a[k][lane];
+                R = fmaf(map_a[k][lane], R, map_c[k][lane]);
+            }
+            if (q.k > 0) {
+                if (more) publish_map(chain, q.k, A, R, in);
+                cy = look_back(chain, q.k, p->limit);
+            } else if (p->dh_out) {
+                cy = p->dh_out[q.b * D + d];
+            }
+            if (more) publish_state(chain, q.k, fmaf(A, cy, R), in);
+#pragma unroll 4
+            for (int k = RUNS - 1; k >= 0; k--) {
+                const float after = fmaf(map_a[k][lane], cy, map_c[k][lane]);
+                map_c[k][lane] = cy;
+                cy = after;
+            }
+            if (q.tile == 0 && p->dh_in && in) p->dh_in[q.b * D + d] = cy;
+        } else {
+            float h = 0.f;
+            if (q.tile > 0) h = p->blocks_in[(q.b * p->blocks_per_seq + q.tile * (TT / LA_GATED_BLOCK)) * D + d];
+            else if (p->h_in) h = p->h_in[q.b * D + d];
+#pragma unroll 4
+            for (int k = 0; k < RUNS; k++) {
+                const float after = fmaf(map_a[k][lane], h, map_h[k][lane]);
+                map_h[k][lane] = h;
+                h = after;
+            }
+        }
+    }
+    __syncthreads();
+    p = gated_args();
+    const OutRows<E, VEC, TPT> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
+    if (!q.full && q.on) {  // rows behind the sequence's end
+        const int rows = (int)max((int64_t)0, min((int64_t)TPT, p->L - (q.t0 + q.run * TPT)));
+        float zero[VEC] = {};
+        for (int j = q.n; j < rows; j++) {
+            gx.put(j, zero);
+            gr.put(j, zero);
+            gi.put(j, zero);
+            if (gated) gz.put(j, zero);
+        }
+    }
+    float sq[VEC] = {}, sr[VEC] = {}, si[VEC] = {};
+    if (q.any) {
+        float h[VEC], cy[VEC], before[TPT][VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            h[v] = map_h[run][col + v];
+            cy[v] = map_c[run][col + v];
+        }
+#pragma unroll
+        for (int j = 0; j < TPT; j++) {
+            float fx[VEC];
+            Row<E, VEC>::get(xr[j], fx);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                before[j][v] = h[v];
+                h[v] = fmaf(a[j][v], h[v], mi[j][v] * fx[v]);
+            }
+        }
+        auto grads = [&](auto known) {
+#pragma unroll
+            for (int j = TPT - 1; j >= 0; j--) {
+                if (!q.full && j >= q.n) continue;
+                float fx[VEC], ox[VEC], orr[VEC], oi[VEC], oz[VEC], s[VEC];
+                here(xr[j], yr[j]);
+                if (gated) here(zr[j]);
+#pragma unroll
+                for (int v = 0; v < VEC; v++) here(rho[j][v]);
+                Row<E, VEC>::get(xr[j], fx);
+                Row<E, VEC>::get(yr[j], s);
+                if (gated) {
                     float z[VEC];
                     Row<E, VEC>::get(zr[j], z);
 #pragma unroll
-                    for (int v = 0; v < VEC; v++) s[j][v] *= z[v] * sigmoid(z[v]);
-                }
-#pragma unroll
-                for (int v = 0; v < VEC; v++) {
-                    const Gates g = gates(fr[v], fi[v], c[v]);
-                    a[j][v] = j < n ? g.a : 1.f;
-                    rho[j][v] = g.rho;
-                    iota[j][v] = g.iota;
-                    mi[j][v] = j < n ? g.mi : 0.f;
-                    s[j][v] = j < n ? s[j][v] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                float A = 1.f, B = 0.f, R = 0.f;
-#pragma unroll
-                for (int j = 0; j < TPT; j++) {
-                    float fx[VEC];
-                    Row<E, VEC>::get(xr[j], fx);
-                    A *= a[j][v];
-                    B = fmaf(a[j][v], B, j < n ? mi[j][v] * fx[v] : 0.f);
-                }
-#pragma unroll
-                for (int j = TPT - 1; j >= 0; j--) R = a[j][v] * (s[j][v] + R);
-                map_a[w][lane * VEC + v] = A;
-                map_h[w][lane * VEC + v] = B;
-                map_c[w][lane * VEC + v] = R;
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                map_a[w][lane * VEC + v] = 1.f;
-                map_h[w][lane * VEC + v] = map_c[w][lane * VEC + v] = 0.f;
-            }
-        }
-        __syncthreads();
-        if (threadIdx.x < CW) {
-            const int ch = threadIdx.x;
-            const bool in = d0 + ch < p.D;
-            const int64_t dc = in ? d0 + ch : d0, first = b * p.tiles * p.D + dc, own = first + k * p.D;
-            float cy = 0.f, h = 0.f;
-            if (k < live) {
-                const bool more = k + 1 < live;
-                float A = 1.f, R = 0.f;
-#pragma unroll
-                for (int q = WAVES - 1; q >= 0; q--) {
-                    A *= map_a[q][ch];
-                    R = fmaf(map_a[q][ch], R, map_c[q][ch]);
-                }
-                if (k > 0) {
-                    if (more && in) publish_map(p.map + own, A, R);
-                    cy = look_back(p.map + first, p.state_word + first, p.D, k, p.limit);
-                } else if (p.dh_out) {
-                    cy = p.dh_out[b * p.D + dc];
-                }
-                if (more && in) publish_state(p.state_word + own, fmaf(A, cy, R));
-                if (tile > 0) h = p.blocks_in[first + tile * p.D];
-                else if (p.h_in) h = p.h_in[b * p.D + dc];
-#pragma unroll
-                for (int q = 0; q < WAVES; q++) {
-                    const float next = fmaf(map_a[q][ch], h, map_h[q][ch]);
-                    map_h[q][ch] = h;
-                    h = next;
-                }
-#pragma unroll
-                for (int q = WAVES - 1; q >= 0; q--) {
-                    const float next = fmaf(map_a[q][ch], cy, map_c[q][ch]);
-                    map_c[q][ch] = cy;
-                    cy = next;
-                }
-                if (tile == 0 && p.dh_in && in) p.dh_in[b * p.D + dc] = cy;
-            } else if (k == 0 && p.dh_in && in) {  // no tokens
-                p.dh_in[b * p.D + dc] = p.dh_out ? p.dh_out[b * p.D + dc] : 0.f;
-            }
-        }
-        __syncthreads();
-        float sq[VEC] = {}, sr[VEC] = {}, si[VEC] = {};
-        E* gx = (E*)p.dx + b * p.sdx.batch + t0 * p.sdx.token;
-        E* gr = (E*)p.dr + b * p.sdr.batch + t0 * p.sdr.token;
-        E* gi = (E*)p.di + b * p.sdi.batch + t0 * p.sdi.token;
-        E* gz = (E*)p.dz + b * p.sdz.batch + t0 * p.sdz.token;
-        if (n > 0) {
-            float h[VEC], cy[VEC], before[TPT][VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                h[v] = map_h[w][lane * VEC + v];
-                cy[v] = map_c[w][lane * VEC + v];
-            }
-#pragma unroll
-            for (int j = 0; j < TPT; j++) {
-                float fx[VEC];
-                Row<E, VEC>::get(xr[j], fx);
-#pragma unroll
-                for (int v = 0; v < VEC; v++) {
-                    before[j][v] = h[v];
-                    h[v] = fmaf(a[j][v], h[v], mi[j][v] * fx[v]);
-                }
-            }
-#pragma unroll
-            for (int j = TPT - 1; j >= 0; j--) {
-                float fx[VEC], ox[VEC], orr[VEC], oi[VEC], oz[VEC];
-                Row<E, VEC>::get(xr[j], fx);
-#pragma unroll
-                for (int v = 0; v < VEC; v++) {
-                    const float g = s[j][v] + cy[v];
-                    cy[v] = a[j][v] * g;
-                    Gates t;
-                    t.v = c[v].rate * rho[j][v];
-                    t.a = a[j][v];
-                    t.s = one_minus_a2(t.v, t.a);
-                    const float bt = mi[j][v] * fx[v];
-                    const float q = g * fmaf(input_slope(t), bt, -t.v * t.a * before[j][v]);
-                    ox[v] = g * mi[j][v];
-                    orr[v] = q * (1.f - rho[j][v]);
-                    oi[v] = g * bt * (1.f - iota[j][v]);
-                    if (j < n) {
-                        sq[v] += q;
-                        sr[v] += orr[v];
-                        si[v] += oi[v];
-                    }
-                }
-                if (p.z) {
-                    float z[VEC], fy[VEC];
-                    Row<E, VEC>::get(zr[j], z);
-                    Row<E, VEC>::get(yr[j], fy);
-#pragma unroll
                     for (int v = 0; v < VEC; v++) {
                         const float sg = sigmoid(z[v]);
-                        oz[v] = fy[v] * fmaf(a[j][v], before[j][v], mi[j][v] * fx[v]) * sg * fmaf(z[v], 1.f - sg, 1.f);
+                        oz[v] = s[v] * fmaf(a[j][v], before[j][v], mi[j][v] * fx[v]) * sg * fmaf(z[v], 1.f - sg, 1.f);
+                        s[v] *= z[v] * sg;
                     }
                 }
-                if (on && j < n) {
-                    st<E, VEC>(gx + j * p.sdx.token, at, ox);
-                    st<E, VEC>(gr + j * p.sdr.token, at, orr);
-                    st<E, VEC>(gi + j * p.sdi.token, at, oi);
-                    if (p.z) st<E, VEC>(gz + j * p.sdz.token, at, oz);
+#pragma unroll
+                for (int v = 0; v < VEC; v++) {
+                    const float g = s[v] + cy[v], bt = mi[j][v] * fx[v], w = rate[v] * rho[j][v];
+                    cy[v] = a[j][v] * g;
+                    const float dw = LN2 * cy[v] * fmaf(input_slope<decltype(known)::value>(w, a[j][v]), bt, -w * before[j][v]);
+                    ox[v] = g * mi[j][v];
+                    orr[v] = dw * (1.f - rho[j][v]);
+                    oi[v] = g * bt * (1.f - iota[j][v]);
+                    sq[v] += dw;
+                    sr[v] += orr[v];
+                    si[v] += oi[v];
+                }
+                if (q.on) {
+                    gx.put(j, ox);
+                    gr.put(j, orr);
+                    gi.put(j, oi);
+                    if (gated) gz.put(j, oz);
                 }
             }
-        }
-        if (on) {
-            float zero[VEC] = {};
-            for (int j = n; j < out; j++) {
-                st<E, VEC>(gx + j * p.sdx.token, at, zero);
-                st<E, VEC>(gr + j * p.sdr.token, at, zero);
-                st<E, VEC>(gi + j * p.sdi.token, at, zero);
-                if (p.z) st<E, VEC>(gz + j * p.sdz.token, at, zero);
-            }
-        }
-        __syncthreads();
+        };
+        if (small) grads(std::true_type());
+        else grads(std::false_type());
+    }
+    __syncthreads();
 #pragma unroll
-        for (int v = 0; v < VEC; v++) {
-            map_a[w][lane * VEC + v] = sq[v];
-            map_h[w][lane * VEC + v] = sr[v];
-            map_c[w][lane * VEC + v] = si[v];
-        }
-        __syncthreads();
-        if (p.tiles > 0 && threadIdx.x < CW && d0 + threadIdx.x < p.D) {
-            float* row = p.part + (b * p.tiles + tile) * 3 * p.D + d0 + threadIdx.x;
-            float t[3] = {};
+    for (int v = 0; v < VEC; v++) {
+        map_a[run][col + v] = sq[v];
+        map_h[run][col + v] = sr[v];
+        map_c[run][col + v] = si[v];
+    }
+    __syncthreads();
+    p = gated_args();
+    if (p->L > 0 && wv < 3 && q.d0 + lane < p->D) {  // a sum per wave
+        const float(*m)[64] = wv == 0 ? map_a : wv == 1 ? map_h : map_c;
+        float t = 0.f;
 #pragma unroll
-            for (int q = 0; q < WAVES; q++) {
-                t[0] += map_a[q][threadIdx.x];
-                t[1] += map_h[q][threadIdx.x];
-                t[2] += map_c[q][threadIdx.x];
-            }
-            row[0] = t[0];
-            row[p.D] = t[1];
-            row[2 * p.D] = t[2];
-        }
+        for (int k = 0; k < RUNS; k++) t += m[k][lane];
+        p->part[((q.b * p->tiles + q.tile) * 3 + wv) * p->D + q.d0 + lane] = t;
     }
 }
 
@@ -638,8 +742,8 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
     if (s < 0 || s >= p.nslots) return;
     if (p.slots && earlier_row_has(p.slots, b, s)) return;
     if (d >= p.D) return;
-    const Channel c = channel(p, d);
-    const Gates g = gates((float)((const E*)p.r)[b * p.sr.batch + d], (float)((const E*)p.i)[b * p.si.batch + d], c);
+    const Channel c = channel(p.lam, p.r_bias, p.i_bias, p.c, d);
+    const Gates g = gates<false>((float)((const E*)p.r)[b * p.sr.batch + d], (float)((const E*)p.i)[b * p.si.batch + d], c);
     float* st = p.state + (int64_t)s * p.D + d;
     float h = fmaf(g.a, *st, g.mi * (float)((const E*)p.x)[b * p.sx.batch + d]);
     *st = h;
@@ -650,16 +754,17 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
     io<E>::st((E*)p.y + b * p.sy.batch + d, h);
 }
 
-int64_t tile_count(int64_t L) { return (L + TILE - 1) / TILE; }
+int64_t tile_count(int64_t L, int tokens) { return std::max<int64_t>(1, (L + tokens - 1) / tokens); }
 
 // Workspace: the published words behind the ticket (none for sequences of one tile), then the backward's partial sums
-// and, where they are not given, the states that enter the tiles.
+// and, where they are not given, the states that enter the blocks.
 constexpr int64_t SUM_ROWS = 512;  // rows of partial sums added by one block
 struct Cut {
     unsigned* ticket;
     uint64_t* map;
     uint32_t* state_word;
-    size_t clear;  // bytes of these three
+    uint32_t* hint;
+    size_t clear;  // bytes of these four
     float* part;
     float* part2;  // one row per SUM_ROWS of them, where there are more
     float* blocks;
@@ -668,18 +773,22 @@ struct Cut {
 Cut cut(void* ws, int64_t B, int64_t L, int64_t D, bool bwd, bool have_blocks) {
     WsCut w{(char*)ws};
     Cut c = {};
-    const size_t n = (size_t)(B * tile_count(L) * D);
-    if (tile_count(L) > 1) {
+    const int64_t blocks = tile_count(L, LA_GATED_BLOCK);
+    const size_t n = (size_t)(B * blocks * D);
+    const int64_t tiles = tile_count(L, std::min(FWD_TOKENS, BWD_TOKENS));
+    const size_t words = (size_t)(B * tiles * D);
+    if (tiles > 1) {
         c.ticket = (unsigned*)w.take(1);
-        c.map = (uint64_t*)w.take(2 * n);
-        c.state_word = (uint32_t*)w.take(n);
+        c.map = (uint64_t*)w.take(2 * words);
+        c.state_word = (uint32_t*)w.take(words);
+        c.hint = (uint32_t*)w.take((size_t)(B * ((D + 63) / 64) * tiles));
         c.clear = w.used;
     }
     if (bwd) {
-        const int64_t rows = B * tile_count(L);
-        c.part = w.take(3 * n);
+        const int64_t rows = B * tile_count(L, BWD_TOKENS);
+        c.part = w.take((size_t)(3 * rows * D));
         if (rows > SUM_ROWS) c.part2 = w.take((size_t)((rows + SUM_ROWS - 1) / SUM_ROWS * 3 * D));
-        if (!have_blocks && tile_count(L) > 1) c.blocks = w.take(n);
+        if (!have_blocks && blocks > 1) c.blocks = w.take(n);
     }
     c.bytes = w.used;
     return c;
@@ -690,52 +799,57 @@ GatedDev dev(const GatedArgs& a) {
     p.x = a.x; p.r = a.r; p.i = a.i; p.lam = a.lam; p.r_bias = a.r_bias; p.i_bias = a.i_bias; p.z = a.z; p.h_in = a.h_in;
     p.lengths = a.lengths; p.y = a.y; p.h_out = a.h_out; p.blocks = a.blocks; p.blocks_in = a.blocks_in; p.dy = a.dy;
     p.dh_out = a.dh_out; p.dx = a.dx; p.dr = a.dr; p.di = a.di; p.dz = a.dz; p.dh_in = a.dh_in; p.state = a.state;
-    p.slots = a.slots; p.nslots = a.nslots; p.c = a.c; p.L = a.L; p.D = a.D; p.tiles = tile_count(a.L);
+    p.slots = a.slots; p.nslots = a.nslots; p.c = a.c; p.L = a.L; p.D = a.D; p.blocks_per_seq = tile_count(a.L, LA_GATED_BLOCK);
     p.sx = a.sx; p.sr = a.sr; p.si = a.si; p.sz = a.sz; p.sy = a.sy; p.sdy = a.sdy; p.sdx = a.sdx; p.sdr = a.sdr;
     p.sdi = a.sdi; p.sdz = a.sdz;
     return p;
 }
 
-// Whether all rows of the views start on `bytes`.
-bool rows_on(size_t bytes, size_t es, std::initializer_list<std::pair<const void*, la_rows>> views) {
+// Whether all rows of the views start on `bytes`, `span` tokens apart within 31 bits.
+bool rows_on(size_t bytes, size_t es, int64_t span, std::initializer_list<std::pair<const void*, la_rows>> views) {
     for (const auto& v : views)
-        if (v.first && ((uintptr_t)v.first % bytes || v.second.batch * es % bytes || v.second.token * es % bytes)) return false;
+        if (v.first && ((uintptr_t)v.first % bytes || v.second.batch * es % bytes || v.second.token * es % bytes ||
+                        v.second.token * (int64_t)es * span >= (int64_t)1 << 31))
+            return false;
     return true;
 }
 
-constexpr unsigned MAX_BLOCKS = 1 << 20;
+constexpr unsigned MAX_X = 1 << 20;  // workgroups along x
 
-template <typename E, int VEC, bool BWD>
+template <typename E, bool BWD, int VEC, int TPT>
 void scan_v(const GatedArgs& a, GatedDev p, const Cut& c) {
-    p.cb = (unsigned)((a.D + 64 * VEC - 1) / (64 * VEC));
+    constexpr int WAVES = Cfg<BWD>::WAVES;
+    p.tiles = tile_count(a.L, WAVES * VEC * TPT);
+    p.cb = (unsigned)((a.D + 63) / 64);
     p.per_tile = (unsigned)a.B * p.cb;
-    p.total = p.per_tile * (unsigned)std::max<int64_t>(1, p.tiles);
-    p.ticket = c.ticket; p.map = c.map; p.state_word = c.state_word; p.limit = chain_spin_limit;
-    if (c.clear) {
+    p.total = p.per_tile * (unsigned)p.tiles;
+    p.ticket = c.ticket; p.map = c.map; p.state_word = c.state_word; p.hint = c.hint; p.limit = chain_spin_limit;
+    if (p.tiles > 1) {
         const int64_t n = (int64_t)(c.clear / 16);
         LA_TRACED(a.tr, "gated_clear", gated_clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0,
                                                             a.stream>>>((u32x4*)c.ticket, n));
     }
-    const unsigned blocks = std::min(p.total, MAX_BLOCKS);
+    const dim3 grid(std::min(p.total, MAX_X), (p.total + MAX_X - 1) / MAX_X);
     if constexpr (BWD)
-        LA_TRACED(a.tr, "gated_scan_bwd", gated_bwd_kernel<E, VEC><<<blocks, 512, 0, a.stream>>>(p));
+        LA_TRACED(a.tr, "gated_scan_bwd", gated_bwd_kernel<E, VEC, WAVES, TPT><<<grid, WAVES * 64, 0, a.stream>>>(p));
     else
-        LA_TRACED(a.tr, "gated_scan", gated_fwd_kernel<E, VEC><<<blocks, 512, 0, a.stream>>>(p));
+        LA_TRACED(a.tr, "gated_scan", gated_fwd_kernel<E, VEC, WAVES, TPT><<<grid, WAVES * 64, 0, a.stream>>>(p));
 }
 
 template <typename E>
 void fwd_t(const GatedArgs& a, const GatedDev& p, const Cut& c) {
-    constexpr int VEC = sizeof(E) == 2 ? 4 : 2;
-    if (a.D % VEC == 0 && rows_on(VEC * sizeof(E), sizeof(E), {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz}, {p.y, p.sy}}))
-        scan_v<E, VEC, false>(a, p, c);
+    typedef Cfg<false> C;
+    if (a.D % C::VEC == 0 && rows_on(C::VEC * sizeof(E), sizeof(E), C::VEC * C::TPT,
+                                     {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz}, {p.y, p.sy}}))
+        scan_v<E, false, C::VEC, C::TPT>(a, p, c);
     else
-        scan_v<E, 1, false>(a, p, c);
+        scan_v<E, false, 1, C::VEC * C::TPT>(a, p, c);
 }
 template <typename E>
 hipError_t bwd_t(const GatedArgs& a) {
     GatedDev p = dev(a);
     const Cut c = cut(a.ws, a.B, a.L, a.D, true, a.blocks_in != nullptr);
-    const int64_t rows = a.B * p.tiles;
+    int64_t rows = a.B * tile_count(a.L, BWD_TOKENS);
     p.part = c.part;
     if (c.blocks) {
         GatedDev f = p;
@@ -744,24 +858,26 @@ hipError_t bwd_t(const GatedArgs& a) {
         p.blocks_in = c.blocks;
     }
     if (a.B > 0) {
-        constexpr int VEC = 2;
-        if (a.D % VEC == 0 && rows_on(VEC * sizeof(E), sizeof(E), {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz},
-                                       {p.dy, p.sdy}, {p.dx, p.sdx}, {p.dr, p.sdr}, {p.di, p.sdi}, {p.dz, p.sdz}}))
-            scan_v<E, VEC, true>(a, p, c);
+        typedef Cfg<true> C;
+        if (a.D % C::VEC == 0 && rows_on(C::VEC * sizeof(E), sizeof(E), C::VEC * C::TPT,
+                                         {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz}, {p.dy, p.sdy}, {p.dx, p.sdx},
+                                          {p.dr, p.sdr}, {p.di, p.sdi}, {p.dz, p.sdz}}))
+            scan_v<E, true, C::VEC, C::TPT>(a, p, c);
         else
-            scan_v<E, 1, true>(a, p, c);
+            scan_v<E, true, 1, C::VEC * C::TPT>(a, p, c);
     }
+    const unsigned cb = (unsigned)((a.D + 15) / 16);
     const float* part = c.part;
-    int64_t n = rows;
-    if (n > SUM_ROWS) {
-        const int64_t chunks = (n + SUM_ROWS - 1) / SUM_ROWS;
-        LA_TRACED(a.tr, "gated_sums", gated_sums_kernel<<<dim3((unsigned)((a.D + 15) / 16), (unsigned)chunks), 256, 0, a.stream>>>(
-                                          part, a.D, n, SUM_ROWS, c.part2, nullptr, nullptr, nullptr, nullptr));
+    if (a.L == 0) rows = 0;
+    if (rows > SUM_ROWS) {
+        const int64_t chunks = (rows + SUM_ROWS - 1) / SUM_ROWS;
+        LA_TRACED(a.tr, "gated_sums", gated_sums_kernel<<<dim3(cb, (unsigned)chunks), 256, 0, a.stream>>>(
+                                          part, a.D, rows, SUM_ROWS, c.part2, nullptr, nullptr, nullptr, nullptr));
         part = c.part2;
-        n = chunks;
+        rows = chunks;
     }
-    LA_TRACED(a.tr, "gated_sums", gated_sums_kernel<<<(unsigned)((a.D + 15) / 16), 256, 0, a.stream>>>(
-                                      part, a.D, n, n, nullptr, a.lam, a.dlam, a.dr_bias, a.di_bias));
+    LA_TRACED(a.tr, "gated_sums", gated_sums_kernel<<<cb, 256, 0, a.stream>>>(part, a.D, rows, rows, nullptr, a.lam, a.dlam,
+                                                                              a.dr_bias, a.di_bias));
     return hipGetLastError();
 }
 
