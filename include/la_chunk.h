@@ -578,7 +578,7 @@ la_status la_add_norm_bwd(const void* dy, const void* h, const float* weight, co
  *
  * Workspaces: la_gated_scan and la_gated_scan_bwd 12 bytes per channel and 64 tokens (nothing for sequences of up to
  * 64 tokens), the backward 12 more for its parameters' derivatives and, without h_blocks, 4 more;
- * la_block_norm_bwd 12 D bytes per row, of 512 rows at most.
+ * la_block_norm_bwd 8 D bytes per row, of 768 rows at most.
  *
  * Random numbers.  Dropout's are Philox4x32-10 (Salmon et al., 2011), so that a mask is made again wherever it is
  * needed and never stored.  rng points to two uint64 on the device, read when the kernels run: {seed, offset} (a
