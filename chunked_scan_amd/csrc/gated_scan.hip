@@ -153,15 +153,17 @@ template <typename E> struct Row<E, 1> {
     static __device__ __forceinline__ void get(raw r, float* f) { f[0] = (float)r; }
     static __device__ __forceinline__ raw put(const float* f) { return (E)f[0]; }
 };
-// A token's row (uniform address) at a lane's channels: `at` bytes, which fit 32 bits.  What is written is not read here
-// and leaves by a streaming store: 2 x 4096 x 2048 bf16 forward and backward 168 -> 159 us.
+// A token's row (a uniform address in device memory) at a lane's channels, `at` bytes behind, which fit 32 bits.  What is
+// written is not read here and leaves by a streaming store: 2 x 4096 x 2048 bf16 forward and backward 168 -> 159 us.
+typedef __attribute__((address_space(1))) char* GlobalRow;
+__device__ __forceinline__ GlobalRow global_row(const void* p) { return (GlobalRow)(uintptr_t)p; }
 template <typename E, int VEC>
-__device__ __forceinline__ typename Row<E, VEC>::raw ld(const E* row, uint32_t at) {
-    return *(const typename Row<E, VEC>::raw*)((const char*)row + at);
+__device__ __forceinline__ typename Row<E, VEC>::raw ld(GlobalRow row, uint32_t at) {
+    return *(const __attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
 }
 template <typename E, int VEC>
-__device__ __forceinline__ void st(E* row, uint32_t at, const float* f) {
-    __builtin_nontemporal_store(Row<E, VEC>::put(f), (typename Row<E, VEC>::raw*)((char*)row + at));
+__device__ __forceinline__ void st(GlobalRow row, uint32_t at, const float* f) {
+    __builtin_nontemporal_store(Row<E, VEC>::put(f), (__attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at));
 }
 
 // Waits that gave up, per device (read and cleared by gated_status).
@@ -243,6 +245,31 @@ __device__ __forceinline__ GatedArgsPtr gated_args() {
     asm volatile("" : "+s"(q));
     return q;
 }
+// VEC channels' parameters as they lie in memory.  Their loads go out ahead of the rows' (which they would wait for
+// otherwise: loads return in order) and without a branch: a bias that is not given is read as lam and dropped.
+template <int VEC>
+struct Params {
+    float lam[VEC], r[VEC], i[VEC];
+    bool has_r, has_i;
+    __device__ __forceinline__ Params(GatedArgsPtr p, int d) {
+        has_r = p->r_bias != nullptr;
+        has_i = p->i_bias != nullptr;
+        const GlobalRow l = global_row(p->lam), rb = global_row(has_r ? p->r_bias : p->lam),
+                        ib = global_row(has_i ? p->i_bias : p->lam);
+        const uint32_t at = (uint32_t)d * 4u;
+        typedef const __attribute__((address_space(1))) float* F;
+#pragma unroll
+        for (int v = 0; v < VEC; v++) {
+            lam[v] = ((F)(l + at))[v];
+            r[v] = ((F)(rb + at))[v];
+            i[v] = ((F)(ib + at))[v];
+        }
+    }
+    __device__ __forceinline__ Channel channel(int v, float c) const {
+        return {has_r ? -LOG2E * r[v] : 0.f, has_i ? -LOG2E * i[v] : 0.f, c * LOG2E * softplus(lam[v])};
+    }
+};
+
 // Keeps what is computed from these registers behind this place: else both sides of a branch's unpacking of all rows moves
 // up in front of it, and its floats fill the registers.
 template <typename... R>
@@ -253,15 +280,14 @@ __device__ __forceinline__ void here(R&... r) {
 // lane, so 64 / VEC lanes span a row and a wave holds VEC runs of TPT tokens, one behind the other.  Long narrow tiles
 // keep few of them in flight on one chain, which is what a look-back has to fold.
 struct Place {
-    int64_t b, d0, len;
-    int64_t t0;    // the wave's first token
+    int b, d0, len;   // sequence, first channel, tokens of the sequence (2^25 at most, all of them)
+    int t0;           // the wave's first token
     int k, tile, live;
-    int run;       // the lane's run
-    int n;         // tokens of it that exist
-    bool on;       // the lane's channels exist (else it does the tile's first ones' work)
-    bool full;     // all tokens of the wave exist
-    bool any;      // at least one does
-    int64_t d;
+    int run;          // the lane's run
+    int n;            // tokens of it that exist
+    int d;            // the lane's first channel; the tile's, where that does not exist (`on` false)
+    bool on;
+    bool full, any;   // all tokens of the wave exist; at least one does
 };
 template <int VEC, int WAVES, int TPT>
 __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool backward) {
@@ -270,14 +296,16 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
     Place q;
     q.k = (int)(idx / p->per_tile);
     const unsigned rest = idx - q.k * p->per_tile;
-    q.b = rest / p->cb;
-    q.d0 = (int64_t)(rest % p->cb) * 64;
-    q.len = seq_len(p->lengths, q.b, p->L);
-    q.live = (int)((q.len + TT - 1) / TT);
+    q.b = (int)(rest / p->cb);
+    q.d0 = (int)(rest - q.b * p->cb) * 64;
+    // read through the scalar cache: no launch in flight writes it
+    q.len = p->lengths ? max(0, min(((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p->lengths)[q.b], (int)p->L))
+                       : (int)p->L;
+    q.live = (q.len + TT - 1) / TT;
     q.tile = backward && q.k < q.live ? q.live - 1 - q.k : q.k;
-    q.t0 = (int64_t)q.tile * TT + wv * (VEC * TPT);
-    q.run = lane / LANES;
-    q.n = (int)max((int64_t)0, min((int64_t)TPT, q.len - (q.t0 + q.run * TPT)));
+    q.t0 = q.tile * TT + wv * (VEC * TPT);
+    q.run = VEC == 1 ? 0 : lane / LANES;
+    q.n = max(0, min(TPT, q.len - (q.t0 + q.run * TPT)));
     q.full = q.t0 + VEC * TPT <= q.len;
     q.any = q.t0 < q.len;
     q.d = q.d0 + lane % LANES * VEC;
@@ -287,21 +315,23 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
 }
 // The rows of one operand: a uniform address and the lane's 32-bit offset (rows_on sees to the range where VEC > 1).
 // Tokens that do not exist are read as the sequence's last.
-template <typename E, int VEC, int TPT>
+// FULL: all of the wave's do.
+template <typename E, int VEC, int TPT, bool FULL>
 __device__ __forceinline__ void load_rows(const void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q,
                                           typename Row<E, VEC>::raw (&r)[TPT]) {
-    const int64_t step = s.token;
-    const E* row = (const E*)base + q.b * s.batch + q.t0 * step;
-    const uint32_t at = (uint32_t)q.d * (uint32_t)sizeof(E), pitch = (uint32_t)step * (uint32_t)sizeof(E);
-    if (VEC == 1 || q.full) {
+    const int64_t step = s.token * (int64_t)sizeof(E);
+    GlobalRow row = global_row((const E*)base + q.b * s.batch + q.t0 * s.token);
+    const uint32_t at = (uint32_t)q.d * (uint32_t)sizeof(E), pitch = (uint32_t)step;
+    if (FULL || VEC == 1) {
         const uint32_t own = VEC == 1 ? at : at + (uint32_t)(q.run * TPT) * pitch;
 #pragma unroll
         for (int j = 0; j < TPT; j++) {
             r[j] = ld<E, VEC>(row, own);
-            if (q.t0 + j + 1 < q.len) row += step;
+            if (FULL || q.t0 + j + 1 < q.len) row += step;
+            asm("" : "+s"(row));  // stays a uniform address with a 32-bit offset, not one 64-bit sum a lane and token
         }
     } else {
-        const int last = (int)(q.len - 1 - q.t0);
+        const int last = q.len - 1 - q.t0;
 #pragma unroll
         for (int j = 0; j < TPT; j++) r[j] = ld<E, VEC>(row, at + (uint32_t)min(q.run * TPT + j, last) * pitch);
     }
@@ -309,28 +339,32 @@ __device__ __forceinline__ void load_rows(const void* base, const __attribute__(
 // An output's rows: the lane's VEC values of its j-th token.
 template <typename E, int VEC, int TPT>
 struct OutRows {
-    E* row;
+    GlobalRow row;
     int64_t step;
     uint32_t own;
     __device__ __forceinline__ OutRows(void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q) {
-        step = s.token;
-        row = (E*)base + q.b * s.batch + q.t0 * step;
+        step = s.token * (int64_t)sizeof(E);
+        row = global_row((E*)base + q.b * s.batch + q.t0 * s.token);
         own = (uint32_t)q.d * (uint32_t)sizeof(E);
-        if (VEC > 1) own += (uint32_t)(q.run * TPT) * ((uint32_t)step * (uint32_t)sizeof(E));
+        if (VEC > 1) own += (uint32_t)(q.run * TPT) * (uint32_t)step;
     }
-    __device__ __forceinline__ void put(int j, const float* f) const { st<E, VEC>(row + j * step, own, f); }
+    __device__ __forceinline__ void put(int j, const float* f) const {
+        GlobalRow at = row + j * step;
+        asm("" : "+s"(at));  // as in load_rows
+        st<E, VEC>(at, own, f);
+    }
 };
 
 __device__ __forceinline__ Chain chain_of(GatedArgsPtr p, const Place& q, int64_t d) {
     const int64_t first = q.b * p->tiles * p->D + d;
-    return {p->map + first, p->state_word + first, p->hint + (q.b * p->cb + q.d0 / 64) * p->tiles, p->D};
+    return {p->map + first, p->state_word + first, p->hint + ((int64_t)q.b * p->cb + q.d0 / 64) * p->tiles, p->D};
 }
 
 // The tile of this workgroup: by ticket, or where sequences have one tile (nobody waits) by its number.
 __device__ __forceinline__ unsigned take(GatedArgsPtr p, unsigned* shared) {
     if (p->tiles == 1) return blockIdx.y * gridDim.x + blockIdx.x;
     if (threadIdx.x == 0) *shared = atomicAdd(p->ticket, 1u) + 1u;  // from all ones
-    __syncthreads();
+    lds_barrier();
     return (unsigned)uniform((int)*shared);
 }
 
@@ -351,16 +385,22 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
     float a[TPT][VEC], bb[TPT][VEC];
     raw zr[TPT];
     if (q.any) {
+        const Params<VEC> par(p, q.d);
         raw xr[TPT], rr[TPT], ir[TPT];
-        load_rows<E, VEC, TPT>(p->r, p->sr, q, rr);
-        load_rows<E, VEC, TPT>(p->i, p->si, q, ir);
-        load_rows<E, VEC, TPT>(p->x, p->sx, q, xr);
-        if (gated) load_rows<E, VEC, TPT>(p->z, p->sz, q, zr);
+        auto load = [&](auto full) {
+            constexpr bool F = decltype(full)::value;
+            load_rows<E, VEC, TPT, F>(p->r, p->sr, q, rr);
+            load_rows<E, VEC, TPT, F>(p->i, p->si, q, ir);
+            load_rows<E, VEC, TPT, F>(p->x, p->sx, q, xr);
+            if (gated) load_rows<E, VEC, TPT, F>(p->z, p->sz, q, zr);
+        };
+        if (q.full) load(std::true_type());
+        else load(std::false_type());
         Channel c[VEC];
         bool small = true;
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
-            c[v] = channel(p->lam, p->r_bias, p->i_bias, p->c, q.d + v);
+            c[v] = par.channel(v, p->c);
             small = small && c[v].rate <= SMALL_W;
         }
         auto maps = [&](auto known) {
@@ -403,7 +443,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
         map_a[run][col + v] = A;
         map_b[run][col + v] = B;
     }
-    __syncthreads();
+    lds_barrier();
     p = gated_args();
     if (wv == 0) {  // a lane per channel
         const int64_t D = p->D;
@@ -429,7 +469,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
         float* blocks = p->blocks && in ? p->blocks + q.b * p->blocks_per_seq * D + d : nullptr;
 #pragma unroll 4
         for (int k = 0; k < RUNS; k++) {
-            const int64_t t = (int64_t)q.tile * TT + k * TPT;
+            const int t = q.tile * TT + k * TPT;
             if (blocks && t % LA_GATED_BLOCK == 0 && t < q.len) blocks[t / LA_GATED_BLOCK * D] = h;
             const float after = fmaf(map_a[k][lane], h, map_b[k][lane]);
             map_b[k][lane] = h;
@@ -438,7 +478,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
         if (p->h_out && in && !more) p->h_out[q.b * D + d] = h;
     }
     if (!p->y) return;
-    __syncthreads();
+    lds_barrier();
     if (!q.any) return;
     float h[VEC];
 #pragma unroll
@@ -483,16 +523,22 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
     bool small = true;
     const int run = wv * VEC + q.run, col = lane % LANES * VEC;
     if (q.any) {
+        const Params<VEC> par(p, q.d);
         raw rr[TPT], ir[TPT];
-        load_rows<E, VEC, TPT>(p->r, p->sr, q, rr);
-        load_rows<E, VEC, TPT>(p->i, p->si, q, ir);
-        load_rows<E, VEC, TPT>(p->x, p->sx, q, xr);
-        load_rows<E, VEC, TPT>(p->dy, p->sdy, q, yr);
-        if (gated) load_rows<E, VEC, TPT>(p->z, p->sz, q, zr);
+        auto load = [&](auto full) {
+            constexpr bool F = decltype(full)::value;
+            load_rows<E, VEC, TPT, F>(p->r, p->sr, q, rr);
+            load_rows<E, VEC, TPT, F>(p->i, p->si, q, ir);
+            load_rows<E, VEC, TPT, F>(p->x, p->sx, q, xr);
+            load_rows<E, VEC, TPT, F>(p->dy, p->sdy, q, yr);
+            if (gated) load_rows<E, VEC, TPT, F>(p->z, p->sz, q, zr);
+        };
+        if (q.full) load(std::true_type());
+        else load(std::false_type());
         Channel c[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
-            c[v] = channel(p->lam, p->r_bias, p->i_bias, p->c, q.d + v);
+            c[v] = par.channel(v, p->c);
             rate[v] = c[v].rate;
             small = small && c[v].rate <= SMALL_W;
         }
@@ -558,7 +604,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
             map_c[run][col + v] = R[v];
         }
     }
-    __syncthreads();
+    lds_barrier();
     p = gated_args();
     if (wv < 2) {  // a lane per channel: the first wave the carry, the second the states
         const int64_t D = p->D;
@@ -601,18 +647,19 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
             }
         }
     }
-    __syncthreads();
+    lds_barrier();
     p = gated_args();
     const OutRows<E, VEC, TPT> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
     if (!q.full && q.on) {  // rows behind the sequence's end
-        const int rows = (int)max((int64_t)0, min((int64_t)TPT, p->L - (q.t0 + q.run * TPT)));
-        float zero[VEC] = {};
-        for (int j = q.n; j < rows; j++) {
-            gx.put(j, zero);
-            gr.put(j, zero);
-            gi.put(j, zero);
-            if (gated) gz.put(j, zero);
-        }
+        const int rows = max(0, min(TPT, (int)p->L - (q.t0 + q.run * TPT)));
+        const float zero[VEC] = {};
+        for (int j = 0; j < TPT; j++)
+            if (j >= q.n && j < rows) {
+                gx.put(j, zero);
+                gr.put(j, zero);
+                gi.put(j, zero);
+                if (gated) gz.put(j, zero);
+            }
     }
     float sq[VEC] = {}, sr[VEC] = {}, si[VEC] = {};
     if (q.any) {
@@ -676,14 +723,14 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
         if (small) grads(std::true_type());
         else grads(std::false_type());
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         map_a[run][col + v] = sq[v];
         map_h[run][col + v] = sr[v];
         map_c[run][col + v] = si[v];
     }
-    __syncthreads();
+    lds_barrier();
     p = gated_args();
     if (p->L > 0 && wv < 3 && q.d0 + lane < p->D) {  // a sum per wave
         const float(*m)[64] = wv == 0 ? map_a : wv == 1 ? map_h : map_c;
