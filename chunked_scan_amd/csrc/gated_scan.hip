@@ -246,16 +246,16 @@ __device__ __forceinline__ GatedArgsPtr gated_args() {
     return q;
 }
 // VEC channels' parameters as they lie in memory.  Their loads go out ahead of the rows' (which they would wait for
-// otherwise: loads return in order) and without a branch: a bias that is not given is read as lam and dropped.
+// otherwise: loads return in order) and without a branch: a bias that is not given is read as lam and times zero.
 template <int VEC>
 struct Params {
     float lam[VEC], r[VEC], i[VEC];
-    bool has_r, has_i;
+    float by_r, by_i;
     __device__ __forceinline__ Params(GatedArgsPtr p, int d) {
-        has_r = p->r_bias != nullptr;
-        has_i = p->i_bias != nullptr;
-        const GlobalRow l = global_row(p->lam), rb = global_row(has_r ? p->r_bias : p->lam),
-                        ib = global_row(has_i ? p->i_bias : p->lam);
+        const float *lm = p->lam, *pr = p->r_bias, *pi = p->i_bias;
+        by_r = pr ? -LOG2E : 0.f;
+        by_i = pi ? -LOG2E : 0.f;
+        const GlobalRow l = global_row(lm), rb = global_row(pr ? pr : lm), ib = global_row(pi ? pi : lm);
         const uint32_t at = (uint32_t)d * 4u;
         typedef const __attribute__((address_space(1))) float* F;
 #pragma unroll
@@ -266,7 +266,7 @@ struct Params {
         }
     }
     __device__ __forceinline__ Channel channel(int v, float c) const {
-        return {has_r ? -LOG2E * r[v] : 0.f, has_i ? -LOG2E * i[v] : 0.f, c * LOG2E * softplus(lam[v])};
+        return {by_r * r[v], by_i * i[v], c * LOG2E * softplus(lam[v])};
     }
 };
 
@@ -287,7 +287,8 @@ struct Place {
     int n;            // tokens of it that exist
     int d;            // the lane's first channel; the tile's, where that does not exist (`on` false)
     bool on;
-    bool full, any;   // all tokens of the wave exist; at least one does
+    bool full;        // all of the tile's tokens exist
+    bool any;         // at least one of the wave's does
 };
 template <int VEC, int WAVES, int TPT>
 __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool backward) {
@@ -306,7 +307,7 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
     q.t0 = q.tile * TT + wv * (VEC * TPT);
     q.run = VEC == 1 ? 0 : lane / LANES;
     q.n = max(0, min(TPT, q.len - (q.t0 + q.run * TPT)));
-    q.full = q.t0 + VEC * TPT <= q.len;
+    q.full = (q.tile + 1) * TT <= q.len;
     q.any = q.t0 < q.len;
     q.d = q.d0 + lane % LANES * VEC;
     q.on = q.d < p->D;
@@ -315,7 +316,7 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
 }
 // The rows of one operand: a uniform address and the lane's 32-bit offset (rows_on sees to the range where VEC > 1).
 // Tokens that do not exist are read as the sequence's last.
-// FULL: all of the wave's do.
+// FULL: all of the tile's do.
 template <typename E, int VEC, int TPT, bool FULL>
 __device__ __forceinline__ void load_rows(const void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q,
                                           typename Row<E, VEC>::raw (&r)[TPT]) {
@@ -368,34 +369,23 @@ __device__ __forceinline__ unsigned take(GatedArgsPtr p, unsigned* shared) {
     return (unsigned)uniform((int)*shared);
 }
 
-template <typename E, int VEC, int WAVES, int TPT>
-__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>::OCC : 4) void gated_fwd_kernel(GatedDev) {
+// One tile.  FULL: all of its tokens exist, and nothing asks.  Two copies, not a branch at each load: the compiler joins
+// such branches again, by waiting for one side's loads where the other's go to the same registers.
+template <typename E, int VEC, int WAVES, int TPT, bool FULL>
+__device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (*map_a)[64], float (*map_b)[64]) {
     constexpr int TT = WAVES * VEC * TPT, RUNS = WAVES * VEC, LANES = 64 / VEC;
     static_assert(LA_GATED_BLOCK % TPT == 0, "a run lies in one block");
     typedef typename Row<E, VEC>::raw raw;
-    __shared__ __align__(16) float map_a[RUNS][64], map_b[RUNS][64];  // map_b: then the states that enter the runs
-    __shared__ unsigned shared;
     const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
-    GatedArgsPtr p = gated_args();
-    const unsigned idx = take(p, &shared);
-    if (idx >= p->total) return;
-    const Place q = place_of<VEC, WAVES, TPT>(p, idx, false);
-    if (q.k > 0 && q.k >= q.live) return;
     const bool gated = p->z && p->y;
     float a[TPT][VEC], bb[TPT][VEC];
     raw zr[TPT];
-    if (q.any) {
+    if (FULL || q.any) {
         const Params<VEC> par(p, q.d);
         raw xr[TPT], rr[TPT], ir[TPT];
-        auto load = [&](auto full) {
-            constexpr bool F = decltype(full)::value;
-            load_rows<E, VEC, TPT, F>(p->r, p->sr, q, rr);
-            load_rows<E, VEC, TPT, F>(p->i, p->si, q, ir);
-            load_rows<E, VEC, TPT, F>(p->x, p->sx, q, xr);
-            if (gated) load_rows<E, VEC, TPT, F>(p->z, p->sz, q, zr);
-        };
-        if (q.full) load(std::true_type());
-        else load(std::false_type());
+        load_rows<E, VEC, TPT, FULL>(p->r, p->sr, q, rr);
+        load_rows<E, VEC, TPT, FULL>(p->i, p->si, q, ir);
+        load_rows<E, VEC, TPT, FULL>(p->x, p->sx, q, xr);
         Channel c[VEC];
         bool small = true;
 #pragma unroll
@@ -422,7 +412,8 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
         if (__all(small)) maps(std::true_type());
         else maps(std::false_type());
     }
-    if (!q.full) {  // tokens that are not there: a = 1, no input
+    if (gated && (FULL || q.any)) load_rows<E, VEC, TPT, FULL>(p->z, p->sz, q, zr);
+    if (!FULL) {  // tokens that are not there: a = 1, no input
 #pragma unroll
         for (int j = 0; j < TPT; j++)
 #pragma unroll
@@ -479,7 +470,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
     }
     if (!p->y) return;
     lds_barrier();
-    if (!q.any) return;
+    if (!FULL && !q.any) return;
     float h[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) h[v] = map_b[run][col + v];
@@ -496,45 +487,47 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
 #pragma unroll
             for (int v = 0; v < VEC; v++) o[v] *= z[v] * sigmoid(z[v]);
         }
-        if (q.on && (q.full || j < q.n)) y.put(j, o);
+        if (q.on && (FULL || j < q.n)) y.put(j, o);
     }
+}
+template <typename E, int VEC, int WAVES, int TPT>
+__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>::OCC : 4) void gated_fwd_kernel(GatedDev) {
+    // the runs' maps; map_b then the states that enter them
+    __shared__ __align__(16) float map_a[WAVES * VEC][64], map_b[WAVES * VEC][64];
+    __shared__ unsigned shared;
+    GatedArgsPtr p = gated_args();
+    const unsigned idx = take(p, &shared);
+    if (idx >= p->total) return;
+    const Place q = place_of<VEC, WAVES, TPT>(p, idx, false);
+    if (q.k > 0 && q.k >= q.live) return;
+    if (q.full) fwd_tile<E, VEC, WAVES, TPT, true>(p, q, map_a, map_b);
+    else fwd_tile<E, VEC, WAVES, TPT, false>(p, q, map_a, map_b);
 }
 
 // Backward.  The same from the sequence's end: the carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the
 // carry that enters it from behind to A c + R.  The states h_{t-1} come from the forward's states at the tiles'
 // starts.  Tiles behind a sequence's end write zeros.
-template <typename E, int VEC, int WAVES, int TPT>
-__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::OCC : 2) void gated_bwd_kernel(GatedDev) {
+template <typename E, int VEC, int WAVES, int TPT, bool FULL>
+__device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (*map_a)[64], float (*map_h)[64],
+                                         float (*map_c)[64]) {
     constexpr int TT = WAVES * VEC * TPT, RUNS = WAVES * VEC, LANES = 64 / VEC;
-    static_assert(TT % LA_GATED_BLOCK == 0 && WAVES >= 2, "a tile starts with a block; a wave for each chain");
+    static_assert(TT % LA_GATED_BLOCK == 0 && WAVES >= 3, "a tile starts with a block; a wave for each chain and each sum");
     typedef typename Row<E, VEC>::raw raw;
-    // the runs' maps of state and carry, then what enters them; then their shares of the parameters' sums
-    __shared__ __align__(16) float map_a[RUNS][64], map_h[RUNS][64], map_c[RUNS][64];
-    __shared__ unsigned shared;
     const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
-    GatedArgsPtr p = gated_args();
-    const unsigned idx = take(p, &shared);
-    if (idx >= p->total) return;
-    const Place q = place_of<VEC, WAVES, TPT>(p, idx, true);
     const bool gated = p->z != nullptr;
     float a[TPT][VEC], rho[TPT][VEC], iota[TPT][VEC], mi[TPT][VEC];
     raw xr[TPT], zr[TPT], yr[TPT];
     float rate[VEC];
     bool small = true;
     const int run = wv * VEC + q.run, col = lane % LANES * VEC;
-    if (q.any) {
+    if (FULL || q.any) {
         const Params<VEC> par(p, q.d);
         raw rr[TPT], ir[TPT];
-        auto load = [&](auto full) {
-            constexpr bool F = decltype(full)::value;
-            load_rows<E, VEC, TPT, F>(p->r, p->sr, q, rr);
-            load_rows<E, VEC, TPT, F>(p->i, p->si, q, ir);
-            load_rows<E, VEC, TPT, F>(p->x, p->sx, q, xr);
-            load_rows<E, VEC, TPT, F>(p->dy, p->sdy, q, yr);
-            if (gated) load_rows<E, VEC, TPT, F>(p->z, p->sz, q, zr);
-        };
-        if (q.full) load(std::true_type());
-        else load(std::false_type());
+        load_rows<E, VEC, TPT, FULL>(p->r, p->sr, q, rr);
+        load_rows<E, VEC, TPT, FULL>(p->i, p->si, q, ir);
+        load_rows<E, VEC, TPT, FULL>(p->x, p->sx, q, xr);
+        load_rows<E, VEC, TPT, FULL>(p->dy, p->sdy, q, yr);
+        if (gated) load_rows<E, VEC, TPT, FULL>(p->z, p->sz, q, zr);
         Channel c[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
@@ -580,7 +573,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
             A[v] = 1.f;
             B[v] = R[v] = 0.f;
         }
-        if (q.any) {
+        if (FULL || q.any) {
 #pragma unroll
             for (int j = 0; j < TPT; j++) {
                 float fx[VEC], s[VEC];
@@ -589,7 +582,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
                 reach(j, s);
 #pragma unroll
                 for (int v = 0; v < VEC; v++) {
-                    const bool there = q.full || j < q.n;
+                    const bool there = FULL || j < q.n;
                     a[j][v] = there ? a[j][v] : 1.f;
                     A[v] *= a[j][v];
                     R[v] = there ? fmaf(A[v], s[v], R[v]) : R[v];  // sum over t of the decays up to t times s_t
@@ -610,7 +603,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
         const int64_t D = p->D;
         const bool in = q.d0 + lane < D;
         const int64_t d = in ? q.d0 + lane : q.d0;
-        if (q.k >= q.live) {
+        if (!FULL && q.k >= q.live) {
             if (wv == 0 && q.k == 0 && p->dh_in && in) p->dh_in[q.b * D + d] = p->dh_out ? p->dh_out[q.b * D + d] : 0.f;
         } else if (wv == 0) {
             const Chain chain = chain_of(p, q, d);
@@ -650,7 +643,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
     lds_barrier();
     p = gated_args();
     const OutRows<E, VEC, TPT> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
-    if (!q.full && q.on) {  // rows behind the sequence's end
+    if (!FULL && q.on) {  // rows behind the sequence's end
         const int rows = max(0, min(TPT, (int)p->L - (q.t0 + q.run * TPT)));
         const float zero[VEC] = {};
         for (int j = 0; j < TPT; j++)
@@ -662,7 +655,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
             }
     }
     float sq[VEC] = {}, sr[VEC] = {}, si[VEC] = {};
-    if (q.any) {
+    if (FULL || q.any) {
         float h[VEC], cy[VEC], before[TPT][VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
@@ -682,7 +675,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
         auto grads = [&](auto known) {
 #pragma unroll
             for (int j = TPT - 1; j >= 0; j--) {
-                if (!q.full && j >= q.n) continue;
+                if (!FULL && j >= q.n) continue;
                 float fx[VEC], ox[VEC], orr[VEC], oi[VEC], oz[VEC], s[VEC];
                 here(xr[j], yr[j]);
                 if (gated) here(zr[j]);
@@ -739,6 +732,18 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::
         for (int k = 0; k < RUNS; k++) t += m[k][lane];
         p->part[((q.b * p->tiles + q.tile) * 3 + wv) * p->D + q.d0 + lane] = t;
     }
+}
+template <typename E, int VEC, int WAVES, int TPT>
+__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::OCC : 2) void gated_bwd_kernel(GatedDev) {
+    // the runs' maps of state and carry, then what enters them; then their shares of the parameters' sums
+    __shared__ __align__(16) float map_a[WAVES * VEC][64], map_h[WAVES * VEC][64], map_c[WAVES * VEC][64];
+    __shared__ unsigned shared;
+    GatedArgsPtr p = gated_args();
+    const unsigned idx = take(p, &shared);
+    if (idx >= p->total) return;
+    const Place q = place_of<VEC, WAVES, TPT>(p, idx, true);
+    if (q.full) bwd_tile<E, VEC, WAVES, TPT, true>(p, q, map_a, map_h, map_c);
+    else bwd_tile<E, VEC, WAVES, TPT, false>(p, q, map_a, map_h, map_c);
 }
 
 // All ones: no word is published, the first ticket is 0.
