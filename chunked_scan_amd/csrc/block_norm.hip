@@ -43,6 +43,94 @@ struct BlockDev {
     int64_t sx, sg, sres, sy, sh, sdy, sdh, sdx, sdg, sdres;
 };
 
+// 8 adjacent elements as they lie in memory, of which n exist (VEC: all, on 16 bytes).  Rows that are not 16-byte aligned
+// are accessed in 16 bytes all the same, which the hardware takes at any address; only a row's last elements, fewer
+// than 8, are stored one by one (8000 x 2047 bf16: forward 153 us with all elements one by one, 50 so, aligned 2048 42;
+// backward of 4000 rows 93, 49 and 38).  ONCE: streaming loads.
+template <typename V> struct __attribute__((packed, aligned(2))) Unaligned {
+    V v;
+};
+template <typename V, bool VEC, bool ONCE>
+__device__ __forceinline__ V word_at(const void* p) {
+    if (!VEC) return ((const Unaligned<V>*)p)->v;
+    return load_word<V, ONCE>((const V*)p);
+}
+template <typename E, bool VEC> struct Chunk;
+// `back`: the row has 8 elements at least, so that its last ones can be loaded with those before them and moved into
+// place afterwards: put together from single loads they would be waited for where they are loaded.
+template <bool VEC> struct Chunk<__bf16, VEC> {
+    u32x4 r;
+    template <bool ONCE = false>
+    __device__ __forceinline__ void load(const __bf16* p, int n, bool back) {
+        if (VEC || back) {
+            r = word_at<u32x4, VEC, ONCE>(VEC ? p : p - (8 - n));
+            return;
+        }
+        const uint16_t* e = (const uint16_t*)p;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            r[i] = (2 * i < n ? (uint32_t)e[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)e[2 * i + 1] << 16 : 0u);
+    }
+    __device__ __forceinline__ void get(float* f, int n, bool back) const {
+        u32x4 t = r;
+        if (!VEC && back && n < 8) {
+            const int by = 8 - n;  // elements to drop in front
+            if (by & 4) t = u32x4{t[2], t[3], 0, 0};
+            if (by & 2) t = u32x4{t[1], t[2], t[3], 0};
+            if (by & 1) t = u32x4{t[0] >> 16 | t[1] << 16, t[1] >> 16 | t[2] << 16, t[2] >> 16 | t[3] << 16, t[3] >> 16};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f[2 * i] = bits_lo_bf16(t[i]);
+            f[2 * i + 1] = bits_hi_bf16(t[i]);
+        }
+    }
+};
+template <bool VEC> struct Chunk<float, VEC> {
+    f32x4 a, b;
+    template <bool ONCE = false>
+    __device__ __forceinline__ void load(const float* p, int n, bool) {
+        if (VEC || n == 8) {
+            a = word_at<f32x4, VEC, ONCE>(p);
+            b = word_at<f32x4, VEC, ONCE>(p + 4);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            a[i] = i < n ? p[i] : 0.f;
+            b[i] = 4 + i < n ? p[4 + i] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void get(float* f, int, bool) const {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    }
+};
+template <typename E, bool VEC, bool ONCE = false>
+__device__ __forceinline__ void get8(const E* p, int n, bool back, float* f) {
+    Chunk<E, VEC> c;
+    c.template load<ONCE>(p, n, back);
+    c.get(f, n, back);
+}
+template <typename E, bool VEC>
+__device__ __forceinline__ void put8(E* p, int n, const float* f) {
+    if (VEC) {
+        store8<E, true>(p, 8, f);
+    } else if (n == 8) {
+        if (sizeof(E) == 2) {
+            ((Unaligned<u32x4>*)p)->v = pack8_pairs(f);
+        } else {
+            ((Unaligned<f32x4>*)p)->v = f32x4{f[0], f[1], f[2], f[3]};
+            ((Unaligned<f32x4>*)(p + 4))->v = f32x4{f[4], f[5], f[6], f[7]};
+        }
+    } else {
+        store8<E, false>(p, n, f);
+    }
+}
+
 // Philox4x32-10: ten rounds of two 32 x 32 -> 64 bit products on a 128-bit counter, the key stepped by the Weyl
 // constants (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as easy as 1, 2, 3; 2011).
 __device__ __forceinline__ u32x4 philox(uint64_t lo, uint64_t hi, uint64_t key) {
@@ -93,6 +181,7 @@ template <typename E, int TPR, int VPT, bool VEC, bool DROP>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(BlockDev p) {
     __shared__ float buf[16];
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    const bool back = p.D >= 8;
     const int tid = threadIdx.x % TPR;
     const int64_t m = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
     if (m >= p.M) return;  // whole waves; TPR >= 256: whole blocks
@@ -103,7 +192,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         const int64_t d = (int64_t)(i * TPR + tid) * 8;
         const int n = (int)min((int64_t)8, p.D - d);
         if (n > 0) {
-            load8<E, VEC, true>((const E*)p.x + m * p.sx + d, n, v[i]);
+            get8<E, VEC, true>((const E*)p.x + m * p.sx + d, n, back, v[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] = 0.f;
@@ -126,17 +215,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         if (n <= 0) continue;
         float f[8];
         if (p.w_post) {
-            load8<float, VEC>(p.w_post + d, n, f);
+            get8<float, VEC>(p.w_post + d, n, back, f);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] *= rp * f[j];
         }
         if (p.gate) {
-            load8<E, VEC, true>((const E*)p.gate + m * p.sg + d, n, f);
+            get8<E, VEC, true>((const E*)p.gate + m * p.sg + d, n, back, f);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] *= act(f[j], p.act);
         }
         if (p.scale) {
-            load8<float, VEC>(p.scale + d, n, f);
+            get8<float, VEC>(p.scale + d, n, back, f);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] *= f[j];
         }
@@ -146,14 +235,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
             for (int j = 0; j < 8; j++) v[i][j] = (k >> j) & 1 ? v[i][j] * p.keep_scale : 0.f;
         }
         if (p.residual) {
-            load8<E, VEC, true>((const E*)p.residual + m * p.sres + d, n, f);
+            get8<E, VEC, true>((const E*)p.residual + m * p.sres + d, n, back, f);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] += f[j];
         }
         if (!VEC)
 #pragma unroll
             for (int j = 0; j < 8; j++) v[i][j] = j < n ? v[i][j] : 0.f;
-        store8<E, VEC>((E*)p.h + m * p.sh + d, n, v[i]);
+        put8<E, VEC>((E*)p.h + m * p.sh + d, n, v[i]);
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(v[i][j], v[i][j], ss);
     }
@@ -166,51 +255,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         const int n = (int)min((int64_t)8, p.D - d);
         if (n <= 0) continue;
         float w[8];
-        load8<float, VEC>(p.w_pre + d, n, w);
+        get8<float, VEC>(p.w_pre + d, n, back, w);
 #pragma unroll
         for (int j = 0; j < 8; j++) w[j] *= v[i][j] * rq;
-        store8<E, VEC>((E*)p.y + m * p.sy + d, n, w);
+        put8<E, VEC>((E*)p.y + m * p.sy + d, n, w);
     }
 }
-
-// 8 adjacent elements as they lie in memory, of which n exist (VEC: all).
-template <typename E, bool VEC> struct Chunk;
-template <> struct Chunk<__bf16, true> {
-    u32x4 r;
-    __device__ __forceinline__ void load(const __bf16* p, int) { r = *(const u32x4*)p; }
-    __device__ __forceinline__ void get(float* f) const {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            f[2 * i] = bits_lo_bf16(r[i]);
-            f[2 * i + 1] = bits_hi_bf16(r[i]);
-        }
-    }
-};
-template <> struct Chunk<float, true> {
-    f32x4 a, b;
-    __device__ __forceinline__ void load(const float* p, int) {
-        a = *(const f32x4*)p;
-        b = *((const f32x4*)p + 1);
-    }
-    __device__ __forceinline__ void get(float* f) const {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
-        }
-    }
-};
-template <typename E> struct Chunk<E, false> {
-    E r[8];
-    __device__ __forceinline__ void load(const E* p, int n) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) r[i] = i < n ? p[i] : (E)0.f;
-    }
-    __device__ __forceinline__ void get(float* f) const {
-#pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = (float)r[i];
-    }
-};
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
@@ -244,18 +294,19 @@ __device__ __forceinline__ float rows_total(float v, float (*buf)[16], int& set)
 // Backward.  A block holds ROWS rows at a time and walks the rows grid-stride; each thread keeps its channels' share of the
 // three parameters' sums in registers, the block's rows add theirs up at the end (LDS, one after the other) and write one
 // row of `part`.  All of a row is loaded before its first sum, the next row's (2-byte types, one chunk a thread) before
-// this one's: a block waits for two sums over its rows, and with the loads behind them it left the memory idle
+// this one's where its registers allow: a block waits for two sums over its rows, and with the loads behind them it left the memory idle
 // (8191 x 2048 bf16 with gate and dropout, 268 MB: 95.6 -> 59.6 us a pass, 4.5 TB/s).  Blocks of 4 waves, three of them a
 // CU within 168 registers: at four, whose 128 spill, 68.7 us, and blocks of 8 waves 73.
 constexpr int bwd_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 template <typename E, int TPR, int VPT, bool VEC, bool DROP>
-__global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(BlockDev p) {
+__global__ __launch_bounds__(bwd_threads(TPR), TPR <= 256 || !VEC ? 3 : 4) void block_norm_bwd_kernel(BlockDev p) {
     constexpr int ROWS = bwd_threads(TPR) / TPR;
-    constexpr bool AHEAD = sizeof(E) == 2 && VPT == 1 && VEC;
+    constexpr bool AHEAD = sizeof(E) == 2 && VPT == 1 && (VEC || TPR <= 256);
     typedef Chunk<E, VEC> C;
     __shared__ float buf[2][16];
     __shared__ float acc[ROWS > 1 ? TPR * VPT * 16 : 1];
     const int tid = threadIdx.x % TPR, rw = threadIdx.x / TPR;
+    const bool back = p.D >= 8;
     int set = 0;
     float sum[2][VPT][8], wq[VPT][8], ws[VPT][8];  // ws = w_post scale
 #pragma unroll
@@ -268,11 +319,11 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
             wq[i][j] = ws[i][j] = 1.f;
         }
         if (n > 0) {
-            if (p.w_pre) load8<float, VEC>(p.w_pre + d, n, wq[i]);
-            if (p.w_post) load8<float, VEC>(p.w_post + d, n, ws[i]);
+            if (p.w_pre) get8<float, VEC>(p.w_pre + d, n, back, wq[i]);
+            if (p.w_post) get8<float, VEC>(p.w_post + d, n, back, ws[i]);
             if (p.scale) {
                 float sc[8];
-                load8<float, VEC>(p.scale + d, n, sc);
+                get8<float, VEC>(p.scale + d, n, back, sc);
 #pragma unroll
                 for (int j = 0; j < 8; j++) ws[i][j] *= sc[j];
             }
@@ -294,12 +345,12 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
             const int n = (int)min((int64_t)8, p.D - d);
             if (n <= 0) continue;
             if (p.w_pre) {
-                r.h[i].load((const E*)p.h_in + m * p.sh + d, n);
-                r.dy[i].load((const E*)p.dy + m * p.sdy + d, n);
+                r.h[i].load((const E*)p.h_in + m * p.sh + d, n, back);
+                r.dy[i].load((const E*)p.dy + m * p.sdy + d, n, back);
             }
-            if (p.dh) r.dh[i].load((const E*)p.dh + m * p.sdh + d, n);
-            r.x[i].load((const E*)p.x + m * p.sx + d, n);
-            if (p.gate) r.g[i].load((const E*)p.gate + m * p.sg + d, n);
+            if (p.dh) r.dh[i].load((const E*)p.dh + m * p.sdh + d, n, back);
+            r.x[i].load((const E*)p.x + m * p.sx + d, n, back);
+            if (p.gate) r.g[i].load((const E*)p.gate + m * p.sg + d, n, back);
         }
     };
     const int64_t step = (int64_t)gridDim.x * ROWS;
@@ -314,12 +365,13 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
-            const bool there = live && (int64_t)(i * TPR + tid) * 8 < p.D;
+            const int n = (int)min((int64_t)8, p.D - (int64_t)(i * TPR + tid) * 8);
+            const bool there = live && n > 0;
 #pragma unroll
             for (int j = 0; j < 8; j++) t[i][j] = xh[i][j] = 0.f;
             if (!there || !p.w_pre) continue;
-            cur.h[i].get(xh[i]);
-            cur.dy[i].get(t[i]);
+            cur.h[i].get(xh[i], n, back);
+            cur.dy[i].get(t[i], n, back);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 xh[i][j] *= cur.rq;  // the normed stream
@@ -339,15 +391,15 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
 #pragma unroll
             for (int j = 0; j < 8; j++) t[i][j] = cur.rq * fmaf(-xh[i][j], dot, t[i][j]);
             if (p.dh) {
-                cur.dh[i].get(f);
+                cur.dh[i].get(f, n, back);
 #pragma unroll
                 for (int j = 0; j < 8; j++) t[i][j] += f[j];
             }
-            if (p.dres) store8<E, VEC>((E*)p.dres + m * p.sdres + d, n, t[i]);
+            if (p.dres) put8<E, VEC>((E*)p.dres + m * p.sdres + d, n, t[i]);
             uint32_t k = 0xff;
             if (DROP) k = keep_bits(rng, m * p.chunks + (i * TPR + tid), p.drop);
-            cur.x[i].get(xh[i]);
-            if (p.gate) cur.g[i].get(g);
+            cur.x[i].get(xh[i], n, back);
+            if (p.gate) cur.g[i].get(g, n, back);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const bool kept = !DROP || ((k >> j) & 1);
@@ -360,7 +412,7 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
                 t[i][j] = kept ? du * a * ws[i][j] : 0.f;
                 dot2 = fmaf(t[i][j], xh[i][j], dot2);
             }
-            if (p.dgate) store8<E, VEC>((E*)p.dgate + m * p.sdg + d, n, o);
+            if (p.dgate) put8<E, VEC>((E*)p.dgate + m * p.sdg + d, n, o);
         }
         dot2 = p.w_post ? rows_total<TPR>(dot2, buf, set) * p.inv_d : 0.f;
 #pragma unroll
@@ -371,7 +423,7 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
             float o[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) o[j] = p.w_post ? cur.rp * fmaf(-xh[i][j], dot2, t[i][j]) : t[i][j];
-            store8<E, VEC>((E*)p.dx + m * p.sdx + d, n, o);
+            put8<E, VEC>((E*)p.dx + m * p.sdx + d, n, o);
         }
         if (AHEAD) cur = next;
         else load(cur, m + step);
@@ -399,7 +451,7 @@ __global__ __launch_bounds__(bwd_threads(TPR), 3) void block_norm_bwd_kernel(Blo
         for (int i = 0; i < VPT; i++) {
             const int64_t d = (int64_t)(i * TPR + tid) * 8;
             const int n = (int)min((int64_t)8, p.D - d);
-            if (n > 0) store8<float, VEC>(p.part + ((int64_t)blockIdx.x * 2 + q) * p.D + d, n, sum[q][i]);
+            if (n > 0) put8<float, VEC>(p.part + ((int64_t)blockIdx.x * 2 + q) * p.D + d, n, sum[q][i]);
         }
 }
 
@@ -434,28 +486,30 @@ template <typename E, bool VEC, bool DROP>
 __global__ __launch_bounds__(256) void dropout_kernel(BlockDev p) {
     Rng rng = {};
     if (DROP) rng = load_rng(p.rng);
+    const bool back = p.D >= 8;
     const int64_t total = p.M * p.chunks;
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
         const int64_t m = q / p.chunks, d = (q - m * p.chunks) * 8;
         const int n = (int)min((int64_t)8, p.D - d);
         float v[8], f[8];
-        load8<E, VEC, true>((const E*)p.x + m * p.sx + d, n, v);
+        get8<E, VEC, true>((const E*)p.x + m * p.sx + d, n, back, v);
         if (DROP) {
             const uint32_t k = keep_bits(rng, q, p.drop);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[j] = (k >> j) & 1 ? v[j] * p.keep_scale : 0.f;
         }
         if (p.residual) {
-            load8<E, VEC, true>((const E*)p.residual + m * p.sres + d, n, f);
+            get8<E, VEC, true>((const E*)p.residual + m * p.sres + d, n, back, f);
 #pragma unroll
             for (int j = 0; j < 8; j++) v[j] += f[j];
         }
-        store8<E, VEC>((E*)p.y + m * p.sy + d, n, v);
+        put8<E, VEC>((E*)p.y + m * p.sy + d, n, v);
     }
 }
 
-constexpr int BWD_BLOCKS = 768;  // three a CU, as many as their registers allow
-int64_t bwd_rows(int64_t M) { return std::min<int64_t>(BWD_BLOCKS, M); }
+// Blocks of the backward, so rows of partial sums: as many as 256 CUs hold at once (their registers allow three blocks of
+// 4 waves a CU, two of 8, one of 16).
+int64_t bwd_rows(int64_t M, int64_t D) { return std::min<int64_t>(D <= 2048 ? 768 : D <= 4096 ? 512 : 256, M); }
 
 BlockDev dev(const BlockArgs& a) {
     BlockDev p = {};
@@ -487,7 +541,7 @@ void fwd_k(const BlockArgs& a, const BlockDev& p) {
 template <typename E, int TPR, int VPT, bool VEC, bool DROP>
 void bwd_k(const BlockArgs& a, const BlockDev& p) {
     constexpr int TH = bwd_threads(TPR), ROWS = TH / TPR;
-    const int64_t blocks = std::min<int64_t>(bwd_rows(a.M), (a.M + ROWS - 1) / ROWS);
+    const int64_t blocks = std::min<int64_t>(bwd_rows(a.M, a.D), (a.M + ROWS - 1) / ROWS);
     if (blocks > 0)
         LA_TRACED(a.tr, "block_norm_bwd",
                   block_norm_bwd_kernel<E, TPR, VPT, VEC, DROP><<<(unsigned)blocks, TH, 0, a.stream>>>(p));
@@ -534,7 +588,7 @@ void dropout_v(const BlockArgs& a, const BlockDev& p) {
 
 }  // namespace
 
-size_t block_norm_bwd_ws(int64_t M, int64_t D) { return (size_t)(bwd_rows(M) * 2 * D) * sizeof(float); }
+size_t block_norm_bwd_ws(int64_t M, int64_t D) { return (size_t)(bwd_rows(M, D) * 2 * D) * sizeof(float); }
 
 hipError_t launch_block_norm(const BlockArgs& a) {
     if (a.M == 0) return hipSuccess;

@@ -829,7 +829,7 @@ Cut cut(void* ws, int64_t B, int64_t L, int64_t D, bool bwd, bool have_blocks) {
     const size_t n = (size_t)(B * blocks * D);
     const int64_t tiles = tile_count(L, std::min(FWD_TOKENS, BWD_TOKENS));
     const size_t words = (size_t)(B * tiles * D);
-    if (tiles > 1) {
+    if (tiles > 1 && words > 0) {
         c.ticket = (unsigned*)w.take(1);
         c.map = (uint64_t*)w.take(2 * words);
         c.state_word = (uint32_t*)w.take(words);

@@ -387,7 +387,7 @@ def gated_prompt(p: GatedParams, n: torch.Tensor, residual: Optional[torch.Tenso
     r, i = project_gates(v)
     o, h_out, blocks = la_gated_scan(v, r, i, p.lam, z=z, h_in=h_in, lengths=lengths, y=blank(),
                                      want_blocks=saved is not None, **p.scan())
-    x, gate = project_out(o.view(B * L, -1))
+    x, gate = project_out(o.view(B * L, u.shape[2]))
     y, h, rstd_post, rstd_pre = la_block_norm(x, _blank_rows(rows(residual), pad), gate=gate, p=p.dropout, rng=rng,
                                               eps=p.eps, **p.norms())
     if saved is not None:
