@@ -443,12 +443,10 @@ __device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (
         const Chain chain = chain_of(p, q, d);
         const bool more = q.k + 1 < q.live;
         float h = 0.f, A = 1.f, B = 0.f;
-        if (more) {
 #pragma unroll 4
-            for (int k = 0; k < RUNS; k++) {
-                A *= map_a[k][lane];
-                B = fmaf(map_a[k][lane], B, map_b[k][lane]);
-            }
+        for (int k = 0; k < RUNS; k++) {
+            A *= map_a[k][lane];
+            B = fmaf(map_a[k][lane], B, map_b[k][lane]);
         }
         if (q.k > 0) {
             if (more) publish_map(chain, q.k, A, B, in);
@@ -456,7 +454,11 @@ __device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (
         } else if (p->h_in) {
             h = p->h_in[q.b * D + d];
         }
-        if (more) publish_state(chain, q.k, fmaf(A, h, B), in);
+        // the state that leaves is the same sum whether it goes to the next tile or to the caller, so that a sequence in
+        // pieces of whole tiles gives the bits that it gives in one
+        const float leaves = fmaf(A, h, B);
+        if (more) publish_state(chain, q.k, leaves, in);
+        else if (p->h_out && in) p->h_out[q.b * D + d] = leaves;
         float* blocks = p->blocks && in ? p->blocks + q.b * p->blocks_per_seq * D + d : nullptr;
 #pragma unroll 4
         for (int k = 0; k < RUNS; k++) {
@@ -466,7 +468,6 @@ __device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (
             map_b[k][lane] = h;
             h = after;
         }
-        if (p->h_out && in && !more) p->h_out[q.b * D + d] = h;
     }
     if (!p->y) return;
     lds_barrier();

@@ -7,7 +7,7 @@ bounds of the elementary steps, from the hardware's exponential, reciprocal and 
   sigma(r + b): two products and a sum in the exponent move it by 2 (|r| + |b|) U, then the exponential, a sum and
     a reciprocal: 2 (|r| + |b|) + 6;
   softplus: its polynomial's 1.3e-7 (3 U), the ulps of the exponential and of the reciprocal and a product: 10;
-  v = c softplus rho: both and two products;   a = e^-v: v times (v's bound + 2), plus 2;
+  v = c softplus rho: both and two products;   a = e^-v: v times (v's bound + 2), plus 2, and 2^-126 absolutely;
   1 - a^2 = 2 a v S: a's and v's and 8;   or directly (v > 1/2): 2 a^2 (a's bound + 1) / (1 - a^2) + 1;   its root: half and 3.
 A state is carried by a product and a sum per token, and in segments by one product more: 4 U per token of H, the
 recurrence of the terms' absolute values.
@@ -46,7 +46,8 @@ class Gates:
         self.v = c * softplus(lam) * self.rho
         self.k_v = self.k_rho + 12
         self.a = np.exp(-self.v)
-        self.k_a = self.v * (self.k_v + 2) + 2
+        # an exponential below fp32's normal range is flushed to zero: 2^-126 absolutely, whatever a is
+        self.k_a = self.v * (self.k_v + 2) + 2 + 2.0 ** -126 / U / np.maximum(self.a, 1e-250)
         m2 = -np.expm1(-2 * self.v)
         self.m = np.sqrt(m2)
         safe = np.where(m2 > 0, m2, 1)

@@ -267,7 +267,7 @@ def test_waits_that_give_up():
     for t, t0 in zip([y, h, *grads[:3]], [y0, h0, *grads0[:3]]):
         assert ((t == t0) | torch.isnan(t0)).all()
         lost = lost or bool(torch.isnan(t0).any())
-    if lost:  # 32 or 63 tiles of one sequence in flight at once: some wait, on every run so far
+    if lost:
         with pytest.raises(la.LaError, match="LA_ERR_TIMEOUT"):
             la.la_chain_status()
     assert la.la_chain_status() == 0
@@ -292,14 +292,15 @@ def test_strong_and_dead_decay():
     for t in got:
         assert torch.isfinite(t).all()
     want = G.scan_bwd(*ref, nonan(a["dy"]), R.f64(a["dh_out"]))
-    # where the step underflows fp32 (v < 2^-120 or so) its root has a relative error of its own: those channels' x and i
-    # derivatives are below 1e-17 and compared as such
+    # lam <= -80: v = 8 softplus(lam) rho < 8 e^-80 = 1.5e-34 and subnormal below -87, where the hardware takes it for zero.  The
+    # input's factor is sqrt(2 v) < 1.8e-17 there, and so are, times a few, the derivatives of x, r and i and the sums of 200
+    # tokens at most: compared with 1e-17 and 1e-15
     live = (a["lam"] > -80).cpu().numpy()
     for name, t, r in zip(GRADS, got, want):
         v, e = r
         if t.dim() == 3:
             e = e + 1e-17 / R.U * ~live
-        if name == "dlam":
+        if t.dim() == 1:
             assert np.abs(R.f64(t)[~live]).max() <= 1e-15
             G.close(t[torch.from_numpy(live).cuda()], v[live], e[live], F32, name)
         else:
