@@ -787,24 +787,38 @@ __global__ __launch_bounds__(256) void gated_sums_kernel(const float* __restrict
     if (di_bias) di_bias[d] = s[2];
 }
 
-// A row per wave and 64 channels.
-template <typename E>
+// One token: a row per wave and 64 VEC channels, all of its loads in flight before the first is used.
+template <typename E, int VEC>
 __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
-    const int64_t b = blockIdx.x / p.cb, d = (int64_t)(blockIdx.x % p.cb) * 64 + threadIdx.x;
+    const int64_t b = blockIdx.x / p.cb, d = ((int64_t)(blockIdx.x % p.cb) * 64 + threadIdx.x) * VEC;
     const int s = p.slots ? p.slots[b] : (int)b;
     if (s < 0 || s >= p.nslots) return;
     if (p.slots && earlier_row_has(p.slots, b, s)) return;
     if (d >= p.D) return;
-    const Channel c = channel(p.lam, p.r_bias, p.i_bias, p.c, d);
-    const Gates g = gates<false>((float)((const E*)p.r)[b * p.sr.batch + d], (float)((const E*)p.i)[b * p.si.batch + d], c);
-    float* st = p.state + (int64_t)s * p.D + d;
-    float h = fmaf(g.a, *st, g.mi * (float)((const E*)p.x)[b * p.sx.batch + d]);
-    *st = h;
-    if (p.z) {
-        const float z = (float)((const E*)p.z)[b * p.sz.batch + d];
-        h *= z * sigmoid(z);
+    const uint32_t at = (uint32_t)d * (uint32_t)sizeof(E);
+    auto row = [&](const void* q, const la_rows& st) { return global_row((const E*)q + b * st.batch); };
+    const auto rr = ld<E, VEC>(row(p.r, p.sr), at), ri = ld<E, VEC>(row(p.i, p.si), at), rx = ld<E, VEC>(row(p.x, p.sx), at);
+    typename Row<E, VEC>::raw rz = {};
+    if (p.z) rz = ld<E, VEC>(row(p.z, p.sz), at);
+    float* hp = p.state + (int64_t)s * p.D + d;
+    const auto rh = *(const typename Row<float, VEC>::raw*)hp;
+    Channel c[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; v++) c[v] = channel(p.lam, p.r_bias, p.i_bias, p.c, d + v);
+    float fr[VEC], fi[VEC], x[VEC], z[VEC], h[VEC], y[VEC];
+    Row<E, VEC>::get(rr, fr);
+    Row<E, VEC>::get(ri, fi);
+    Row<E, VEC>::get(rx, x);
+    Row<E, VEC>::get(rz, z);
+    Row<float, VEC>::get(rh, h);
+#pragma unroll
+    for (int v = 0; v < VEC; v++) {
+        const Gates g = gates<false>(fr[v], fi[v], c[v]);
+        y[v] = h[v] = fmaf(g.a, h[v], g.mi * x[v]);
+        if (p.z) y[v] *= z[v] * sigmoid(z[v]);
     }
-    io<E>::st((E*)p.y + b * p.sy.batch + d, h);
+    *(typename Row<float, VEC>::raw*)hp = Row<float, VEC>::put(h);
+    st<E, VEC>(row(p.y, p.sy), at, y);
 }
 
 int64_t tile_count(int64_t L, int tokens) { return std::max<int64_t>(1, (L + tokens - 1) / tokens); }
@@ -934,6 +948,22 @@ hipError_t bwd_t(const GatedArgs& a) {
     return hipGetLastError();
 }
 
+template <typename E, int VEC>
+void step_v(const GatedArgs& a) {
+    GatedDev p = dev(a);
+    p.cb = (unsigned)((a.D + 64 * VEC - 1) / (64 * VEC));
+    LA_TRACED(a.tr, "gated_step", gated_step_kernel<E, VEC><<<(unsigned)(a.B * p.cb), 64, 0, a.stream>>>(p));
+}
+// Four channels a lane where that leaves two waves a CU (256 x 4096 bf16 in a graph 6.8 us, one a lane 7.3; the floor of its
+// 19 MB is 3.7), else one: a few rows are a matter of latency (1 x 2048 2.4 us), which more waves hide.
+template <typename E>
+hipError_t step_t(const GatedArgs& a) {
+    const bool vec = a.D % 4 == 0 && a.B * ((a.D + 255) / 256) >= 512 && (uintptr_t)a.state % 16 == 0 &&
+                     rows_on(4 * sizeof(E), sizeof(E), 0, {{a.x, a.sx}, {a.r, a.sr}, {a.i, a.si}, {a.z, a.sz}, {a.y, a.sy}});
+    vec ? step_v<E, 4>(a) : step_v<E, 1>(a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t gated_fwd_ws(int64_t B, int64_t L, int64_t D) { return cut(nullptr, B, L, D, false, false).bytes; }
@@ -960,14 +990,7 @@ hipError_t launch_gated_scan_bwd(const GatedArgs& a) {
 }
 hipError_t launch_gated_step(const GatedArgs& a) {
     if (a.B == 0 || a.D == 0) return hipSuccess;
-    GatedDev p = dev(a);
-    p.cb = (unsigned)((a.D + 63) / 64);
-    const unsigned blocks = (unsigned)(a.B * p.cb);
-    if (a.bf16)
-        LA_TRACED(a.tr, "gated_step", gated_step_kernel<__bf16><<<blocks, 64, 0, a.stream>>>(p));
-    else
-        LA_TRACED(a.tr, "gated_step", gated_step_kernel<float><<<blocks, 64, 0, a.stream>>>(p));
-    return hipGetLastError();
+    return a.bf16 ? step_t<__bf16>(a) : step_t<float>(a);
 }
 
 }  // namespace la
