@@ -823,15 +823,30 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
 
 int64_t tile_count(int64_t L, int tokens) { return std::max<int64_t>(1, (L + tokens - 1) / tokens); }
 
-// Workspace: the published words behind the ticket (none for sequences of one tile), then the backward's partial sums
-// and, where they are not given, the states that enter the blocks.
-constexpr int64_t SUM_ROWS = 512;  // rows of partial sums added by one block
-struct Cut {
+// The words that the workgroups of one launch publish, behind the ticket (none for sequences of one tile).
+struct Words {
     unsigned* ticket;
     uint64_t* map;
-    uint32_t* state_word;
+    uint32_t* state;
     uint32_t* hint;
-    size_t clear;  // bytes of these four
+    size_t bytes;
+};
+Words words_of(void* ws, int64_t B, int64_t tiles, int64_t D) {
+    WsCut w{(char*)ws};
+    Words c = {};
+    const size_t n = (size_t)(B * tiles * D);
+    if (tiles > 1 && n > 0) {
+        c.ticket = (unsigned*)w.take(1);
+        c.map = (uint64_t*)w.take(2 * n);
+        c.state = (uint32_t*)w.take(n);
+        c.hint = (uint32_t*)w.take((size_t)(B * ((D + 63) / 64) * tiles));
+    }
+    c.bytes = w.used;
+    return c;
+}
+// Workspace: the words, then the backward's partial sums and, where they are not given, the states that enter the blocks.
+constexpr int64_t SUM_ROWS = 512;  // rows of partial sums added by one block
+struct Cut {
     float* part;
     float* part2;  // one row per SUM_ROWS of them, where there are more
     float* blocks;
@@ -840,22 +855,15 @@ struct Cut {
 Cut cut(void* ws, int64_t B, int64_t L, int64_t D, bool bwd, bool have_blocks) {
     WsCut w{(char*)ws};
     Cut c = {};
-    const int64_t blocks = tile_count(L, LA_GATED_BLOCK);
-    const size_t n = (size_t)(B * blocks * D);
-    const int64_t tiles = tile_count(L, std::min(FWD_TOKENS, BWD_TOKENS));
-    const size_t words = (size_t)(B * tiles * D);
-    if (tiles > 1 && words > 0) {
-        c.ticket = (unsigned*)w.take(1);
-        c.map = (uint64_t*)w.take(2 * words);
-        c.state_word = (uint32_t*)w.take(words);
-        c.hint = (uint32_t*)w.take((size_t)(B * ((D + 63) / 64) * tiles));
-        c.clear = w.used;
-    }
+    const int64_t blocks = tile_count(L, LA_GATED_BLOCK), tiles = tile_count(L, BWD_TOKENS);
+    const bool fwd = !bwd || (!have_blocks && blocks > 1);
+    w.used = std::max(fwd ? words_of(nullptr, B, tile_count(L, FWD_TOKENS), D).bytes : 0,
+                      bwd ? words_of(nullptr, B, tiles, D).bytes : 0);
     if (bwd) {
-        const int64_t rows = B * tile_count(L, BWD_TOKENS);
+        const int64_t rows = B * tiles;
         c.part = w.take((size_t)(3 * rows * D));
         if (rows > SUM_ROWS) c.part2 = w.take((size_t)((rows + SUM_ROWS - 1) / SUM_ROWS * 3 * D));
-        if (!have_blocks && blocks > 1) c.blocks = w.take(n);
+        if (fwd) c.blocks = w.take((size_t)(B * blocks * D));
     }
     c.bytes = w.used;
     return c;
@@ -884,17 +892,18 @@ bool rows_on(size_t bytes, size_t es, int64_t span, std::initializer_list<std::p
 constexpr unsigned MAX_X = 1 << 20;  // workgroups along x
 
 template <typename E, bool BWD, int VEC, int TPT>
-void scan_v(const GatedArgs& a, GatedDev p, const Cut& c) {
+void scan_v(const GatedArgs& a, GatedDev p) {
     constexpr int WAVES = Cfg<BWD>::WAVES;
     p.tiles = tile_count(a.L, WAVES * VEC * TPT);
     p.cb = (unsigned)((a.D + 63) / 64);
     p.per_tile = (unsigned)a.B * p.cb;
     p.total = p.per_tile * (unsigned)p.tiles;
-    p.ticket = c.ticket; p.map = c.map; p.state_word = c.state_word; p.hint = c.hint; p.limit = chain_spin_limit;
+    const Words w = words_of(a.ws, a.B, p.tiles, a.D);
+    p.ticket = w.ticket; p.map = w.map; p.state_word = w.state; p.hint = w.hint; p.limit = chain_spin_limit;
     if (p.tiles > 1) {
-        const int64_t n = (int64_t)(c.clear / 16);
+        const int64_t n = (int64_t)(w.bytes / 16);
         LA_TRACED(a.tr, "gated_clear", gated_clear_kernel<<<(unsigned)std::min<int64_t>((n + 255) / 256, 4096), 256, 0,
-                                                            a.stream>>>((u32x4*)c.ticket, n));
+                                                            a.stream>>>((u32x4*)a.ws, n));
     }
     const dim3 grid(std::min(p.total, MAX_X), (p.total + MAX_X - 1) / MAX_X);
     if constexpr (BWD)
@@ -904,13 +913,13 @@ void scan_v(const GatedArgs& a, GatedDev p, const Cut& c) {
 }
 
 template <typename E>
-void fwd_t(const GatedArgs& a, const GatedDev& p, const Cut& c) {
+void fwd_t(const GatedArgs& a, const GatedDev& p) {
     typedef Cfg<false> C;
     if (a.D % C::VEC == 0 && rows_on(C::VEC * sizeof(E), sizeof(E), C::VEC * C::TPT,
                                      {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz}, {p.y, p.sy}}))
-        scan_v<E, false, C::VEC, C::TPT>(a, p, c);
+        scan_v<E, false, C::VEC, C::TPT>(a, p);
     else
-        scan_v<E, false, 1, C::VEC * C::TPT>(a, p, c);
+        scan_v<E, false, 1, C::VEC * C::TPT>(a, p);
 }
 template <typename E>
 hipError_t bwd_t(const GatedArgs& a) {
@@ -921,7 +930,7 @@ hipError_t bwd_t(const GatedArgs& a) {
     if (c.blocks) {
         GatedDev f = p;
         f.y = nullptr; f.h_out = nullptr; f.blocks = c.blocks;
-        fwd_t<E>(a, f, c);
+        fwd_t<E>(a, f);
         p.blocks_in = c.blocks;
     }
     if (a.B > 0) {
@@ -929,9 +938,9 @@ hipError_t bwd_t(const GatedArgs& a) {
         if (a.D % C::VEC == 0 && rows_on(C::VEC * sizeof(E), sizeof(E), C::VEC * C::TPT,
                                          {{p.x, p.sx}, {p.r, p.sr}, {p.i, p.si}, {p.z, p.sz}, {p.dy, p.sdy}, {p.dx, p.sdx},
                                           {p.dr, p.sdr}, {p.di, p.sdi}, {p.dz, p.sdz}}))
-            scan_v<E, true, C::VEC, C::TPT>(a, p, c);
+            scan_v<E, true, C::VEC, C::TPT>(a, p);
         else
-            scan_v<E, true, 1, C::VEC * C::TPT>(a, p, c);
+            scan_v<E, true, 1, C::VEC * C::TPT>(a, p);
     }
     const unsigned cb = (unsigned)((a.D + 15) / 16);
     const float* part = c.part;
@@ -980,8 +989,7 @@ hipError_t gated_status(unsigned int* give_ups, bool clear) {
 hipError_t launch_gated_scan(const GatedArgs& a) {
     if (a.B == 0 || a.D == 0) return hipSuccess;
     const GatedDev p = dev(a);
-    const Cut c = cut(a.ws, a.B, a.L, a.D, false, false);
-    a.bf16 ? fwd_t<__bf16>(a, p, c) : fwd_t<float>(a, p, c);
+    a.bf16 ? fwd_t<__bf16>(a, p) : fwd_t<float>(a, p);
     return hipGetLastError();
 }
 hipError_t launch_gated_scan_bwd(const GatedArgs& a) {

@@ -576,8 +576,8 @@ la_status la_add_norm_bwd(const void* dy, const void* h, const float* weight, co
  * gate, a residual scale, dropout and the residual sum), and dropout by itself.  Layouts, padded batches, memory, limits
  * and numerics are those of the selective layer above, with what is said here.
  *
- * Workspaces: la_gated_scan and la_gated_scan_bwd 12 bytes per channel and 64 tokens (nothing for sequences of up to
- * 64 tokens), the backward 12 more for its parameters' derivatives and, without h_blocks, 4 more;
+ * Workspaces: la_gated_scan 12 bytes per channel and 128 tokens (nothing for sequences of up to 128 tokens),
+ * la_gated_scan_bwd 24 per channel and 64 tokens, 28 without h_blocks;
  * la_block_norm_bwd 8 D bytes per row, of 768 rows at most.
  *
  * Random numbers.  Dropout's are Philox4x32-10 (Salmon et al., 2011), so that a mask is made again wherever it is

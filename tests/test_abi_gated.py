@@ -91,7 +91,7 @@ def test_scan_validation(lib, bwd):
         assert lib.la_gated_scan_workspace(ctypes.byref(gated_shape(c=0.0)), mode) == SHAPE
     for mode in (-1, 3):
         assert lib.la_gated_scan_workspace(ctypes.byref(s), mode) == UNSUP
-    assert lib.la_gated_scan_workspace(ctypes.byref(gated_shape(L=64)), 0) == 0
+    assert lib.la_gated_scan_workspace(ctypes.byref(gated_shape(L=128)), 0) == 0
 
 
 def test_step_validation(lib):
