@@ -529,8 +529,8 @@ def la_trim_workspace() -> None:
 
 
 def la_chain_status(clear: bool = True) -> int:
-    """Synchronise the current device and return how many chained-forward waves gave up on a wait
-    since the counter was last cleared (raises LaError(LA_ERR_TIMEOUT) when any did)."""
+    """Synchronise the current device and return how many waves of chained forwards and gated recurrences gave up
+    on a wait since the counter was last cleared (raises LaError(LA_ERR_TIMEOUT) when any did)."""
     n = ctypes.c_int64(0)
     st = lib().la_chain_status(1 if clear else 0, ctypes.byref(n))
     _check("la_chain_status", st)

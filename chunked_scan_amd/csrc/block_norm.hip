@@ -7,6 +7,10 @@
 // adjacent elements in fp32.  The mask is Philox4x32-10's output for the chunk's counter, one call per chunk: 16 bits an
 // element, so that the generator's 20 wide products cost 8 elements, not 4; the probability is a multiple of 2^-16 for it,
 // and the kept share in the scale is exact.
+//
+// Measured, bf16: norms, gate and scale over 16384 x 2048 66 us (335 MB, 5.1 TB/s, a copy's rate); their backward with dropout
+// over 8191 x 2048 53 + 6 us (268 MB); dropout with a residual of 16384 x 2048 33 us (201 MB, 6.0 TB/s, of which the last-level
+// cache holds a part).  A mask made by its counter costs no more than the loads hide.
 #include <algorithm>
 
 #include "la_mixer.h"

@@ -103,6 +103,14 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 // one that leaves it, and walks its tokens, whose a and b have stayed in registers.  So every input is read once, a
 // sequence fills the card however few channels there are, and no tile waits for more than the tiles in flight before it.
 //
+// Measured, bf16 with gate (the clearing of the words among it): 1 x 16384 x 2048 forward 82 us, 335 MB at 4.1 TB/s, where
+// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 86 (302 MB; a copy 58).  What bounds it is
+// latency: the vector units are busy 46 % of the time and nothing but inputs is read from memory, but a workgroup whose tile
+// has been read waits for its state before it takes the next one, and six waves a SIMD (backward three, by registers) do
+// not hide all of that.  Why this tile: 64 channels make a state word a lane in the wave that looks back; 32 and 64 tokens
+// make more of them to fold (122 to 136 us where 128 took 106), 16 waves a workgroup wait for each other (97 to 134 where 8
+// took 98), and four channels a lane hold twice the registers (90 against 85).
+//
 // Order.  Workgroups take tiles by a ticket, those of one position in their sequences before the next position's, so
 // every tile that a workgroup waits for has been taken by one that runs already, and the first of them waits for
 // nothing: the waits end whatever the order of dispatch.  They are bounded all the same (chain_spin_limit polls): a
@@ -315,8 +323,7 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
     return q;
 }
 // The rows of one operand: a uniform address and the lane's 32-bit offset (rows_on sees to the range where VEC > 1).
-// Tokens that do not exist are read as the sequence's last.
-// FULL: all of the tile's do.
+// Tokens that do not exist are read as the sequence's last.  FULL: all of the tile's tokens exist.
 template <typename E, int VEC, int TPT, bool FULL>
 __device__ __forceinline__ void load_rows(const void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q,
                                           typename Row<E, VEC>::raw (&r)[TPT]) {
@@ -505,7 +512,8 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
     else fwd_tile<E, VEC, WAVES, TPT, false>(p, q, map_a, map_b);
 }
 
-// Backward.  The same from the sequence's end: the carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the
+// Backward, 64 tokens a tile since its rows and gates stay in registers (168 of them and 13 spilled, three waves a SIMD; two
+// 95 us where three took 87).  The same from the sequence's end: the carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the
 // carry that enters it from behind to A c + R.  The states h_{t-1} come from the forward's states at the tiles'
 // starts.  Tiles behind a sequence's end write zeros.
 template <typename E, int VEC, int WAVES, int TPT, bool FULL>
@@ -787,7 +795,8 @@ __global__ __launch_bounds__(256) void gated_sums_kernel(const float* __restrict
     if (di_bias) di_bias[d] = s[2];
 }
 
-// One token: a row per wave and 64 VEC channels, all of its loads in flight before the first is used.
+// One token: a row per wave and 64 VEC channels, all of its loads in flight before the first is used.  Latency or the host
+// bounds it: 1 x 2048 takes 2.4 us in a graph and 11 from Python.
 template <typename E, int VEC>
 __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
     const int64_t b = blockIdx.x / p.cb, d = ((int64_t)(blockIdx.x % p.cb) * 64 + threadIdx.x) * VEC;

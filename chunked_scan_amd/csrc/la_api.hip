@@ -186,7 +186,7 @@ const char* la_status_str(int32_t status) {
         case LA_ERR_LAUNCH: return "HIP launch or workspace allocation failed";
         case LA_ERR_DECAY: return "invalid decay mode or gate_norm";
         case LA_ERR_WORKSPACE: return "the call needs more workspace than the allocation-free entry point holds";
-        case LA_ERR_TIMEOUT: return "a chained forward's bounded wait gave up; its outputs hold NaN";
+        case LA_ERR_TIMEOUT: return "a bounded wait of a chained forward or gated recurrence gave up; its outputs hold NaN";
     }
     return "unknown status";
 }

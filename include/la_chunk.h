@@ -61,7 +61,7 @@ typedef enum la_status {
     LA_ERR_DECAY = -7,       /* unknown decay mode, or gate_norm <= 0 in gate mode */
     LA_ERR_WORKSPACE = -8,   /* la_chunk_fwd_noalloc: the call needs more than LA_NOALLOC_SCRATCH_BYTES; calls
                                 that take a workspace: it is NULL, unaligned or too small */
-    LA_ERR_TIMEOUT = -9      /* la_chain_status: a chained forward's bounded wait gave up */
+    LA_ERR_TIMEOUT = -9      /* la_chain_status: a bounded wait of a chained forward or gated recurrence gave up */
 } la_status;
 
 typedef enum la_dtype { LA_F32 = 0, LA_BF16 = 1 } la_dtype;
@@ -729,15 +729,15 @@ la_status la_dropout(const void* x, const void* residual, const uint64_t* rng, v
  * Returns LA_OK or LA_ERR_LAUNCH. */
 la_status la_trim_workspace(void);
 
-/* Give-up counter of the chained forward (fwd_schedule = 2) and of the gated recurrence, forward and backward, whose
- * workgroups take the state that enters their tokens from those before.  They wait for each other's
- * flags; every wait is bounded, and a compute wave that polls a flag la_set_chain_spin_limit's
- * number of times without seeing it set stops waiting, computes on a NaN state (so its outputs are
+/* Give-up counter of the chained forward (fwd_schedule = 2) and of the gated recurrence, forward and backward: their
+ * workgroups take the state that enters their tokens from those before and wait for each other's
+ * flags; every wait is bounded, and a wave that polls la_set_chain_spin_limit's number of times
+ * without seeing what it waits for stops waiting, computes on a NaN state (so its outputs are
  * NaN rather than the GPU hanging) and adds one to a per-device counter.  This call synchronises
  * the current device (do not call it while a stream of that device is being captured), stores the
- * counter in *give_ups (if not NULL) and, when clear != 0, resets it to zero.  A chained launch
- * whose workgroups are all resident (the library only chains grids that fit the device) does not
- * give up at the default limit.
+ * counter in *give_ups (if not NULL) and, when clear != 0, resets it to zero.  At the default limit
+ * neither gives up: a chained forward's workgroups are all resident (the library only chains grids
+ * that fit the device), the gated recurrence's wait only for workgroups that started before them.
  * Returns LA_OK if the counter was zero, LA_ERR_TIMEOUT if not, LA_ERR_LAUNCH if the runtime failed. */
 la_status la_chain_status(int32_t clear, int64_t* give_ups);
 
