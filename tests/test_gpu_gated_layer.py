@@ -462,3 +462,42 @@ def test_block_and_dropout_of_the_most_rows():
         assert np.array_equal(R.f64(y[0, first : first + n]) != 0, bits >= 16384), first
     share = float((y[0, : 1 << 30] != 0).double().mean())
     assert abs(share - 0.75) < 5 * (0.75 * 0.25 / 2 ** 30) ** 0.5
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(3, 9), (5, 1001), (600, 515), (7, 2047), (4, 4095), (3, 8201)])
+def test_in_place_rows_of_every_alignment(M, D, dtype):
+    """Rows whose last elements are loaded with those before them, updated in place: the bits of separate outputs, and
+    nothing between the rows is touched."""
+    note(f"in place {M} {D} {dtype}")
+    g = Draw(M + D)
+    p, rng = 0.25, rng_of(3, 4)
+    wide = {k: g.normal(M, D + 3, dtype=dtype) for k in ("x", "gate", "res", "dy", "dh")}
+    w = {k: 1 + g.normal(D, std=0.2) for k in ("w_post", "w_pre", "scale")}
+
+    def views():
+        t = {k: v.clone() for k, v in wide.items()}
+        return t, {k: v[:, 1 : D + 1] for k, v in t.items()}
+
+    def untouched(t, k):
+        assert torch.equal(t[k][:, :1], wide[k][:, :1]) and torch.equal(t[k][:, D + 1 :], wide[k][:, D + 1 :])
+
+    _, v = views()
+    kw = dict(gate=v["gate"], p=p, rng=rng, **w)
+    y, h, rp, rq = la.la_block_norm(v["x"], v["res"], **kw)
+    out = la.la_block_norm_bwd(v["x"], h, v["dy"], v["dh"], rstd_post=rp, rstd_pre=rq, **kw)
+    drop = la.la_dropout(v["x"], rng, p, v["res"])
+    for k in ("x", "res"):
+        t, v = views()
+        y2, h2, _, _ = la.la_block_norm(v["x"], v["res"], h=v[k], **kw)
+        assert torch.equal(h2, h) and torch.equal(y2, y)
+        untouched(t, k)
+        t, v = views()
+        assert torch.equal(la.la_dropout(v["x"], rng, p, v["res"], y=v[k]), drop)
+        untouched(t, k)
+    for k in ("dy", "dh"):
+        t, v = views()
+        got = la.la_block_norm_bwd(v["x"], h, v["dy"], v["dh"], rstd_post=rp, rstd_pre=rq, dresidual=v[k], **kw)
+        for a, b in zip(got, out):
+            assert torch.equal(a, b)
+        untouched(t, k)
