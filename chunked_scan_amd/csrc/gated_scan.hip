@@ -89,11 +89,9 @@ __device__ __forceinline__ Gates gates(float r, float i, const Channel& c) {
     return g;
 }
 // k / (a ln2) = a v / (m^2 ln2): 1 / p, or a w / (1 - a^2)
-template <bool SMALL>
 __device__ __forceinline__ float input_slope(float w, float a) {
-    const float k = rcp(poly_p(w));
-    if (SMALL) return k;
-    return w <= SMALL_W ? k : a * w * rcp(fmaf(-a, a, 1.f));
+    const bool small = w <= SMALL_W;
+    return (small ? 1.f : a * w) * rcp(small ? poly_p(w) : fmaf(-a, a, 1.f));
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -104,7 +102,7 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 // sequence fills the card however few channels there are, and no tile waits for more than the tiles in flight before it.
 //
 // Measured, bf16 with gate (the clearing of the words among it): 1 x 16384 x 2048 forward 82 us, 335 MB at 4.1 TB/s, where
-// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 86 (302 MB; a copy 58).  What bounds it is
+// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 87 (302 MB; a copy 58).  What bounds it is
 // latency: the vector units are busy 46 % of the time and nothing but inputs is read from memory, but a workgroup whose tile
 // has been read waits for its state before it takes the next one, and six waves a SIMD (backward three, by registers) do
 // not hide all of that.  Why this tile: 64 channels make a state word a lane in the wave that looks back; 32 and 64 tokens
@@ -125,7 +123,8 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 
 constexpr uint32_t EMPTY = ~0u;
 
-// Access size, tokens a lane, waves a workgroup, and the least waves a SIMD of the 2-byte vector form, whose registers fit.
+// Access size, tokens a lane, waves a workgroup, and the least waves a SIMD of the vector form (forward: of 2-byte types),
+// whose registers fit.
 template <bool BWD> struct Cfg;
 template <> struct Cfg<false> { static constexpr int VEC = 2, TPT = 8, WAVES = 8, OCC = 6; };
 template <> struct Cfg<true> { static constexpr int VEC = 2, TPT = 8, WAVES = 4, OCC = 3; };
@@ -515,10 +514,10 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
     else fwd_tile<E, VEC, WAVES, TPT, false>(p, q, map_a, map_b);
 }
 
-// Backward, 64 tokens a tile since its rows and gates stay in registers (168 of them and 13 spilled, three waves a SIMD; two
-// 95 us where three took 87).  The same from the sequence's end: the carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the
-// carry that enters it from behind to A c + R.  The states h_{t-1} come from the forward's states at the tiles'
-// starts.  Tiles behind a sequence's end write zeros.
+// Backward, 64 tokens a tile since its rows and gates stay in registers: three waves a SIMD fit (132 registers; fp32 162, two
+// waves 83 us at 2 x 2048 x 2048, three 80), four spill (93 us where three take 88).  The same from the sequence's end: the
+// carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the carry that enters it from behind to A c + R.  The
+// states h_{t-1} come from the forward's states at the tiles' starts.  Tiles behind a sequence's end write zeros.
 template <typename E, int VEC, int WAVES, int TPT, bool FULL>
 __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (*map_a)[64], float (*map_h)[64],
                                          float (*map_c)[64]) {
@@ -668,7 +667,7 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
     }
     float sq[VEC] = {}, sr[VEC] = {}, si[VEC] = {};
     if (FULL || q.any) {
-        float h[VEC], cy[VEC], before[TPT][VEC];
+        float h[VEC], cy[VEC], before[TPT][VEC], sv[TPT][VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             h[v] = map_h[run][col + v];
@@ -676,57 +675,56 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
         }
 #pragma unroll
         for (int j = 0; j < TPT; j++) {
-            float fx[VEC];
+            float fx[VEC], oz[VEC];
+            here(xr[j], yr[j]);
             Row<E, VEC>::get(xr[j], fx);
+            Row<E, VEC>::get(yr[j], sv[j]);
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 before[j][v] = h[v];
                 h[v] = fmaf(a[j][v], h[v], mi[j][v] * fx[v]);
             }
-        }
-        auto grads = [&](auto known) {
-#pragma unroll
-            for (int j = TPT - 1; j >= 0; j--) {
-                if (!FULL && j >= q.n) continue;
-                float fx[VEC], ox[VEC], orr[VEC], oi[VEC], oz[VEC], s[VEC];
-                here(xr[j], yr[j]);
-                if (gated) here(zr[j]);
-#pragma unroll
-                for (int v = 0; v < VEC; v++) here(rho[j][v]);
-                Row<E, VEC>::get(xr[j], fx);
-                Row<E, VEC>::get(yr[j], s);
-                if (gated) {
-                    float z[VEC];
-                    Row<E, VEC>::get(zr[j], z);
-#pragma unroll
-                    for (int v = 0; v < VEC; v++) {
-                        const float sg = sigmoid(z[v]);
-                        oz[v] = s[v] * fmaf(a[j][v], before[j][v], mi[j][v] * fx[v]) * sg * fmaf(z[v], 1.f - sg, 1.f);
-                        s[v] *= z[v] * sg;
-                    }
-                }
+            if (gated) {
+                float z[VEC];
+                here(zr[j]);
+                Row<E, VEC>::get(zr[j], z);
 #pragma unroll
                 for (int v = 0; v < VEC; v++) {
-                    const float g = s[v] + cy[v], bt = mi[j][v] * fx[v], w = rate[v] * rho[j][v];
-                    cy[v] = a[j][v] * g;
-                    const float dw = LN2 * cy[v] * fmaf(input_slope<decltype(known)::value>(w, a[j][v]), bt, -w * before[j][v]);
-                    ox[v] = g * mi[j][v];
-                    orr[v] = dw * (1.f - rho[j][v]);
-                    oi[v] = g * bt * (1.f - iota[j][v]);
-                    sq[v] += dw;
-                    sr[v] += orr[v];
-                    si[v] += oi[v];
+                    const float sg = sigmoid(z[v]);
+                    oz[v] = sv[j][v] * h[v] * sg * fmaf(z[v], 1.f - sg, 1.f);
+                    sv[j][v] *= z[v] * sg;
                 }
-                if (q.on) {
-                    gx.put(j, ox);
-                    gr.put(j, orr);
-                    gi.put(j, oi);
-                    if (gated) gz.put(j, oz);
-                }
+                if (q.on && (FULL || j < q.n)) gz.put(j, oz);
             }
-        };
-        if (small) grads(std::true_type());
-        else grads(std::false_type());
+        }
+        // One copy for all decays: a second one for weak decays alone took so many registers that some spilled
+        // (2 x 4096 x 2048 bf16 87 us, with strong decays 97; so 88 for both).
+#pragma unroll
+        for (int j = TPT - 1; j >= 0; j--) {
+            if (!FULL && j >= q.n) continue;
+            float fx[VEC], ox[VEC], orr[VEC], oi[VEC];
+            here(xr[j]);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) here(rho[j][v]);
+            Row<E, VEC>::get(xr[j], fx);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                const float g = sv[j][v] + cy[v], bt = mi[j][v] * fx[v], w = rate[v] * rho[j][v];
+                cy[v] = a[j][v] * g;
+                const float dw = LN2 * cy[v] * fmaf(input_slope(w, a[j][v]), bt, -w * before[j][v]);
+                ox[v] = g * mi[j][v];
+                orr[v] = dw * (1.f - rho[j][v]);
+                oi[v] = g * bt * (1.f - iota[j][v]);
+                sq[v] += dw;
+                sr[v] += orr[v];
+                si[v] += oi[v];
+            }
+            if (q.on) {
+                gx.put(j, ox);
+                gr.put(j, orr);
+                gi.put(j, oi);
+            }
+        }
     }
     lds_barrier();
 #pragma unroll
@@ -746,7 +744,7 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
     }
 }
 template <typename E, int VEC, int WAVES, int TPT>
-__global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<true>::OCC : 2) void gated_bwd_kernel(GatedDev) {
+__global__ __launch_bounds__(WAVES * 64, VEC > 1 ? Cfg<true>::OCC : 2) void gated_bwd_kernel(GatedDev) {
     // the runs' maps of state and carry, then what enters them; then their shares of the parameters' sums
     __shared__ __align__(16) float map_a[WAVES * VEC][64], map_h[WAVES * VEC][64], map_c[WAVES * VEC][64];
     __shared__ unsigned shared;
