@@ -102,12 +102,12 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 // sequence fills the card however few channels there are, and no tile waits for more than the tiles in flight before it.
 //
 // Measured, bf16 with gate (the clearing of the words among it): 1 x 16384 x 2048 forward 82 us, 335 MB at 4.1 TB/s, where
-// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 87 (302 MB; a copy 58).  What bounds it is
-// latency: the vector units are busy 46 % of the time and nothing but inputs is read from memory, but a workgroup whose tile
-// has been read waits for its state before it takes the next one, and six waves a SIMD (backward three, by registers) do
-// not hide all of that.  Why this tile: 64 channels make a state word a lane in the wave that looks back; 32 and 64 tokens
-// make more of them to fold (122 to 136 us where 128 took 106), 16 waves a workgroup wait for each other (97 to 134 where 8
-// took 98), and four channels a lane hold twice the registers (90 against 85).
+// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 86 (302 MB; a copy 58 to 63).  What bounds it:
+// 128 sequences of one tile, which neither clear nor wait, take 70 us, a copy's rate; sequences of two tiles 76, so clearing
+// and tickets cost 6, and the look-back over 128 tiles another 6.  Arithmetic is hidden but for 2 us (4 in the backward).  Why
+// this tile: 64 channels make a state word a lane in the wave that looks back; 32 and 64 tokens make more of them to fold
+// (122 to 136 us where 128 took 106), 16 waves a workgroup wait for each other (97 to 134 where 8 took 98), and four channels
+// a lane hold twice the registers (90 against 85).
 //
 // Order.  Workgroups take tiles by a ticket, those of one position in their sequences before the next position's, so
 // every tile that a workgroup waits for has been taken by one that runs already, and the first of them waits for
@@ -160,17 +160,22 @@ template <typename E> struct Row<E, 1> {
     static __device__ __forceinline__ void get(raw r, float* f) { f[0] = (float)r; }
     static __device__ __forceinline__ raw put(const float* f) { return (E)f[0]; }
 };
-// A token's row (a uniform address in device memory) at a lane's channels, `at` bytes behind, which fit 32 bits.  What is
-// written is not read here and leaves by a streaming store: 2 x 4096 x 2048 bf16 forward and backward 168 -> 159 us.
+// A token's row (a uniform address in device memory) at a lane's channels, `at` bytes behind, which fit 32 bits.
+// The last-level cache is left to what is read again soon: the forward's outputs leave by streaming stores (2 x 4096 x 2048
+// bf16 forward and backward 168 -> 159 us), since the backward reads its inputs again; the backward, their last reader,
+// loads them by streaming loads and stores its outputs by ordinary ones (88 -> 85.6; fp32 2 x 2048 x 2048 80.5 -> 75.4).
 typedef __attribute__((address_space(1))) char* GlobalRow;
 __device__ __forceinline__ GlobalRow global_row(const void* p) { return (GlobalRow)(uintptr_t)p; }
-template <typename E, int VEC>
+template <typename E, int VEC, bool STREAM = false>
 __device__ __forceinline__ typename Row<E, VEC>::raw ld(GlobalRow row, uint32_t at) {
-    return *(const __attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
+    const auto* q = (const __attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
+    return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
-template <typename E, int VEC>
+template <typename E, int VEC, bool STREAM = true>
 __device__ __forceinline__ void st(GlobalRow row, uint32_t at, const float* f) {
-    __builtin_nontemporal_store(Row<E, VEC>::put(f), (__attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at));
+    auto* q = (__attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
+    if (STREAM) __builtin_nontemporal_store(Row<E, VEC>::put(f), q);
+    else *q = Row<E, VEC>::put(f);
 }
 
 // Waits that gave up, per device (read and cleared by gated_status).
@@ -323,7 +328,7 @@ __device__ __forceinline__ Place place_of(GatedArgsPtr p, unsigned idx, bool bac
 }
 // The rows of one operand: a uniform address and the lane's 32-bit offset (rows_on sees to the range where VEC > 1).
 // Tokens that do not exist are read as the sequence's last.  FULL: all of the tile's tokens exist.
-template <typename E, int VEC, int TPT, bool FULL>
+template <typename E, int VEC, int TPT, bool FULL, bool STREAM = false>
 __device__ __forceinline__ void load_rows(const void* base, const __attribute__((address_space(4))) la_rows& s, const Place& q,
                                           typename Row<E, VEC>::raw (&r)[TPT]) {
     const int64_t step = s.token * (int64_t)sizeof(E);
@@ -333,18 +338,18 @@ __device__ __forceinline__ void load_rows(const void* base, const __attribute__(
         const uint32_t own = VEC == 1 ? at : at + (uint32_t)(q.run * TPT) * pitch;
 #pragma unroll
         for (int j = 0; j < TPT; j++) {
-            r[j] = ld<E, VEC>(row, own);
+            r[j] = ld<E, VEC, STREAM>(row, own);
             if (FULL || q.t0 + j + 1 < q.len) row += step;
             asm("" : "+s"(row));  // stays a uniform address with a 32-bit offset, not one 64-bit sum a lane and token
         }
     } else {
         const int last = q.len - 1 - q.t0;
 #pragma unroll
-        for (int j = 0; j < TPT; j++) r[j] = ld<E, VEC>(row, at + (uint32_t)min(q.run * TPT + j, last) * pitch);
+        for (int j = 0; j < TPT; j++) r[j] = ld<E, VEC, STREAM>(row, at + (uint32_t)min(q.run * TPT + j, last) * pitch);
     }
 }
 // An output's rows: the lane's VEC values of its j-th token.
-template <typename E, int VEC, int TPT>
+template <typename E, int VEC, int TPT, bool STREAM>
 struct OutRows {
     GlobalRow row;
     int64_t step;
@@ -358,7 +363,7 @@ struct OutRows {
     __device__ __forceinline__ void put(int j, const float* f) const {
         GlobalRow at = row + j * step;
         asm("" : "+s"(at));  // as in load_rows
-        st<E, VEC>(at, own, f);
+        st<E, VEC, STREAM>(at, own, f);
     }
 };
 
@@ -485,7 +490,7 @@ __device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (
 #pragma unroll
     for (int v = 0; v < VEC; v++) h[v] = map_b[run][col + v];
     p = gated_args();
-    const OutRows<E, VEC, TPT> y(p->y, p->sy, q);
+    const OutRows<E, VEC, TPT, true> y(p->y, p->sy, q);
 #pragma unroll
     for (int j = 0; j < TPT; j++) {
         float o[VEC];
@@ -515,7 +520,7 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
 }
 
 // Backward, 64 tokens a tile since its rows and gates stay in registers: three waves a SIMD fit (132 registers; fp32 162, two
-// waves 83 us at 2 x 2048 x 2048, three 80), four spill (93 us where three take 88).  The same from the sequence's end: the
+// waves 83 us at 2 x 2048 x 2048, three 80); a fourth gains nothing (88 us with the input gates in LDS, as with three).  The same from the sequence's end: the
 // carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the carry that enters it from behind to A c + R.  The
 // states h_{t-1} come from the forward's states at the tiles' starts.  Tiles behind a sequence's end write zeros.
 template <typename E, int VEC, int WAVES, int TPT, bool FULL>
@@ -534,11 +539,11 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
     if (FULL || q.any) {
         const Params<VEC> par(p, q.d);
         raw rr[TPT], ir[TPT];
-        load_rows<E, VEC, TPT, FULL>(p->r, p->sr, q, rr);
-        load_rows<E, VEC, TPT, FULL>(p->i, p->si, q, ir);
-        load_rows<E, VEC, TPT, FULL>(p->x, p->sx, q, xr);
-        load_rows<E, VEC, TPT, FULL>(p->dy, p->sdy, q, yr);
-        if (gated) load_rows<E, VEC, TPT, FULL>(p->z, p->sz, q, zr);
+        load_rows<E, VEC, TPT, FULL, true>(p->r, p->sr, q, rr);
+        load_rows<E, VEC, TPT, FULL, true>(p->i, p->si, q, ir);
+        load_rows<E, VEC, TPT, FULL, true>(p->x, p->sx, q, xr);
+        load_rows<E, VEC, TPT, FULL, true>(p->dy, p->sdy, q, yr);
+        if (gated) load_rows<E, VEC, TPT, FULL, true>(p->z, p->sz, q, zr);
         Channel c[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
@@ -653,7 +658,7 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
     }
     lds_barrier();
     p = gated_args();
-    const OutRows<E, VEC, TPT> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
+    const OutRows<E, VEC, TPT, false> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
     if (!FULL && q.on) {  // rows behind the sequence's end
         const int rows = max(0, min(TPT, (int)p->L - (q.t0 + q.run * TPT)));
         const float zero[VEC] = {};
