@@ -161,9 +161,9 @@ template <typename E> struct Row<E, 1> {
     static __device__ __forceinline__ raw put(const float* f) { return (E)f[0]; }
 };
 // A token's row (a uniform address in device memory) at a lane's channels, `at` bytes behind, which fit 32 bits.
-// The last-level cache is left to what is read again soon: the forward's outputs leave by streaming stores (2 x 4096 x 2048
-// bf16 forward and backward 168 -> 159 us), since the backward reads its inputs again; the backward, their last reader,
-// loads them by streaming loads and stores its outputs by ordinary ones (88 -> 85.6; fp32 2 x 2048 x 2048 80.5 -> 75.4).
+// Outputs leave by streaming stores (2 x 4096 x 2048 bf16 forward and backward 168 -> 159 us), so that the last-level cache
+// keeps the forward's inputs, which the backward reads again; the backward, their last reader, takes them by streaming
+// loads (134.8 -> 131.6; with ordinary stores 142).
 typedef __attribute__((address_space(1))) char* GlobalRow;
 __device__ __forceinline__ GlobalRow global_row(const void* p) { return (GlobalRow)(uintptr_t)p; }
 template <typename E, int VEC, bool STREAM = false>
@@ -171,11 +171,9 @@ __device__ __forceinline__ typename Row<E, VEC>::raw ld(GlobalRow row, uint32_t 
     const auto* q = (const __attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
     return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
-template <typename E, int VEC, bool STREAM = true>
+template <typename E, int VEC>
 __device__ __forceinline__ void st(GlobalRow row, uint32_t at, const float* f) {
-    auto* q = (__attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at);
-    if (STREAM) __builtin_nontemporal_store(Row<E, VEC>::put(f), q);
-    else *q = Row<E, VEC>::put(f);
+    __builtin_nontemporal_store(Row<E, VEC>::put(f), (__attribute__((address_space(1))) typename Row<E, VEC>::raw*)(row + at));
 }
 
 // Waits that gave up, per device (read and cleared by gated_status).
@@ -349,7 +347,7 @@ __device__ __forceinline__ void load_rows(const void* base, const __attribute__(
     }
 }
 // An output's rows: the lane's VEC values of its j-th token.
-template <typename E, int VEC, int TPT, bool STREAM>
+template <typename E, int VEC, int TPT>
 struct OutRows {
     GlobalRow row;
     int64_t step;
@@ -363,7 +361,7 @@ struct OutRows {
     __device__ __forceinline__ void put(int j, const float* f) const {
         GlobalRow at = row + j * step;
         asm("" : "+s"(at));  // as in load_rows
-        st<E, VEC, STREAM>(at, own, f);
+        st<E, VEC>(at, own, f);
     }
 };
 
@@ -490,7 +488,7 @@ __device__ __forceinline__ void fwd_tile(GatedArgsPtr p, const Place& q, float (
 #pragma unroll
     for (int v = 0; v < VEC; v++) h[v] = map_b[run][col + v];
     p = gated_args();
-    const OutRows<E, VEC, TPT, true> y(p->y, p->sy, q);
+    const OutRows<E, VEC, TPT> y(p->y, p->sy, q);
 #pragma unroll
     for (int j = 0; j < TPT; j++) {
         float o[VEC];
@@ -658,7 +656,7 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
     }
     lds_barrier();
     p = gated_args();
-    const OutRows<E, VEC, TPT, false> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
+    const OutRows<E, VEC, TPT> gx(p->dx, p->sdx, q), gr(p->dr, p->sdr, q), gi(p->di, p->sdi, q), gz(p->dz, p->sdz, q);
     if (!FULL && q.on) {  // rows behind the sequence's end
         const int rows = max(0, min(TPT, (int)p->L - (q.t0 + q.run * TPT)));
         const float zero[VEC] = {};
