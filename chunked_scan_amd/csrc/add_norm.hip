@@ -83,8 +83,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(h[i][j], h[i][j], ss);
     }
-    const float r = row_rstd<TPR, VPT>(h, ss, p.inv_d, p.eps, buf);
-    if (p.rstd && tid == 0) p.rstd[m] = r;
+    const RowScale rs = row_rstd<TPR, VPT>(h, ss, p.inv_d, p.eps, buf);
+    if (p.rstd && tid == 0) p.rstd[m] = rs.own();
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(NormDev
         float w[8];
         load8<float, VEC>(p.weight + d, n, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) h[i][j] *= r * w[j];
+        for (int j = 0; j < 8; j++) h[i][j] = h[i][j] * rs.s * (rs.r * w[j]);
         if (!Y8)
             store8<E, VEC>((E*)p.y + m * p.sy + d, n, h[i]);
         else

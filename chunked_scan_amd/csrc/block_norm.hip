@@ -218,10 +218,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
 #pragma unroll
         for (int j = 0; j < 8; j++) ss = fmaf(v[i][j], v[i][j], ss);
     }
-    float rp = 1.f;
+    RowScale rp = {1.f, 1.f};
     if (p.w_post) {
         rp = row_rstd<TPR, VPT>(v, ss, p.inv_d, p.eps, buf);
-        if (p.rstd_post && tid == 0) p.rstd_post[m] = rp;
+        if (p.rstd_post && tid == 0) p.rstd_post[m] = rp.own();
     }
     Rng rng = {};
     if (DROP) rng = load_rng(p.rng);
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
             if (AHEAD) post0.get(f, n, back);
             else get8<float, VEC>(p.w_post + d, n, back, f);
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[i][j] *= rp * f[j];
+            for (int j = 0; j < 8; j++) v[i][j] = v[i][j] * rp.s * (rp.r * f[j]);
         }
         if (p.gate) {
             if (AHEAD) gate0.get(f, n, back);
@@ -269,8 +269,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         for (int j = 0; j < 8; j++) ss = fmaf(v[i][j], v[i][j], ss);
     }
     if (!p.w_pre) return;
-    const float rq = row_rstd<TPR, VPT>(v, ss, p.inv_d, p.eps, buf);
-    if (p.rstd_pre && tid == 0) p.rstd_pre[m] = rq;
+    const RowScale rq = row_rstd<TPR, VPT>(v, ss, p.inv_d, p.eps, buf);
+    if (p.rstd_pre && tid == 0) p.rstd_pre[m] = rq.own();
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
         const int64_t d = (int64_t)(i * TPR + tid) * 8;
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_kernel(Block
         if (AHEAD) pre0.get(w, n, back);
         else get8<float, VEC>(p.w_pre + d, n, back, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) w[j] *= v[i][j] * rq;
+        for (int j = 0; j < 8; j++) w[j] *= v[i][j] * rq.s * rq.r;
         put8<E, VEC>((E*)p.y + m * p.sy + d, n, w);
     }
 }

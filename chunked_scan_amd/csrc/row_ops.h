@@ -107,21 +107,29 @@ __device__ __forceinline__ float inv_sqrt(float v) {
     return small ? x * 0x1p+32f : x;
 }
 
+// A row's reciprocal deviation, as that of the row times s: s = 1, or a power of two for rows of large values, whose own
+// may lie below fp32's normal range.  A normed value is (h s) (r w), which keeps its digits.
+struct RowScale {
+    float r, s;
+    __device__ __forceinline__ float own() const { return r * s; }
+};
 // 1 / sqrt(mean h^2 + eps) of a row held by TPR threads; ss: the thread's share of the sum of squares.
 template <int TPR, int VPT>
-__device__ __forceinline__ float row_rstd(const float (&h)[VPT][8], float ss, float inv_d, float eps, float* buf) {
+__device__ __forceinline__ RowScale row_rstd(const float (&h)[VPT][8], float ss, float inv_d, float eps, float* buf) {
     ss = row_sum<TPR>(ss, buf);
-    if (ss < INFINITY) return inv_sqrt(fmaf(ss, inv_d, eps));
-    // squares past fp32 (values of 1e19 and more): the sum of (h 2^-64)^2.  All threads of the row come here.
+    if (ss < INFINITY) return {inv_sqrt(fmaf(ss, inv_d, eps)), 1.f};
+    // squares past fp32 (some value is 2^64 / sqrt(D) or more): the sum of (h 2^-96)^2, at most 2^64 D; what underflows
+    // is less than 2^-70 of the sum.  All threads of the row come here.
+    constexpr float S = 0x1p-96f;
     float s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; i++)
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const float v = h[i][j] * 0x1p-64f;
+            const float v = h[i][j] * S;
             s2 = fmaf(v, v, s2);
         }
-    return inv_sqrt(fmaf(row_sum<TPR>(s2, buf), inv_d, eps * 0x1p-64f * 0x1p-64f)) * 0x1p-64f;
+    return {inv_sqrt(fmaf(row_sum<TPR>(s2, buf), inv_d, eps * S * S)), S};
 }
 
 // Whether rows `stride` elements apart all start on 16 bytes.

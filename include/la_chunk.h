@@ -539,7 +539,8 @@ typedef struct la_norm_shape {
  *   h           : [M,D] dtype or NULL, the sum, rounded (the norm takes the unrounded sum); may be
  *                 the same pointer, with the same stride, as residual or x
  *   rstd        : float[M] or NULL, r of every row.
- * Holds for any finite h, also where its squares overflow fp32.
+ * Holds for any finite h, also where its squares overflow fp32 (r of values near fp32's largest is a subnormal number, so
+ * rstd and what the backward pass makes of it are off by half a step of those, 2^-22 of r, there).
  * No output may otherwise overlap another argument.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
  */
@@ -681,7 +682,7 @@ typedef struct la_block_shape {
  *   h                 : [M,D] dtype, the stream, rounded (the norm takes the unrounded sum); may be the same pointer,
  *                       with the same stride, as residual or x
  *   rstd_post, rstd_pre : float[M] or NULL, rp and rq of every row (only written where there is such a norm).
- * Both norms hold for any finite row, also where its squares overflow fp32.
+ * Both norms hold for any finite row, also where its squares overflow fp32 (the rstd outputs as in la_add_norm).
  * No output may otherwise overlap another argument.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED or LA_ERR_LAUNCH.
  */
