@@ -238,6 +238,10 @@ __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x);
 // below zero e^-x overflows to infinity and the result is 0.
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + __builtin_amdgcn_exp2f(x * -LOG2E)); }
 
+// 1 - s for s = sigma(x) = 1 / (1 + e), e = e^-x: e s where s is the greater part, since the difference keeps none of the
+// digits of what is left next to 1.  (e infinite: s = 0, and the difference is exact.)
+__device__ __forceinline__ float complement(float e, float s) { return e < 1.f ? e * s : 1.f - s; }
+
 // delta = log(1 + e^x) = max(x, 0) + log1p(y), y = e^-|x| in [0, 1].  Step sizes of 1e-3 are ordinary,
 // so log1p needs its relative accuracy near y = 0, which log2(1 + y) loses (2^-24 / y).  With
 // s = y / (2 + y) <= 1/3, log1p(y) = 2 atanh(s) = s P(s^2); the degree-4 P below was fitted at the

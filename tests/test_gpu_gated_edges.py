@@ -8,7 +8,7 @@ import gated_ref as G
 import mixer_ref as R
 from chunked_scan_amd import binding as la
 from gpu_util import note
-from test_gpu_gated import block_inputs, check_block
+from test_gpu_gated import block_inputs, check_block, scan_inputs, scan_kw, scan_ref
 from test_gpu_mixer import BF, F32, Draw
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,54 @@ def test_norms_of_rows_near_the_largest_value(D, dtype):
     tol = np.abs(want) * (2.0 ** -4 + (D / 8 + 40) * R.U) + s * 2.0 ** -10 * 1.01
     assert (np.abs(R.f64(q.float()) * s - want) <= tol).all()
     check_rstd(rstd, r[:, 0], D)
+
+
+# ------------------------------------------------------------------------------------ gates that are all but open
+
+# sigma(-v) next to zero is a small number in its own right.  With e = exp(-v), 1 - sigma(v) = e sigma(v): e's relative bound
+# 2 (|r| + |b|) + 2, and the sum, the reciprocal and the product; so gated_ref's bound of sigma, and one rounding where it is
+# taken as a difference from 1 (there it is above 1/2).
+
+
+def open_gates_ref(a, c):
+    """[(value, bound)] of dr, di, dr_bias, di_bias without output gate and lengths, relative to 1 - rho and 1 - iota."""
+    x, r, i, lam, rb, ib, _, h_in, _, _ = scan_ref(a, None, c)
+    g, _, _, _, _, before, e_before, H_before, b = G.scan(x, r, i, lam, rb, ib, None, h_in, None, c)[3]
+    dy = R.f64(a["dy"])
+    carry, ec = np.zeros_like(h_in), np.zeros_like(h_in)
+    gs, eg, Gm = np.zeros_like(x), np.zeros_like(x), np.zeros_like(x)
+    C = np.abs(carry)
+    for t in range(x.shape[1] - 1, -1, -1):
+        gs[:, t], Gm[:, t] = dy[:, t] + carry, np.abs(dy[:, t]) + C
+        eg[:, t] = ec + 4 * Gm[:, t]
+        at = g.a[:, t]
+        carry, C, ec = at * gs[:, t], at * Gm[:, t], at * (eg[:, t] + (g.k_a[:, t] + 1) * Gm[:, t])
+    co_r, co_i, ab = R.sig(-(r + rb)), R.sig(-(i + ib)), np.abs(b)
+    q = gs * (g.slope * b - g.v * g.a * before)
+    eq = eg * (g.slope * ab + g.v * g.a * H_before) + Gm * (
+        g.slope * ab * (g.k_slope + g.k_mi + 4) + g.v * g.a * (e_before + (g.k_v + g.k_a + 5) * H_before))
+    Q = Gm * (g.slope * ab + g.v * g.a * H_before)
+    dr = (q * co_r, co_r * (eq + Q * (g.k_rho + 3)))
+    di = (gs * b * co_i, ab * co_i * (eg + Gm * (g.k_mi + g.k_iota + 6)))
+    n = x.shape[0] * x.shape[1] + 8
+    return [dr, di, (dr[0].sum((0, 1)), dr[1].sum((0, 1)) + n * (Q * co_r).sum((0, 1))),
+            (di[0].sum((0, 1)), di[1].sum((0, 1)) + n * (ab * Gm * co_i).sum((0, 1)))]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(40, 1, 64), (2, 70, 130), (1, 200, 65)])
+def test_scan_gradients_of_gates_that_are_all_but_open(B, L, D, dtype):
+    """r + r_bias and i + i_bias from -20 to 40: the gates' gradients keep their digits however close to 1 a gate is."""
+    note(f"gated scan: open gates {B} {L} {D} {dtype}")
+    a, _ = scan_inputs((B, L, D, None, False, False, True, True, -5.0), dtype, 51)
+    g = Draw(52)
+    for k in ("r", "i"):
+        a[k] = g.uniform(B, L, D, lo=-20.0, hi=38.0).to(dtype)
+    got = la.la_gated_scan_bwd(*[a[k] for k in ("x", "r", "i", "lam", "dy")], **scan_kw(a, None))
+    names = ("dr", "di", "dr_bias", "di_bias")
+    for name, t, ref in zip(names, (got[1], got[2], got[4], got[5]), open_gates_ref(a, 8.0)):
+        G.close(t, *ref, dtype if t.dim() == 3 else F32, name)
+    # and where sigma's complement leaves fp32 there is no value but zero
+    a["r"].fill_(200.0), a["i"].fill_(200.0)
+    got = la.la_gated_scan_bwd(*[a[k] for k in ("x", "r", "i", "lam", "dy")], **scan_kw(a, None))
+    assert (got[1] == 0).all() and (got[2] == 0).all() and all(torch.isfinite(t).all() for t in got if t is not None)
