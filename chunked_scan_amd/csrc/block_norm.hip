@@ -176,9 +176,9 @@ __device__ __forceinline__ void act_slope(float g, int kind, float* f, float* df
     *f = g;
     *df = 1.f;
     if (kind == LA_GATE_LINEAR) return;
-    const float s = sigmoid(g);
+    const float e = __builtin_amdgcn_exp2f(g * -LOG2E), s = rcp(1.f + e), shut = complement(e, s);
     *f = kind == LA_GATE_SIGMOID ? s : g * s;
-    *df = kind == LA_GATE_SIGMOID ? s * (1.f - s) : s * fmaf(g, 1.f - s, 1.f);
+    *df = kind == LA_GATE_SIGMOID ? s * shut : s * fmaf(g, shut, 1.f);
 }
 
 template <typename E, int TPR, int VPT, bool VEC, bool DROP>

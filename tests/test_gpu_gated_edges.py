@@ -108,3 +108,22 @@ def test_scan_gradients_of_gates_that_are_all_but_open(B, L, D, dtype):
     a["r"].fill_(200.0), a["i"].fill_(200.0)
     got = la.la_gated_scan_bwd(*[a[k] for k in ("x", "r", "i", "lam", "dy")], **scan_kw(a, None))
     assert (got[1] == 0).all() and (got[2] == 0).all() and all(torch.isfinite(t).all() for t in got if t is not None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 1001])
+def test_norm_gradients_of_gates_that_are_all_but_open(D, dtype):
+    note(f"block norm: open gates {D} {dtype}")
+    M = 5
+    a = block_inputs(M, D, dtype, 53)
+    a["gate"] = Draw(54).uniform(M, D, lo=-20.0, hi=40.0).to(dtype)
+    _, h, rp, rq = la.la_block_norm(a["x"], a["res"], w_post=a["w_post"], w_pre=a["w_pre"], gate=a["gate"], act="sigmoid",
+                                    scale=a["scale"])
+    got = la.la_block_norm_bwd(a["x"], h, a["dy"], a["dh"], w_post=a["w_post"], w_pre=a["w_pre"], gate=a["gate"],
+                               act="sigmoid", scale=a["scale"], rstd_post=rp, rstd_pre=rq)[2]
+    # du n scale, which the linear gate's derivative is; times s (1 - s), each with the gate's relative bound
+    v, e = G.block_bwd(R.f64(a["x"]), R.f64(a["gate"]), R.f64(h), *[R.f64(a[k]) for k in ("w_post", "scale", "w_pre")], "linear",
+                       R.f64(rp), R.f64(rq), R.f64(a["dy"]), R.f64(a["dh"]))[2]
+    gate = R.f64(a["gate"])
+    slope = R.sig(gate) * R.sig(-gate)
+    G.close(got, v * slope, (e + np.abs(v) * (4 * np.abs(gate) + 20)) * slope, dtype, "dgate")
