@@ -61,10 +61,19 @@ struct GatedDev {
 struct Channel {
     float nr, ni, rate;
 };
+constexpr float MAX_RATE = 0x1.fffffep127f;
+// A rate past fp32 is its largest value: infinity times a closed gate's zero would be NaN.  (c softplus(lam) first: c log2 e
+// may be infinite where softplus is zero.)
+__device__ __forceinline__ float rate_of(float lam, float c) {
+    const float v = c * softplus(lam) * LOG2E;
+    return v > MAX_RATE ? MAX_RATE : v;  // NaN stays
+}
 __device__ __forceinline__ Channel channel(const float* lam, const float* r_bias, const float* i_bias, float c, int64_t d) {
-    return {r_bias ? -LOG2E * r_bias[d] : 0.f, i_bias ? -LOG2E * i_bias[d] : 0.f, c * LOG2E * softplus(lam[d])};
+    return {r_bias ? -LOG2E * r_bias[d] : 0.f, i_bias ? -LOG2E * i_bias[d] : 0.f, rate_of(lam[d], c)};
 }
 
+// 2^-w is zero in fp32.
+constexpr float NO_DECAY_LEFT = 256.f;
 // With w = v log2 e, a = 2^-w.  1 - a^2 = a w p for w up to SMALL_W (v <= 1/2), where p = 2 ln2 S is a polynomial in w^2;
 // above it 1 - a^2 itself has its digits.  SMALL: every w is small (a channel's rate bounds its w, so a whole wave knows).
 constexpr float SMALL_W = 0.5f * LOG2E;
@@ -289,7 +298,7 @@ struct Params {
         }
     }
     __device__ __forceinline__ Channel channel(int v, float c) const {
-        return {by_r * r[v], by_i * i[v], c * LOG2E * softplus(lam[v])};
+        return {by_r * r[v], by_i * i[v], rate_of(lam[v], c)};
     }
 };
 
@@ -727,7 +736,8 @@ __device__ __forceinline__ void bwd_tile(GatedArgsPtr p, const Place& q, float (
             for (int v = 0; v < VEC; v++) {
                 float rh, rest;
                 both(rho[j][v], &rh, &rest);
-                const float g = sv[j][v] + cy[v], bt = mi[j][v] * fx[v], w = rate[v] * rh;
+                const float g = sv[j][v] + cy[v], bt = mi[j][v] * fx[v];
+                const float w = fminf(rate[v] * rh, NO_DECAY_LEFT);  // a = 0 there already, and w times the state may not overflow
                 cy[v] = a[j][v] * g;
                 const float dw = LN2 * cy[v] * fmaf(input_slope(w, a[j][v]), bt, -w * before[j][v]);
                 ox[v] = g * mi[j][v];

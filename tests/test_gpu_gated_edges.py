@@ -127,3 +127,55 @@ def test_norm_gradients_of_gates_that_are_all_but_open(D, dtype):
     gate = R.f64(a["gate"])
     slope = R.sig(gate) * R.sig(-gate)
     G.close(got, v * slope, (e + np.abs(v) * (4 * np.abs(gate) + 20)) * slope, dtype, "dgate")
+
+
+# ------------------------------------------------------------------------------------ rates past fp32's range
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 65])
+def test_rates_beyond_the_range(D, dtype):
+    """c softplus(lam) up to infinity in fp32 for finite c and lam: the decay is complete (a = 0, m = 1) where the gate is
+    open, a closed gate holds the state, and every gradient is finite."""
+    note(f"gated scan: rates beyond the range {D} {dtype}")
+    B, L = 2, 150
+    a, _ = scan_inputs((B, L, D, None, False, True, True, True, -5.0), dtype, 61)
+    a["lam"] = torch.tensor([3e38, 1e38, 3e37, 1e30, 1e20, 200.0, -3.0], device="cuda").repeat(D)[:D].contiguous()
+    a["x"] = a["x"] * 1e6
+    a["h_in"] = a["h_in"] * 1e9
+    a["r"][:, 10:14] = float("-inf")
+    a["r"][:, 130:] = float("-inf")
+    kw, args = scan_kw(a, None), [a[k] for k in ("x", "r", "i", "lam")]
+    y, h, _ = la.la_gated_scan(*args, **kw)
+    ref = scan_ref(a, None, 8.0)
+    ref[1] = np.where(np.isneginf(R.f64(a["r"])), -np.inf, ref[1])  # scan_ref takes infinities to large numbers
+    with np.errstate(invalid="ignore", over="ignore"):
+        ry, rh, _, _ = G.scan(*ref)
+    live = np.broadcast_to(R.f64(a["lam"]) < 1e3, ry[0].shape)
+    # a complete decay has no roundings in its exponent: the state is iota x of the last open token, or the incoming one
+    open_ = ~np.isneginf(R.f64(a["r"]))
+    want, s = np.zeros_like(ry[0]), R.f64(a["h_in"])
+    iota = R.sig(ref[2] + ref[5])
+    for t in range(L):
+        s = np.where(open_[:, t], iota[:, t] * ref[0][:, t], s)
+        want[:, t] = s
+    k_iota = 2 * (np.abs(ref[2]) + np.abs(ref[5])) + 10
+    z, kz = G.silu_of(ref[6])
+    held = np.maximum.accumulate(np.where(open_, np.arange(L)[None, :, None], 0), 1)
+    ks = np.take_along_axis(k_iota, held, 1)
+    G.close(y, np.where(live, ry[0], want * z), np.where(live, ry[1], np.abs(want * z) * (ks + kz + 4)), dtype, "y")
+    assert torch.isfinite(h).all()
+    # bf16 rows of dy times states of 1e9 stay in range
+    got = la.la_gated_scan_bwd(*args, a["dy"], dh_out=a["dh_out"], **kw)
+    full = torch.from_numpy(~live[0, 0]).cuda()
+    for t in got:
+        assert torch.isfinite(t).all()
+    # v dL/dv is zero at a complete decay, and zero where the state is held
+    assert (got[1][..., full] == 0).all() and (got[3][full] == 0).all() and (got[4][full] == 0).all()
+    state = a["h_in"].clone()
+    one = [t[:, 10].contiguous() for t in (a["x"], a["r"], a["i"])]
+    la.la_gated_step(*one, a["lam"], state, r_bias=a["rb"], i_bias=a["ib"])
+    assert torch.equal(state, a["h_in"])
+    # a large c and a softplus that is zero: no decay
+    h = la.la_gated_scan(*args[:3], torch.full_like(a["lam"], -200.0), c=3e38, **kw)[1]
+    assert torch.equal(h, a["h_in"])
