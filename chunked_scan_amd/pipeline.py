@@ -374,8 +374,9 @@ def gated_prompt(p: GatedParams, n: torch.Tensor, residual: Optional[torch.Tenso
     the convolved [B, L, D] to (r, i): two [B, L, D]; project_out the recurrence's rows [B L, D] to (x, gate): two
     [B L, Dm], gate possibly None.  Rows of n and residual behind a sequence's length may hold anything and count as
     zero.  conv_state [B, W-1, D] and h_in [B, D]: states of the tokens before, or None; rng: dropout's seed and
-    offset.  Returns (y [B, L, Dm] the next layer's n or None without w_pre, h [B, L, Dm] the residual stream, conv_state,
-    h_out).  `saved`, a dict, receives what gated_backward takes."""
+    offset, which may be changed in place after the call (`saved` holds a copy).  Returns (y [B, L, Dm] the next layer's n
+    or None without w_pre, h [B, L, Dm] the residual stream, conv_state, h_out).  `saved`, a dict, receives what
+    gated_backward takes."""
     B, L, Dm = n.shape
     pad = _padding(lengths, B, L, n.device)
     rows = lambda t: None if t is None else t.reshape(B * L, Dm)  # noqa: E731
@@ -391,6 +392,8 @@ def gated_prompt(p: GatedParams, n: torch.Tensor, residual: Optional[torch.Tenso
     y, h, rstd_post, rstd_pre = la_block_norm(x, _blank_rows(rows(residual), pad), gate=gate, p=p.dropout, rng=rng,
                                               eps=p.eps, **p.norms())
     if saved is not None:
+        if rng is not None:
+            rng = rng.clone()  # what it holds now: the caller may move on to the next layer's offset in place
         saved.update(u=u, z=z, v=v, r=r, i=i, conv_state=conv_state, h_in=h_in, lengths=lengths, blocks=blocks, x=x,
                      gate=gate, h=h, rstd_post=rstd_post, rstd_pre=rstd_pre, rng=rng)
     return None if y is None else y.view(B, L, Dm), h.view(B, L, Dm), conv_out, h_out

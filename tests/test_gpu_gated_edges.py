@@ -7,8 +7,10 @@ import torch
 import gated_ref as G
 import mixer_ref as R
 from chunked_scan_amd import binding as la
+from chunked_scan_amd import pipeline
 from gpu_util import note
-from test_gpu_gated import block_inputs, check_block, scan_inputs, scan_kw, scan_ref
+from test_gpu_gated import block_inputs, check_block, rng_of, scan_inputs, scan_kw, scan_ref
+from test_gpu_gated_layer import layer
 from test_gpu_mixer import BF, F32, Draw
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +181,24 @@ def test_rates_beyond_the_range(D, dtype):
     # a large c and a softplus that is zero: no decay
     h = la.la_gated_scan(*args[:3], torch.full_like(a["lam"], -200.0), c=3e38, **kw)[1]
     assert torch.equal(h, a["h_in"])
+
+
+# ------------------------------------------------------------------------------------ the layer's generator
+
+
+def test_layer_backward_after_the_generator_moved_on():
+    """One generator for several layers, its offset advanced in place behind each forward: a layer's backward drops what
+    its own forward dropped."""
+    note("gated layer: the generator moves on")
+    B, L, D, Dm, W = 2, 40, 32, 48, 4
+    p, proj, backwards = layer(D, Dm, W, 71, dropout=0.4)
+    g = Draw(72)
+    n, res, dy, dh = (g.normal(B, L, Dm) for _ in range(4))
+    grads = []
+    for step in (0, 1):
+        rng, saved = rng_of(3, 100), {}
+        pipeline.gated_prompt(p, n, res, *proj, rng=rng, saved=saved)
+        rng[1] += step
+        grads.append(pipeline.gated_backward(p, saved, dy, dh, **backwards(F32)))
+    for k, t in grads[0].items():
+        assert (t is None) == (grads[1][k] is None) and (t is None or torch.equal(t, grads[1][k])), k
