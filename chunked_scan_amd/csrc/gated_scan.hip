@@ -965,7 +965,7 @@ hipError_t bwd_t(const GatedArgs& a) {
     const Cut c = cut(a.ws, a.B, a.L, a.D, true, a.blocks_in != nullptr);
     int64_t rows = a.B * tile_count(a.L, BWD_TOKENS);
     p.part = c.part;
-    if (c.blocks) {
+    if (c.blocks && a.B > 0) {  // an empty region of a given workspace has an address too
         GatedDev f = p;
         f.y = nullptr; f.h_out = nullptr; f.blocks = c.blocks;
         fwd_t<E>(a, f);

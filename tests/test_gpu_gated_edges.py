@@ -1,5 +1,7 @@
 """The gated recurrent layer's operators and the residual norm where their numbers are extreme, against the fp64 forms of
 gated_ref.py."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -11,7 +13,7 @@ from chunked_scan_amd import pipeline
 from gpu_util import note
 from test_gpu_gated import block_inputs, check_block, rng_of, scan_inputs, scan_kw, scan_ref
 from test_gpu_gated_layer import layer
-from test_gpu_mixer import BF, F32, Draw
+from test_gpu_mixer import BF, F32, SENTINEL, Draw
 
 pytestmark = pytest.mark.gpu
 
@@ -202,3 +204,31 @@ def test_layer_backward_after_the_generator_moved_on():
         grads.append(pipeline.gated_backward(p, saved, dy, dh, **backwards(F32)))
     for k, t in grads[0].items():
         assert (t is None) == (grads[1][k] is None) and (t is None or torch.equal(t, grads[1][k])), k
+
+
+# ------------------------------------------------------------------------------------ empty batches
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("L", [5, 100, 200])
+def test_empty_batch_with_a_workspace(L, dtype):
+    """No sequences, and a workspace that the caller has from other calls: the parameters' derivatives are zero."""
+    note(f"gated scan backward: empty batch {L} {dtype}")
+    D = 72
+    lam = torch.zeros(D, device="cuda")
+    sums = [torch.full((D,), SENTINEL, device="cuda") for _ in range(3)]
+    ws = torch.full((1 << 16,), 7, dtype=torch.uint8, device="cuda")
+    shp = la.GatedShape(0, L, D, 0 if dtype == F32 else 1, 8.0)
+    shp.stream = torch.cuda.current_stream().cuda_stream
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    none = ctypes.c_void_p(None)
+    lib = la.lib()
+    assert lib.la_gated_scan_workspace(ctypes.byref(shp), 1) == 0
+    st = lib.la_gated_scan(none, none, none, p(lam), none, none, none, none, none, none, none, none, p(ws), 1 << 16,
+                           ctypes.byref(shp))
+    assert st == 0
+    st = lib.la_gated_scan_bwd(none, none, none, p(lam), p(lam), p(lam), none, none, none, none, none, none, none, none, none,
+                               p(sums[0]), p(sums[1]), p(sums[2]), none, none, p(ws), 1 << 16, ctypes.byref(shp))
+    assert st == 0
+    torch.cuda.synchronize()
+    assert all((t == 0).all() for t in sums) and (ws == 7).all()
