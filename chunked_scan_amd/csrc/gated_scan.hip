@@ -141,7 +141,8 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 // passes between workgroups, so no fences.
 //
 // Results do not depend on scheduling: a state is always the left fold h_k+1 = A_k h_k + B_k from the sequence's start,
-// wherever a workgroup finds it done.
+// wherever a workgroup finds it done.  An infinite state, which token by token stays one, becomes NaN where A_k underflows: a
+// least A_k in its place would let states pass a complete decay.
 
 constexpr uint32_t EMPTY = ~0u;
 

@@ -623,8 +623,9 @@ int64_t la_gated_scan_workspace(const la_gated_shape* shape, int32_t backward);
  *   h_blocks: float[B, ceil(L / 64), D] or NULL: the state that enters every 64 tokens, for the backward pass; blocks
  *             behind a sequence's last token are left as they were.
  * No output may otherwise overlap another argument.  c softplus(lam) past fp32's largest value counts as that.  r = -infinity
- * holds the state (a = 1, no input).  A channel with
- * a NaN in x, r or i gives NaN from that token on.
+ * holds the state (a = 1, no input).  A channel with a NaN in x, r or i gives NaN from that token on; one with an infinite
+ * x or state gives infinity or NaN from there on, in y without z and in the states handed on (which of the two depends on
+ * where tiles end: a tile whose decays' product underflows takes an infinite state times zero).
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_DTYPE, LA_ERR_ALIAS, LA_ERR_UNSUPPORTED,
  * LA_ERR_WORKSPACE or LA_ERR_LAUNCH.
  */

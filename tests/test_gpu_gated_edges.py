@@ -232,3 +232,39 @@ def test_empty_batch_with_a_workspace(L, dtype):
     assert st == 0
     torch.cuda.synchronize()
     assert all((t == 0).all() for t in sums) and (ws == 7).all()
+
+
+# ------------------------------------------------------------------------------------ infinities
+
+
+@pytest.mark.parametrize("D", [64, 65])
+def test_infinity_stays_in_its_channel(D):
+    """An infinite x or state leaves its channel infinite or NaN from that token on, forward and in the states handed on;
+    what came before it and every other channel keeps its bits."""
+    note(f"gated scan: infinity {D}")
+    B, L = 2, 700
+    a, _ = scan_inputs((B, L, D, None, False, False, True, True, -1.0), F32, 81)
+    args, kw = lambda x: (x, a["r"], a["i"], a["lam"]), scan_kw(a, None)  # noqa: E731
+    y, h, _ = la.la_gated_scan(*args(a["x"]), **kw)
+    for where in ("x", "h_in"):
+        x, s = a["x"].clone(), a["h_in"].clone()
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        if where == "x":
+            x[1, 140, 33] = float("inf")
+            bad[1, 140:, 33] = True
+        else:
+            s[1, 33] = float("-inf")
+            bad[1, :, 33] = True
+        y2, h2, _ = la.la_gated_scan(*args(x), **dict(kw, h_in=s))
+        assert not torch.isfinite(y2[bad]).any() and torch.equal(y2[~bad], y[~bad])
+        assert not torch.isfinite(h2[1, 33]) and int((~torch.isfinite(h2)).sum()) == 1
+        got = la.la_gated_scan_bwd(*args(x), a["dy"], **dict(kw, h_in=s))
+        ref = la.la_gated_scan_bwd(*args(a["x"]), a["dy"], **kw)
+        for t, q in zip(got, ref):  # other channels, also in the sums over sequences
+            if t is not None:
+                keep = torch.arange(D, device="cuda") != 33
+                assert torch.equal(t[..., keep], q[..., keep])
+    state = a["h_in"].clone()
+    state[1, 33] = float("inf")
+    la.la_gated_step(a["x"][:, 0], a["r"][:, 0], a["i"][:, 0], a["lam"], state, r_bias=a["rb"], i_bias=a["ib"])
+    assert not torch.isfinite(state[1, 33]) and int((~torch.isfinite(state)).sum()) == 1
