@@ -1,5 +1,6 @@
-"""The gated recurrent layer's operators and the residual norm where their numbers are extreme, against the fp64 forms of
-gated_ref.py."""
+"""The gated recurrent layer's operators and the residual norm where their numbers are extreme (rows near the type's largest
+value, gates that are all but open, rates past fp32's range, infinities), on empty batches, and on the paths that only
+large batches take, against the fp64 forms of gated_ref.py."""
 import ctypes
 
 import numpy as np
@@ -11,7 +12,7 @@ import mixer_ref as R
 from chunked_scan_amd import binding as la
 from chunked_scan_amd import pipeline
 from gpu_util import note
-from test_gpu_gated import block_inputs, check_block, rng_of, scan_inputs, scan_kw, scan_ref
+from test_gpu_gated import block_inputs, check_block, check_grads, nonan, rng_of, scan_inputs, scan_kw, scan_ref
 from test_gpu_gated_layer import layer
 from test_gpu_mixer import BF, F32, SENTINEL, Draw
 
@@ -268,3 +269,65 @@ def test_infinity_stays_in_its_channel(D):
     state[1, 33] = float("inf")
     la.la_gated_step(a["x"][:, 0], a["r"][:, 0], a["i"][:, 0], a["lam"], state, r_bias=a["rb"], i_bias=a["ib"])
     assert not torch.isfinite(state[1, 33]) and int((~torch.isfinite(state)).sum()) == 1
+
+
+# ------------------------------------------------------------------------------------ large batches
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(3500, 96), (3500, 41), (1700, 1000), (900, 2047), (600, 4095), (600, 4096), (300, 8191), (300, 8192),
+                                 (300, 8200), (300, 16384), (300, 9001)])
+def test_block_of_more_rows_than_blocks(M, D, dtype):
+    """The backward's blocks walk several rows each (at most 768, 512 or 256 blocks by width), and the forward takes its forms
+    for many rows; the parameters' sums against the fp64 form."""
+    note(f"block norm of many rows {M} {D} {dtype}")
+    a = block_inputs(M, D, dtype, M + D)
+    check_block(a, "silu", 0.0, dtype, M, D)
+    check_block(a, "sigmoid", 0.3, dtype, M, D)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(600, 1024), (600, 5000), (600, 600)])
+def test_block_of_two_chunks_a_thread(M, D, dtype):
+    note(f"block norm, wide rows in many {M} {D} {dtype}")
+    a = block_inputs(M, D, dtype, M + D)
+    check_block(a, "silu", 0.3, dtype, M, D)
+
+
+def check_sums(got, ref, a):
+    """dlam, dr_bias and di_bias as sums of the fp64 form's own terms, bound by the terms' bounds and by the roundings of
+    the sum, which is no chain over all tokens: 16 of a lane's, 8 runs of a tile, 32 and 16 of 512 rows, and up to 17 behind
+    them, 100 in all; sigma / softplus 24 more."""
+    (dr, er), (di, ei) = ref[1:3]
+    co = R.sig(-(R.f64(a["r"]) + R.f64(a["rb"])))
+    with np.errstate(invalid="ignore"):
+        q, eq = np.nan_to_num(dr / co), np.nan_to_num(er / co)
+    lam = R.f64(a["lam"])
+    for t, v, e, k, by in ((got[3], q, eq, 124, R.sig(lam) / G.softplus(lam)), (got[4], dr, er, 100, 1.0), (got[5], di, ei, 100, 1.0)):
+        G.close(t, by * v.sum((0, 1)), by * (e.sum((0, 1)) + k * np.abs(v).sum((0, 1))), F32, "sums")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", [(3, 64 * 171 + 5, 5, None, False, False, True, True, -3.0),
+                                  (20, 64 * 60 + 9, 6, None, False, False, True, True, -3.0),
+                                  (700, 70, 8, [70, 0, 3, 64, 65] * 140, False, True, True, True, -3.0)], ids=lambda c: str(c[:3]))
+def test_scan_sums_of_many_partial_rows(case, dtype):
+    """More than 512 rows of partial sums (a row per sequence and 64 tokens: 516, 1220, 1400), so that they are added in
+    two steps; the last step's share is not a whole one."""
+    note(f"gated scan: many partial rows {case[:3]} {dtype}")
+    a, n = scan_inputs(case, dtype, 91)
+    got = la.la_gated_scan_bwd(*[a[k] for k in ("x", "r", "i", "lam", "dy")], dh_out=a["dh_out"], **scan_kw(a, case[3]))
+    ref = G.scan_bwd(*scan_ref(a, n, 8.0), nonan(a["dy"]), R.f64(a["dh_out"]))
+    check_grads(got, ref, dtype, n)
+    check_sums(got, ref, a)
+    # a few rows alone, at the ends of the first step's shares: none of them can be lost in the others' bounds
+    B, L = case[:2]
+    tiles = -(-L // 64)
+    last = B * tiles - 1
+    rows = [k for k in (0, 15, 16, 511, 512, 527, 528, 1023, 1024, last - 1, last) if k <= last]
+    mask = torch.zeros(B * tiles, dtype=torch.bool)
+    mask[rows] = True
+    mask = mask.view(B, tiles, 1).expand(B, tiles, 64).reshape(B, tiles * 64)[:, :L, None].cuda()
+    a["dy"] = torch.where(mask, a["dy"], torch.zeros_like(a["dy"]))
+    got = la.la_gated_scan_bwd(*[a[k] for k in ("x", "r", "i", "lam", "dy")], **scan_kw(a, case[3]))
+    check_sums(got, G.scan_bwd(*scan_ref(a, n, 8.0), nonan(a["dy"]), None), a)
