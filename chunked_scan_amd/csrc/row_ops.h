@@ -129,7 +129,9 @@ __device__ __forceinline__ RowScale row_rstd(const float (&h)[VPT][8], float ss,
             const float v = h[i][j] * S;
             s2 = fmaf(v, v, s2);
         }
-    return {inv_sqrt(fmaf(row_sum<TPR>(s2, buf), inv_d, eps * S * S)), S};
+    const float r = inv_sqrt(fmaf(row_sum<TPR>(s2, buf), inv_d, eps * S * S));
+    // rows below 2^100: their own reciprocal, far from the subnormal numbers, so that their smallest values need no scale
+    return r * S >= 0x1p-100f ? RowScale{r * S, 1.f} : RowScale{r, S};
 }
 
 // Whether rows `stride` elements apart all start on 16 bytes.
