@@ -8,8 +8,8 @@
 // element, so that the generator's 20 wide products cost 8 elements, not 4; the probability is a multiple of 2^-16 for it,
 // and the kept share in the scale is exact.
 //
-// Measured, bf16: norms, gate and scale over 16384 x 2048 66 us (335 MB, 5.1 TB/s, a copy's rate); their backward with dropout
-// over 8191 x 2048 53 + 6 us (268 MB); dropout with a residual of 16384 x 2048 33 us (201 MB, 6.0 TB/s, of which the last-level
+// Measured, bf16: norms, gate and scale over 16384 x 2048 63 to 68 us (335 MB, 5 TB/s, a copy's rate); their backward with
+// dropout over 8191 x 2048 53 + 6 us (268 MB; fp32 over 4096 x 2048 56 us, 4.8 TB/s); dropout with a residual of 16384 x 2048 33 us (201 MB, 6.0 TB/s, of which the last-level
 // cache holds a part).  A mask made by its counter costs no more than the loads hide.
 #include <algorithm>
 
@@ -316,10 +316,12 @@ __device__ __forceinline__ float rows_total(float v, float (*buf)[16], int& set)
 
 // Backward.  A block holds ROWS rows at a time and walks the rows grid-stride; each thread keeps its channels' share of the
 // three parameters' sums in registers, the block's rows add theirs up at the end (LDS, one after the other) and write one
-// row of `part`.  All of a row is loaded before its first sum, the next row's (2-byte types, one chunk a thread) before
-// this one's where its registers allow: a block waits for two sums over its rows, and with the loads behind them it left the memory idle
-// (8191 x 2048 bf16 with gate and dropout, 268 MB: 95.6 -> 59.6 us a pass, 4.5 TB/s).  Blocks of 4 waves, three of them a
-// CU within 168 registers: at four, whose 128 spill, 68.7 us, and blocks of 8 waves 73.
+// row of `part`.  All of a row is loaded before its first sum, the next row's before this one's where the registers allow
+// (2-byte types, one chunk a thread; unaligned rows up to 2048 channels): a block waits for two sums over its rows, and
+// with the loads behind them it left the memory idle (8191 x 2048 bf16 with gate and dropout, 268 MB: 95.6 -> 59.6 us a
+// pass, 4.5 TB/s).  Blocks of 4 waves, three of them a CU within 168 registers: at four, whose 128 spill, 68.7 us, and
+// blocks of 8 waves 73.  Over 8192 channels two chunks a thread do not fit the 128 registers of 16 waves: 125 to 213 spill
+// (unaligned 329 to 1127), and that bounds it: 4096 x 16384 bf16 444 us, 2.4 TB/s, fp32 905; 4096 x 9000 295 and 587.
 constexpr int bwd_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 template <typename E, int TPR, int VPT, bool VEC, bool DROP>
 __global__ __launch_bounds__(bwd_threads(TPR), TPR <= 256 || !VEC ? 3 : 4) void block_norm_bwd_kernel(BlockDev p) {
@@ -531,7 +533,8 @@ __global__ __launch_bounds__(256) void dropout_kernel(BlockDev p) {
 }
 
 // Blocks of the backward, so rows of partial sums: as many as 256 CUs hold at once (their registers allow three blocks of
-// 4 waves a CU, two of 8, one of 16).
+// 4 waves a CU; two of 8, of which aligned rows spill 6 to 16 registers for it, unaligned ones come in two rounds; one
+// of 16).
 int64_t bwd_rows(int64_t M, int64_t D) { return std::min<int64_t>(D <= 2048 ? 768 : D <= 4096 ? 512 : 256, M); }
 
 BlockDev dev(const BlockArgs& a) {

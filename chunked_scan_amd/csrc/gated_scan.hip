@@ -124,7 +124,7 @@ __device__ __forceinline__ float input_slope(float w, float a) {
 // sequence fills the card however few channels there are, and no tile waits for more than the tiles in flight before it.
 //
 // Measured, bf16 with gate (the clearing of the words among it): 1 x 16384 x 2048 forward 82 us, 335 MB at 4.1 TB/s, where
-// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 86 (302 MB; a copy 58 to 63).  What bounds it:
+// a large copy of as many bytes takes 70; 2 x 4096 x 2048 forward 48 and backward 88 (302 MB; a copy 58 to 63).  What bounds it:
 // 128 sequences of one tile, which neither clear nor wait, take 70 us, a copy's rate; sequences of two tiles 76, so clearing
 // and tickets cost 6, and the look-back over 128 tiles another 6.  Arithmetic is hidden but for 2 us (4 in the backward).  Why
 // this tile: 64 channels make a state word a lane in the wave that looks back; 32 and 64 tokens make more of them to fold
@@ -540,8 +540,10 @@ __global__ __launch_bounds__(WAVES * 64, sizeof(E) == 2 && VEC > 1 ? Cfg<false>:
     else fwd_tile<E, VEC, WAVES, TPT, false>(p, q, map_a, map_b);
 }
 
-// Backward, 64 tokens a tile since its rows and gates stay in registers: three waves a SIMD fit (132 registers; fp32 162, two
-// waves 83 us at 2 x 2048 x 2048, three 80); a fourth gains nothing (88 us with the input gates in LDS, as with three).  The same from the sequence's end: the
+// Backward, 64 tokens a tile since its rows and gates stay in registers: three waves a SIMD fit (132 registers; fp32 166, two
+// waves 83 us at 2 x 2048 x 2048, three 80); a fourth gains nothing (88 us with the input gates in LDS, as with three).
+// fp32 at 2 x 4096 x 2048 128 us, 604 MB at 4.7 TB/s; rows that are not aligned, one channel a lane and 16 tokens: 2 x 4000 x
+// 2047 bf16 162 us (2048 channels 86), fp32 215 (127).  The same from the sequence's end: the
 // carry c_t = a_t g_t runs c_t = a_t (s_t + c_{t+1}) and a tile maps the carry that enters it from behind to A c + R.  The
 // states h_{t-1} come from the forward's states at the tiles' starts.  Tiles behind a sequence's end write zeros.
 template <typename E, int VEC, int WAVES, int TPT, bool FULL>
@@ -825,8 +827,9 @@ __global__ __launch_bounds__(256) void gated_sums_kernel(const float* __restrict
     if (di_bias) di_bias[d] = s[2];
 }
 
-// One token: a row per wave and 64 VEC channels, all of its loads in flight before the first is used.  Latency or the host
-// bounds it: 1 x 2048 takes 2.4 us in a graph and 11 from Python.
+// One token: a row per wave and 64 VEC channels.  The slot and the earlier rows' slots come first, then the rows and the
+// state together, then the parameters, each bias behind its own branch: a chain of waits, which bounds it (1 x 2048 takes
+// 2.4 us in a graph and 11 from Python, 256 x 4096 6.7 in a graph, bf16 and fp32).
 template <typename E, int VEC>
 __global__ __launch_bounds__(64) void gated_step_kernel(GatedDev p) {
     const int64_t b = blockIdx.x / p.cb, d = ((int64_t)(blockIdx.x % p.cb) * 64 + threadIdx.x) * VEC;
